@@ -313,6 +313,130 @@ pkv_status pkv_paged_attn_decode_noalloc(const void *q, const void *k_cache, con
                                          int D, int64_t NB, int bs, float scale, void *out,
                                          int32_t *err_flag, void *stream);
 
+/*
+ * A cache with a budget: the calls below record how much attention every
+ * cached token receives and trim contexts to the tokens that receive most.
+ * (No counterpart in the pages, whose caches only grow; the formulas are
+ * given in full here.)
+ *
+ *   weights  device, fp32 [NB, Hkv, bs], 16-byte aligned: one value per cached
+ *            token and KV head, under the same block ids as the caches.
+ *
+ * With p[i, h, t] the softmax weight of cached token t for query i and query
+ * head h, a recording call adds, for every token t a query of the call sees
+ * and every KV head,
+ *     sum over the call's (recorded) queries i and the group's heads h of
+ *     p[i, h, t]
+ * to weights[block of t, kv head, offset of t].  For the tokens that are new
+ * in the call (the last context token of a decode step, the q_len new tokens
+ * of a prefill step) it is stored instead of added, so a slot's earlier
+ * content never needs clearing: every token's weight starts with the step that
+ * stores it.  A token stored by a step whose attention does not record has the
+ * weight its slot had before; set it where that matters.
+ *
+ * p is formed in fp32 from the fp32 scores and the row's fp32 log-sum-exp.
+ * Blocks shared by several sequences of a call receive every sequence's
+ * addition, in no fixed order (fp32 sums may differ in the last bits from run
+ * to run); without shared blocks the results are the same in every run.
+ * Tokens of blocks outside [0, NB) have no weight and receive none.  A query
+ * row whose scores contain a NaN or +inf adds NaN to the tokens it sees.
+ */
+
+/*
+ * pkv_paged_attn_decode_weights / _fp8 - pkv_paged_attn_decode (_fp8) that
+ * also records.
+ *
+ * Arguments, limits, flags and `out` as in the calls they extend (same
+ * kernels, same split; out agrees bit for bit), plus `weights` (above) and a
+ * larger workspace: pkv_decode_weights_workspace_bytes with the same sizes,
+ * for either cache type.  Beside the decode call's scratch it holds every
+ * score until its row's sum is known: 4 * Hq bytes per token of the B * MBS *
+ * bs the tables can name (134 MB for 512 sequences of 4096 tokens and 16
+ * query heads), of which a call touches the part that its contexts fill.
+ * A context of length 0 records nothing.  Three kernels on `stream`: decode,
+ * merge, and one that turns the scores into weights.
+ */
+size_t pkv_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas);
+
+pkv_status pkv_paged_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache,
+                                         const int32_t *block_tables, int MBS,
+                                         const int32_t *context_lens, int B, int Hq, int Hkv, int D,
+                                         int64_t NB, int bs, float scale, void *out, float *weights,
+                                         void *workspace, size_t workspace_bytes, int max_ctas,
+                                         int32_t *err_flag, void *stream);
+
+pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                             const int32_t *block_tables, int MBS,
+                                             const int32_t *context_lens, int B, int Hq, int Hkv,
+                                             int D, int64_t NB, int bs, float scale, float k_scale,
+                                             float v_scale, void *out, float *weights,
+                                             void *workspace, size_t workspace_bytes, int max_ctas,
+                                             int32_t *err_flag, void *stream);
+
+/*
+ * pkv_paged_prefill_weights - pkv_paged_prefill that also records.
+ *
+ * Arguments, limits, flags and `out` as in pkv_paged_prefill (bit for bit),
+ * plus
+ *   weights    above
+ *   window     0: every new token's queries are recorded; w >= 1: only those
+ *              of each sequence's last w new tokens (all, where it has fewer);
+ *              new tokens still have their weight set, to 0 where no recorded
+ *              query sees them
+ *   workspace  device scratch of pkv_prefill_weights_workspace_bytes(Tq, Hq)
+ *              bytes, 16-byte aligned (every row's log-sum-exp)
+ * Hkv <= 65535.  A sequence that the attention skips records nothing.
+ */
+size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq);
+
+pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const void *v_cache,
+                                     const int32_t *block_tables, int MBS,
+                                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B,
+                                     int64_t Tq, int max_seqlen_q, int Hq, int Hkv, int D, int64_t NB,
+                                     int bs, float scale, void *out, float *weights, int window,
+                                     void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                     void *stream);
+
+/*
+ * pkv_evict_kvcache - trim contexts to `budget` tokens.
+ *
+ * For every sequence b with n = context_lens[b] > budget, and each KV head on
+ * its own: the last `recent` tokens stay, and of the n - recent before them
+ * the budget - recent with the largest weights (equal weights: the lower
+ * position stays; NaN counts as larger than any number; -0 equals 0).  The
+ * tokens that stay move, in their order, to positions 0 .. budget - 1 of the
+ * sequence's blocks: K rows, V rows (bit for bit) and weights.  Slots past
+ * budget - 1 keep what they hold.  out_lens[b] = min(n, budget); the blocks
+ * past ceil(budget / bs) are then free for reuse (pkv_bm_evict).
+ *
+ * Attention over the trimmed context is attention over the tokens that
+ * stayed.  Cached keys are moved as they are, so a rotary position stays the
+ * one the token was stored with; the caller goes on counting positions from
+ * the untrimmed length.  Heads keep different tokens, so afterwards a
+ * position holds a different token for every KV head.
+ *
+ *   k_cache, v_cache  [NB, bs, Hkv, D] of elem_bytes = 2 (bf16) or 1 (E4M3),
+ *                     D in {64, 128}; updated in place
+ *   weights           above; updated in place
+ *   context_lens      int32 [B]; out_lens int32 [B], may be context_lens
+ *   budget >= 1, 0 <= recent <= budget; bs a multiple of 16; B, Hkv <= 65535
+ *   workspace         pkv_evict_workspace_bytes(B, Hkv, MBS, bs, budget) bytes,
+ *                     16-byte aligned: 4 bytes per kept token and KV head
+ * The blocks of a sequence that is trimmed must belong to it alone: a block
+ * named twice by the tables of a call (a shared prefix, a repeated entry) ends
+ * up with unspecified rows (pkv_bm_evict refuses shared blocks).  A sequence
+ * with a length outside [0, MBS * bs] or a needed table entry outside [0, NB)
+ * is left alone, sets PKV_FLAG_BAD_CONTEXT_LEN or PKV_FLAG_BAD_BLOCK, and has
+ * out_lens[b] = context_lens[b].
+ */
+size_t pkv_evict_workspace_bytes(int B, int Hkv, int MBS, int bs, int budget);
+
+pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
+                             const int32_t *block_tables, int MBS, const int32_t *context_lens,
+                             int B, int Hkv, int D, int elem_bytes, int64_t NB, int bs, int budget,
+                             int recent, int32_t *out_lens, void *workspace, size_t workspace_bytes,
+                             int32_t *err_flag, void *stream);
+
 /* Message describing the last non-OK status returned on this host thread. */
 const char *pkv_last_error(void);
 

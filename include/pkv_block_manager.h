@@ -79,6 +79,25 @@ pkv_status pkv_bm_append_batch(pkv_block_manager *bm, const int64_t *seq_ids,
 /* Release seq_id: every block loses one reference; free blocks at 0. */
 pkv_status pkv_bm_deallocate(pkv_block_manager *bm, int64_t seq_id);
 
+/*
+ * 1 if every block of seq_id belongs to it alone (no shared prefix), so that
+ * pkv_evict_kvcache may trim it in place; 0 otherwise or if it is unknown.
+ */
+int pkv_bm_can_evict(const pkv_block_manager *bm, int64_t seq_id);
+
+/*
+ * Trim seq_id to its budget, beside pkv_evict_kvcache with the same budget:
+ * if it holds more than `budget` tokens it holds `budget` afterwards, the
+ * blocks past ceil(budget / block_size) return to the pool (last first), and
+ * none of its blocks, now or later, is offered for prefix reuse (their rows are
+ * no longer a prefix of any prompt).  Otherwise nothing changes.  Fails with
+ * PKV_ERR_INVALID_ARG, changing nothing, if a block is shared.  Take the
+ * block tables for pkv_evict_kvcache before this call (pkv_bm_decode_batch);
+ * a block handed out again is safe to write by work enqueued on the same
+ * stream after the eviction.
+ */
+pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget);
+
 /* Free blocks in the pool. */
 int64_t pkv_bm_num_free_blocks(const pkv_block_manager *bm);
 

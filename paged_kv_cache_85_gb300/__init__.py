@@ -10,6 +10,14 @@ missing library is an error.
 
     store_kvcache(k, v, k_cache, v_cache, slot_mapping)
     paged_attn_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out)
+    paged_prefill(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, scale, out)
+
+and, for a cache with a budget, the same attention recording the weight every
+cached token received, and the eviction that goes by it:
+
+    paged_attn_decode_weights(..., out, weights)
+    paged_prefill_weights(..., out, weights, window=0)
+    evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget, recent, out_lens)
 
 Layouts: k, v ``[N, Hkv, D]``; caches ``[NB, bs, Hkv, D]``; q, out
 ``[B, Hq, D]`` (all bf16, contiguous, on one CUDA device); slot_mapping int64
@@ -31,6 +39,13 @@ __all__ = [
     "paged_prefill",
     "paged_attn_decode_fp8",
     "decode_workspace_bytes",
+    "paged_attn_decode_weights",
+    "paged_attn_decode_weights_fp8",
+    "paged_prefill_weights",
+    "evict_kvcache",
+    "decode_weights_workspace_bytes",
+    "prefill_weights_workspace_bytes",
+    "evict_workspace_bytes",
     "load_library",
     "library_path",
     "PkvError",
@@ -96,6 +111,24 @@ def load_library():
         lib.pkv_paged_prefill.restype = i32
         lib.pkv_paged_prefill.argtypes = [P, P, P, P, i32, P, P, i32, i64, i32, i32, i32, i32,
                                           i64, i32, f32, P, P, P]
+        lib.pkv_decode_weights_workspace_bytes.restype = sz
+        lib.pkv_decode_weights_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        lib.pkv_paged_attn_decode_weights.restype = i32
+        lib.pkv_paged_attn_decode_weights.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64,
+                                                      i32, f32, P, P, P, sz, i32, P, P]
+        lib.pkv_paged_attn_decode_weights_fp8.restype = i32
+        lib.pkv_paged_attn_decode_weights_fp8.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64,
+                                                          i32, f32, f32, f32, P, P, P, sz, i32, P, P]
+        lib.pkv_prefill_weights_workspace_bytes.restype = sz
+        lib.pkv_prefill_weights_workspace_bytes.argtypes = [i64, i32]
+        lib.pkv_paged_prefill_weights.restype = i32
+        lib.pkv_paged_prefill_weights.argtypes = [P, P, P, P, i32, P, P, i32, i64, i32, i32, i32, i32,
+                                                  i64, i32, f32, P, P, i32, P, sz, P, P]
+        lib.pkv_evict_workspace_bytes.restype = sz
+        lib.pkv_evict_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.pkv_evict_kvcache.restype = i32
+        lib.pkv_evict_kvcache.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64, i32, i32, i32,
+                                          P, P, sz, P, P]
         lib.pkv_last_error.restype = ctypes.c_char_p
         lib.pkv_last_error.argtypes = []
         lib.pkv_version.restype = i32
@@ -346,3 +379,204 @@ def paged_prefill(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k,
             int(max_seqlen_q), Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(),
             err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)))
     return out
+
+
+# ---------------------------------------------------------------- a cache with a budget
+
+
+def decode_weights_workspace_bytes(B, Hq, Hkv, D, MBS, bs, max_ctas=0) -> int:
+    """Workspace bytes paged_attn_decode_weights (and _fp8) needs for these sizes (0 when B == 0)."""
+    return int(load_library().pkv_decode_weights_workspace_bytes(B, Hq, Hkv, D, MBS, bs, max_ctas))
+
+
+def prefill_weights_workspace_bytes(Tq, Hq) -> int:
+    """Workspace bytes paged_prefill_weights needs."""
+    return int(load_library().pkv_prefill_weights_workspace_bytes(Tq, Hq))
+
+
+def evict_workspace_bytes(B, Hkv, MBS, bs, budget) -> int:
+    """Workspace bytes evict_kvcache needs."""
+    return int(load_library().pkv_evict_workspace_bytes(B, Hkv, MBS, bs, budget))
+
+
+def _scratch(workspace, nbytes, device):
+    """The caller's workspace, or one for this call alone: the caching allocator
+    hands it out on the current stream (inside a capture, from the graph's own
+    pool), so neither another call nor another graph shares it."""
+    import torch
+
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.device != device:
+        raise ValueError(f"workspace must be a CUDA tensor on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.is_cuda and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {first.device}")
+
+
+def _require_weights(weights, k_cache):
+    import torch
+
+    _require(weights, "weights", torch.float32, 3)
+    NB, bs, Hkv, _ = k_cache.shape
+    if tuple(weights.shape) != (NB, Hkv, bs):
+        raise ValueError(f"weights must be [NB, Hkv, bs] = {(NB, Hkv, bs)} for these caches; got "
+                         f"{tuple(weights.shape)}")
+
+
+def _decode_weights(name, fp8, q, k_cache, v_cache, block_tables, context_lens, scale, scales, out,
+                    weights, max_ctas, workspace, err_flag):
+    import torch
+
+    _require(q, "q", torch.bfloat16, 3)
+    if fp8:
+        _require_fp8_cache(k_cache, "k_cache")
+        _require_fp8_cache(v_cache, "v_cache")
+    else:
+        _require(k_cache, "k_cache", torch.bfloat16, 4)
+        _require(v_cache, "v_cache", torch.bfloat16, 4)
+    _require(block_tables, "block_tables", torch.int32, 2)
+    _require(context_lens, "context_lens", torch.int32, 1)
+    _require(out, "out", torch.bfloat16, 3, host_ok=True)
+    _require_weights(weights, k_cache)
+    if err_flag is not None:
+        _require(err_flag, "err_flag", torch.int32, 1)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, out=out, weights=weights, err_flag=err_flag)
+    B, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    if v_cache.shape != k_cache.shape or D2 != D or out.shape != q.shape:
+        raise ValueError(f"{name}: shapes do not match")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError(f"{name}: block_tables/context_lens batch != q batch")
+    MBS = max(block_tables.shape[1], 1)
+    lib = _lib or load_library()
+    idx = q.get_device()
+    with _on_device(idx):
+        ws = _scratch(workspace, int(lib.pkv_decode_weights_workspace_bytes(
+            B, Hq, Hkv, D, MBS, bs, max_ctas)), q.device)
+        args = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MBS,
+                context_lens.data_ptr(), B, Hq, Hkv, D, NB, bs, float(scale), *scales,
+                out.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                int(max_ctas), err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)]
+        _check((lib.pkv_paged_attn_decode_weights_fp8 if fp8 else lib.pkv_paged_attn_decode_weights)(*args))
+    return out
+
+
+def paged_attn_decode_weights(q, k_cache, v_cache, block_tables, context_lens, scale, out, weights,
+                              max_ctas=0, workspace=None, err_flag=None):
+    """``paged_attn_decode`` that also records the attention every cached token received.
+
+    ``weights`` is fp32 ``[NB, Hkv, bs]``, under the caches' block ids.  Every
+    token's softmax weight, summed over the query heads of its KV head's group,
+    is added to it; the step's newest token (the last of each context) has its
+    weight set rather than added to, so freshly stored slots need no clearing.
+    Writes ``out`` and returns it.
+    """
+    return _decode_weights("paged_attn_decode_weights", False, q, k_cache, v_cache, block_tables,
+                           context_lens, scale, (), out, weights, max_ctas, workspace, err_flag)
+
+
+def paged_attn_decode_weights_fp8(q, k_cache, v_cache, block_tables, context_lens, scale, k_scale,
+                                  v_scale, out, weights, max_ctas=0, workspace=None, err_flag=None):
+    """``paged_attn_decode_weights`` over FP8 (E4M3) caches."""
+    return _decode_weights("paged_attn_decode_weights_fp8", True, q, k_cache, v_cache, block_tables,
+                           context_lens, scale, (float(k_scale), float(v_scale)), out, weights,
+                           max_ctas, workspace, err_flag)
+
+
+def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                          scale, out, weights, window=0, workspace=None, err_flag=None):
+    """``paged_prefill`` that also records the attention every cached token received.
+
+    As in ``paged_attn_decode_weights``: prefix tokens have the weight added,
+    the step's new tokens have it set.  ``window`` > 0 records only the queries
+    of each sequence's last ``window`` new tokens; 0 records all of them.
+    Writes ``out`` and returns it.
+    """
+    import torch
+
+    _require(q, "q", torch.bfloat16, 3)
+    _require(k_cache, "k_cache", torch.bfloat16, 4)
+    _require(v_cache, "v_cache", torch.bfloat16, 4)
+    _require(block_tables, "block_tables", torch.int32, 2)
+    _require(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _require(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    _require(out, "out", torch.bfloat16, 3, host_ok=True)
+    _require_weights(weights, k_cache)
+    if err_flag is not None:
+        _require(err_flag, "err_flag", torch.int32, 1)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, out=out,
+                 cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, weights=weights,
+                 err_flag=err_flag)
+    Tq, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    if v_cache.shape != k_cache.shape or D2 != D or out.shape != q.shape:
+        raise ValueError("paged_prefill_weights: shapes do not match")
+    B = cu_seqlens_q.shape[0] - 1
+    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("paged_prefill_weights: cu_seqlens / block_tables batch sizes differ")
+    lib = _lib or load_library()
+    idx = q.get_device()
+    with _on_device(idx):
+        ws = _scratch(workspace, int(lib.pkv_prefill_weights_workspace_bytes(Tq, Hq)), q.device)
+        _check(lib.pkv_paged_prefill_weights(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            max(block_tables.shape[1], 1), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
+            int(max_seqlen_q), Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), weights.data_ptr(),
+            int(window), ws.data_ptr(), ws.numel() * ws.element_size(),
+            err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)))
+    return out
+
+
+def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget, recent, out_lens,
+                  workspace=None, err_flag=None):
+    """Trim every context longer than ``budget`` to ``budget`` tokens, in place.
+
+    Per KV head the last ``recent`` tokens stay and, of those before them, the
+    ``budget - recent`` with the largest ``weights`` (ties: the lower position).
+    They move in order to the front of the sequence's blocks, K, V (bf16 or
+    E4M3 caches) and weights; ``out_lens`` (may be ``context_lens``) receives
+    the new lengths and is returned.  A trimmed sequence's blocks must be its
+    own: ``BlockManager.evict`` checks that and gives the freed ones back.
+    """
+    import torch
+
+    fp8 = isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.bfloat16
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if fp8:
+            _require_fp8_cache(t, name)
+        else:
+            _require(t, name, torch.bfloat16, 4)
+    _require_weights(weights, k_cache)
+    _require(block_tables, "block_tables", torch.int32, 2)
+    _require(context_lens, "context_lens", torch.int32, 1)
+    _require(out_lens, "out_lens", torch.int32, 1)
+    if err_flag is not None:
+        _require(err_flag, "err_flag", torch.int32, 1)
+    _same_device(k_cache, v_cache=v_cache, weights=weights, block_tables=block_tables,
+                 context_lens=context_lens, out_lens=out_lens, err_flag=err_flag)
+    NB, bs, Hkv, D = k_cache.shape
+    B = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("evict_kvcache: cache shapes differ")
+    if block_tables.shape[0] != B or out_lens.shape[0] != B:
+        raise ValueError("evict_kvcache: block_tables/out_lens batch != context_lens batch")
+    MBS = max(block_tables.shape[1], 1)
+    lib = _lib or load_library()
+    idx = k_cache.get_device()
+    with _on_device(idx):
+        ws = _scratch(workspace, int(lib.pkv_evict_workspace_bytes(B, Hkv, MBS, bs, int(budget))),
+                      k_cache.device)
+        _check(lib.pkv_evict_kvcache(
+            k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(), MBS,
+            context_lens.data_ptr(), B, Hkv, D, k_cache.element_size(), NB, bs, int(budget),
+            int(recent), out_lens.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+            err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)))
+    return out_lens

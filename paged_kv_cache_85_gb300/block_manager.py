@@ -39,6 +39,10 @@ def _lib():
         lib.pkv_bm_append_batch.argtypes = [P, P, P, i32, P]
         lib.pkv_bm_deallocate.restype = i32
         lib.pkv_bm_deallocate.argtypes = [P, i64]
+        lib.pkv_bm_can_evict.restype = i32
+        lib.pkv_bm_can_evict.argtypes = [P, i64]
+        lib.pkv_bm_evict.restype = i32
+        lib.pkv_bm_evict.argtypes = [P, i64, i64]
         lib.pkv_bm_num_free_blocks.restype = i64
         lib.pkv_bm_num_free_blocks.argtypes = [P]
         lib.pkv_bm_seq_len.restype = i64
@@ -119,6 +123,16 @@ class BlockManager:
 
     def deallocate(self, seq_id: int):
         _check(self._lib, self._lib.pkv_bm_deallocate(self._h, seq_id))
+
+    def can_evict(self, seq_id: int) -> bool:
+        """Whether every block of the sequence is its own, so that it may be trimmed in place."""
+        return bool(self._lib.pkv_bm_can_evict(self._h, seq_id))
+
+    def evict(self, seq_id: int, budget: int):
+        """Trim the sequence to ``budget`` tokens (if it holds more) and give back the freed
+        blocks, beside ``evict_kvcache`` with the same budget; take that call's block tables
+        first.  Raises PkvError if a block is shared."""
+        _check(self._lib, self._lib.pkv_bm_evict(self._h, seq_id, int(budget)))
 
     @property
     def num_free_blocks(self) -> int:

@@ -13,6 +13,7 @@
 
 #include "pkv.h"
 #include "pkv_decode.cuh"
+#include "pkv_evict.h"
 #include "pkv_kernels.h"
 #include "pkv_prefill.h"
 #include "pkv_prefill_tc.cuh"
@@ -22,7 +23,11 @@ namespace pkv {
     cudaError_t launch_decode_d##D##_w##NW(int G, const CUtensorMap *tmk, const CUtensorMap *tmv, \
                                            const DecodeParams &p, int grid, size_t smem,          \
                                            cudaStream_t stream);                                  \
-    const void *decode_kernel_d##D##_w##NW(int G);
+    const void *decode_kernel_d##D##_w##NW(int G);                                                \
+    cudaError_t launch_decodew_d##D##_w##NW(int G, const CUtensorMap *tmk, const CUtensorMap *tmv, \
+                                            const DecodeParams &p, int grid, size_t smem,         \
+                                            cudaStream_t stream);                                 \
+    const void *decodew_kernel_d##D##_w##NW(int G);
 PKV_DECLARE_SHAPE(64, 4)
 PKV_DECLARE_SHAPE(64, 8)
 PKV_DECLARE_SHAPE(128, 4)
@@ -32,7 +37,11 @@ PKV_DECLARE_SHAPE(128, 8)
     cudaError_t launch_decode8_d##D##_w##NW(int G, int bt, const CUtensorMap *tmk,                \
                                             const CUtensorMap *tmv, const DecodeParams &p,        \
                                             int grid, size_t smem, cudaStream_t stream);          \
-    const void *decode_kernel8_d##D##_w##NW(int G, int bt);
+    const void *decode_kernel8_d##D##_w##NW(int G, int bt);                                       \
+    cudaError_t launch_decodew8_d##D##_w##NW(int G, int bt, const CUtensorMap *tmk,               \
+                                             const CUtensorMap *tmv, const DecodeParams &p,       \
+                                             int grid, size_t smem, cudaStream_t stream);         \
+    const void *decodew8_kernel_d##D##_w##NW(int G, int bt);
 PKV_DECLARE_SHAPE8(64, 4)
 PKV_DECLARE_SHAPE8(64, 8)
 PKV_DECLARE_SHAPE8(128, 4)
@@ -63,9 +72,20 @@ const void *prefill_kernel(int D, int G)
 size_t prefill_smem_bytes(int D) { return tc_smem_layout(D).total; }
 
 // bt: tokens per box (16, or 32 for FP8 caches with block sizes divisible by 32)
-const void *decode_kernel(int D, int NW, int G, bool f8, int bt)
+// weights: the kernels that also record every score for the attention weights
+const void *decode_kernel(int D, int NW, int G, bool f8, int bt, bool weights)
 {
     const bool pair = NW == kPairWorkers;
+    if (weights) {
+        if (f8) {
+            if (D == 128)
+                return pair ? decodew8_kernel_d128_w4(G, bt) : decodew8_kernel_d128_w8(G, bt);
+            return pair ? decodew8_kernel_d64_w4(G, bt) : decodew8_kernel_d64_w8(G, bt);
+        }
+        if (D == 128)
+            return pair ? decodew_kernel_d128_w4(G) : decodew_kernel_d128_w8(G);
+        return pair ? decodew_kernel_d64_w4(G) : decodew_kernel_d64_w8(G);
+    }
     if (f8) {
         if (D == 128)
             return pair ? decode_kernel8_d128_w4(G, bt) : decode_kernel8_d128_w8(G, bt);
@@ -81,6 +101,20 @@ cudaError_t launch_decode(int D, int NW, int G, bool f8, int bt, const CUtensorM
                           cudaStream_t stream)
 {
     const bool pair = NW == kPairWorkers;
+    if (p.ws_score) {
+        if (f8) {
+            if (D == 128)
+                return pair ? launch_decodew8_d128_w4(G, bt, tmk, tmv, p, grid, smem, stream)
+                            : launch_decodew8_d128_w8(G, bt, tmk, tmv, p, grid, smem, stream);
+            return pair ? launch_decodew8_d64_w4(G, bt, tmk, tmv, p, grid, smem, stream)
+                        : launch_decodew8_d64_w8(G, bt, tmk, tmv, p, grid, smem, stream);
+        }
+        if (D == 128)
+            return pair ? launch_decodew_d128_w4(G, tmk, tmv, p, grid, smem, stream)
+                        : launch_decodew_d128_w8(G, tmk, tmv, p, grid, smem, stream);
+        return pair ? launch_decodew_d64_w4(G, tmk, tmv, p, grid, smem, stream)
+                    : launch_decodew_d64_w8(G, tmk, tmv, p, grid, smem, stream);
+    }
     if (f8) {
         if (D == 128)
             return pair ? launch_decode8_d128_w4(G, bt, tmk, tmv, p, grid, smem, stream)
@@ -121,7 +155,7 @@ struct DeviceState {
     bool ready = false;
     int dev = 0;
     int sms = 0;
-    bool smem_set[2][2][2][2][9] = {};  // [fp8][32-token boxes][D == 128][NW == 8][G]
+    bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
     bool pf_smem_set[2][9] = {};     // prefill: [D == 128][G]
 };
 DeviceState g_dev[kMaxDevices];
@@ -170,7 +204,7 @@ struct OccEntry {
     size_t smem = 0;
     int occ = 0;
 };
-constexpr int kOccCache = 32;
+constexpr int kOccCache = 64;
 OccEntry g_occ[kMaxDevices][kOccCache];
 
 pkv_status occupancy(int dev, const void *fn, int threads, size_t smem, int *occ)
@@ -332,11 +366,13 @@ struct DecodePlan {
     int G = 0, NW = 0, stages = 0, grid = 0;
     int bt = pkv::kBox;  // tokens per box
     size_t smem = 0, hdr_bytes = 0, ws_bytes = 0;
+    // with weights: where the log-sum-exps, box descriptors and scores start
+    size_t lse_at = 0, box_at = 0, score_at = 0;
     const void *kernel = nullptr;
 };
 
 pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas,
-                       bool with_device, DecodePlan *plan, bool f8 = false)
+                       bool with_device, DecodePlan *plan, bool f8 = false, bool weights = false)
 {
     if (B < 1 || Hq < 1 || Hkv < 1 || MBS < 1 || bs < 1 || max_ctas < 0)
         return fail(PKV_ERR_INVALID_ARG,
@@ -419,6 +455,12 @@ pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_c
     plan->hdr_bytes = pkv::align_up((size_t)(pkv::kWsHeaderInts + B + 1) * 4, 256);
     plan->ws_bytes = plan->hdr_bytes +
                      (size_t)workers_cap * 2 * G * (size_t)(D + 4) * sizeof(float);
+    if (weights) {
+        plan->lse_at = pkv::align_up(plan->ws_bytes, 256);
+        plan->box_at = pkv::align_up(plan->lse_at + (size_t)B * Hq * sizeof(float), 256);
+        plan->score_at = pkv::align_up(plan->box_at + (size_t)box_max * sizeof(int4), 256);
+        plan->ws_bytes = plan->score_at + (size_t)box_max * G * pkv::kBox * sizeof(float);
+    }
     plan->grid = (int)grid_cap;
     if (!with_device)
         return PKV_OK;
@@ -426,10 +468,10 @@ pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_c
     pkv_status ps = device_state(&st);
     if (ps != PKV_OK)
         return ps;
-    const void *kfn = pkv::decode_kernel(D, NW, G, f8, bt);
+    const void *kfn = pkv::decode_kernel(D, NW, G, f8, bt, weights);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->smem_set[f8][bt != pkv::kBox][D == 128][NW == pkv::kWideWorkers][G];
+        bool &set = st->smem_set[weights][f8][bt != pkv::kBox][D == 128][NW == pkv::kWideWorkers][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kMaxDynSmem);
@@ -465,7 +507,7 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
                               int B, int Hq, int Hkv, int D, int64_t NB, int bs, float scale,
                               void *out, void *workspace, size_t workspace_bytes, int max_ctas,
                               int32_t *err_flag, void *stream, bool f8, float k_scale,
-                              float v_scale)
+                              float v_scale, bool record = false, float *weights = nullptr)
 {
     if (B < 0 || NB < 1)
         return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode: bad sizes B=%d NB=%lld", B, (long long)NB);
@@ -483,11 +525,13 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     if (f8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f ||
                v_scale <= 0.f))
         return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode_fp8: scales must be finite and > 0");
-    pkv_status ps = plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, true, &plan, f8);
+    pkv_status ps = plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, true, &plan, f8, record);
     if (ps != PKV_OK)
         return ps;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out)
         return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode: null pointer");
+    if (record && (!weights || !aligned16(weights)))
+        return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode_weights: weights null or misaligned");
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
         !aligned16(workspace) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
         (reinterpret_cast<uintptr_t>(context_lens) & 3u))
@@ -521,6 +565,12 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     p.stages = plan.stages;
     p.scale_log2 = scale * 1.4426950408889634f * (f8 ? k_scale : 1.f);
     p.v_scale = f8 ? v_scale : 1.f;
+    if (record) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_at);
+        p.ws_box = reinterpret_cast<int4 *>(ws + plan.box_at);
+        p.ws_score = reinterpret_cast<float *>(ws + plan.score_at);
+    }
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = pkv::launch_decode(D, plan.NW, plan.G, f8, plan.bt, &tmk, &tmv, p, plan.grid,
@@ -530,6 +580,15 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     e = pkv::launch_merge(D, plan.G, p, s);
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "merge launch: %s", cudaGetErrorString(e));
+    if (record) {
+        DeviceState *st = nullptr;
+        if ((ps = device_state(&st)) != PKV_OK)
+            return ps;
+        const long long boxes = (long long)B * Hkv * (((long long)MBS * bs + plan.bt - 1) / plan.bt);
+        e = pkv::launch_add_weights(plan.G, plan.bt, p, weights, boxes, st->sms, s);
+        if (e != cudaSuccess)
+            return fail(PKV_ERR_CUDA, "paged_attn_decode_weights launch: %s", cudaGetErrorString(e));
+    }
     return PKV_OK;
 }
 
@@ -614,11 +673,50 @@ pkv_status pkv_paged_attn_decode_fp8(const void *q, const void *k_cache, const v
                        k_scale, v_scale);
 }
 
-pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
-                             const int32_t *block_tables, int MBS, const int32_t *cu_seqlens_q,
-                             const int32_t *cu_seqlens_k, int B, int64_t Tq, int max_seqlen_q,
-                             int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
-                             int32_t *err_flag, void *stream)
+size_t pkv_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas)
+{
+    DecodePlan plan;
+    if (B == 0 || plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, false, &plan, false, true) != PKV_OK)
+        return 0;
+    return plan.ws_bytes;
+}
+
+pkv_status pkv_paged_attn_decode_weights(const void *q, const void *k_cache, const void *v_cache,
+                                         const int32_t *block_tables, int MBS,
+                                         const int32_t *context_lens, int B, int Hq, int Hkv, int D,
+                                         int64_t NB, int bs, float scale, void *out, float *weights,
+                                         void *workspace, size_t workspace_bytes, int max_ctas,
+                                         int32_t *err_flag, void *stream)
+{
+    return decode_impl(q, k_cache, v_cache, block_tables, MBS, context_lens, B, Hq, Hkv, D, NB, bs,
+                       scale, out, workspace, workspace_bytes, max_ctas, err_flag, stream, false,
+                       1.f, 1.f, true, weights);
+}
+
+pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                             const int32_t *block_tables, int MBS,
+                                             const int32_t *context_lens, int B, int Hq, int Hkv,
+                                             int D, int64_t NB, int bs, float scale, float k_scale,
+                                             float v_scale, void *out, float *weights,
+                                             void *workspace, size_t workspace_bytes, int max_ctas,
+                                             int32_t *err_flag, void *stream)
+{
+    return decode_impl(q, k_cache, v_cache, block_tables, MBS, context_lens, B, Hq, Hkv, D, NB, bs,
+                       scale, out, workspace, workspace_bytes, max_ctas, err_flag, stream, true,
+                       k_scale, v_scale, true, weights);
+}
+
+} // extern "C"
+
+// record: also leave every row's log-sum-exp in the workspace and add the
+// attention weights (pkv_paged_prefill_weights)
+static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, int MBS, const int32_t *cu_seqlens_q,
+                               const int32_t *cu_seqlens_k, int B, int64_t Tq, int max_seqlen_q,
+                               int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
+                               int32_t *err_flag, void *stream, bool record = false,
+                               float *weights = nullptr, int window = 0, void *workspace = nullptr,
+                               size_t workspace_bytes = 0)
 {
     if (B < 0 || Tq < 0 || max_seqlen_q < 0 || NB < 1 || MBS < 1 || bs < 1 || Hq < 1 || Hkv < 1)
         return fail(PKV_ERR_INVALID_ARG, "paged_prefill: bad sizes B=%d Tq=%lld max_seqlen_q=%d "
@@ -639,6 +737,10 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
         return fail(PKV_ERR_INVALID_ARG, "paged_prefill: NB*bs and MBS*bs must be < 2^31");
     if (Tq >= 0x7fffffffLL || B > 65535)
         return fail(PKV_ERR_UNSUPPORTED, "paged_prefill: Tq must be < 2^31 and B <= 65535");
+    if (record && window < 0)
+        return fail(PKV_ERR_INVALID_ARG, "paged_prefill_weights: window=%d is negative", window);
+    if (record && Hkv > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "paged_prefill_weights: Hkv must be <= 65535");
     if (B == 0 || Tq == 0 || max_seqlen_q == 0)
         return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !cu_seqlens_k || !out)
@@ -648,6 +750,14 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
         (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3u))
         return fail(PKV_ERR_INVALID_ARG, "paged_prefill: misaligned pointer");
+    if (record) {
+        if (!weights || !aligned16(weights))
+            return fail(PKV_ERR_INVALID_ARG, "paged_prefill_weights: weights null or misaligned");
+        const size_t need = pkv_prefill_weights_workspace_bytes(Tq, Hq);
+        if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+            return fail(PKV_ERR_WORKSPACE, "paged_prefill_weights: workspace needs %zu bytes "
+                        "(16-byte aligned), got %zu", need, workspace ? workspace_bytes : (size_t)0);
+    }
     // work items: pairs of adjacent 128-row query tiles of one sequence and KV head
     const long long pairs =
         ((long long)max_seqlen_q * G + 2 * pkv::kPrefillRows - 1) / (2 * pkv::kPrefillRows);
@@ -703,6 +813,8 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
     p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
     p.neg_scale = scale < 0.f;
     p.tile_copies = tile_copies ? 1 : 0;
+    if (record)
+        p.lse = static_cast<float *>(workspace);
     // Persistent grid: one CTA per SM (each holds all of the SM's TMEM
     // columns, and asks for more than half of its shared memory so that no
     // second CTA lands beside it), each walking its share of the work items.
@@ -716,6 +828,128 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
                                         smem, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_prefill launch: %s", cudaGetErrorString(e));
+    if (record) {
+        e = pkv::launch_prompt_weights(D, p, k_cache, weights, window, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return fail(PKV_ERR_CUDA, "paged_prefill_weights launch: %s", cudaGetErrorString(e));
+    }
+    return PKV_OK;
+}
+
+extern "C" {
+
+pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, int MBS, const int32_t *cu_seqlens_q,
+                             const int32_t *cu_seqlens_k, int B, int64_t Tq, int max_seqlen_q,
+                             int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
+                             int32_t *err_flag, void *stream)
+{
+    return prefill_impl(q, k_cache, v_cache, block_tables, MBS, cu_seqlens_q, cu_seqlens_k, B, Tq,
+                        max_seqlen_q, Hq, Hkv, D, NB, bs, scale, out, err_flag, stream);
+}
+
+size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq)
+{
+    return Tq < 1 || Hq < 1 ? 0 : pkv::align_up((size_t)Tq * Hq * sizeof(float), 256);
+}
+
+pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const void *v_cache,
+                                     const int32_t *block_tables, int MBS,
+                                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B,
+                                     int64_t Tq, int max_seqlen_q, int Hq, int Hkv, int D, int64_t NB,
+                                     int bs, float scale, void *out, float *weights, int window,
+                                     void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                     void *stream)
+{
+    return prefill_impl(q, k_cache, v_cache, block_tables, MBS, cu_seqlens_q, cu_seqlens_k, B, Tq,
+                        max_seqlen_q, Hq, Hkv, D, NB, bs, scale, out, err_flag, stream, true, weights,
+                        window, workspace, workspace_bytes);
+}
+
+size_t pkv_evict_workspace_bytes(int B, int Hkv, int MBS, int bs, int budget)
+{
+    if (B < 1 || Hkv < 1 || MBS < 1 || bs < 1 || budget < 1)
+        return 0;
+    const long long ctx = (long long)MBS * bs;
+    const size_t keep = (size_t)(budget < ctx ? budget : ctx);
+    return pkv::align_up((size_t)B * Hkv * sizeof(int2), 256) +
+           pkv::align_up((size_t)B * keep * sizeof(int32_t), 256) +
+           (size_t)B * Hkv * keep * sizeof(int32_t);
+}
+
+pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
+                             const int32_t *block_tables, int MBS, const int32_t *context_lens,
+                             int B, int Hkv, int D, int elem_bytes, int64_t NB, int bs, int budget,
+                             int recent, int32_t *out_lens, void *workspace, size_t workspace_bytes,
+                             int32_t *err_flag, void *stream)
+{
+    if (B < 0 || Hkv < 1 || MBS < 1 || bs < 1 || NB < 1)
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: bad sizes B=%d Hkv=%d MBS=%d bs=%d NB=%lld", B,
+                    Hkv, MBS, bs, (long long)NB);
+    if (budget < 1 || recent < 0 || recent > budget)
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: need budget >= 1 and 0 <= recent <= budget, "
+                    "got budget=%d recent=%d", budget, recent);
+    if (D != 64 && D != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "evict_kvcache: head_dim %d not in {64,128}", D);
+    if (elem_bytes != 1 && elem_bytes != 2)
+        return fail(PKV_ERR_UNSUPPORTED, "evict_kvcache: %d bytes per element not in {1,2}", elem_bytes);
+    if (bs % pkv::kBox != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "evict_kvcache: block_size %d not a multiple of 16", bs);
+    if ((long long)NB * bs >= 0x7fffffffLL || (long long)MBS * bs >= 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: NB*bs and MBS*bs must be < 2^31");
+    if (B > 65535 || Hkv > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "evict_kvcache: B and Hkv must be <= 65535");
+    if (B == 0)
+        return PKV_OK;
+    if (!k_cache || !v_cache || !weights || !block_tables || !context_lens || !out_lens)
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: null pointer");
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+        (reinterpret_cast<uintptr_t>(context_lens) & 3u) || (reinterpret_cast<uintptr_t>(out_lens) & 3u))
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: misaligned pointer");
+    const size_t need = pkv_evict_workspace_bytes(B, Hkv, MBS, bs, budget);
+    if (!workspace || workspace_bytes < need)
+        return fail(PKV_ERR_WORKSPACE, "evict_kvcache: workspace needs %zu bytes, got %zu", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    DeviceState *st = nullptr;
+    pkv_status ps = device_state(&st);
+    if (ps != PKV_OK)
+        return ps;
+    pkv::EvictParams p;
+    p.k_cache = static_cast<uint4 *>(k_cache);
+    p.v_cache = static_cast<uint4 *>(v_cache);
+    p.weights = weights;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.out_lens = out_lens;
+    p.err_flag = err_flag;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.MBS = MBS;
+    p.bs = bs;
+    p.NB = (int)NB;
+    p.units = D * elem_bytes / 16;
+    p.budget = budget;
+    p.recent = recent;
+    const long long ctx = (long long)MBS * bs;
+    p.keep = (int)(budget < ctx ? budget : ctx);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_moved = reinterpret_cast<int2 *>(ws);
+    ws += pkv::align_up((size_t)B * Hkv * sizeof(int2), 256);
+    p.ws_dst = reinterpret_cast<int32_t *>(ws);
+    ws += pkv::align_up((size_t)B * p.keep * sizeof(int32_t), 256);
+    p.ws_src = reinterpret_cast<int32_t *>(ws);
+    // whole rows per CTA where the (sequence, KV head) pairs fill the GPU, else
+    // slices of them, down to one 32-byte sector
+    p.slices = 1;
+    while (p.slices < p.units && (long long)p.slices * B * Hkv < 4LL * st->sms)
+        p.slices *= 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = pkv::launch_evict_select(p, s);
+    if (e == cudaSuccess)
+        e = pkv::launch_evict_move(p, s);
+    if (e != cudaSuccess)
+        return fail(PKV_ERR_CUDA, "evict_kvcache launch: %s", cudaGetErrorString(e));
     return PKV_OK;
 }
 

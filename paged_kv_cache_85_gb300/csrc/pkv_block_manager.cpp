@@ -39,6 +39,7 @@ struct Block {
 struct Sequence {
     std::vector<int32_t> tokens;
     std::vector<int32_t> table;     // block ids, logical order
+    bool trimmed = false;           // its blocks no longer hold its tokens in order: never hashed
 };
 
 // FIFO pool of free block ids as a doubly linked list threaded through
@@ -140,6 +141,17 @@ struct pkv_block_manager {
         blk.hash = chain_hash(prefix_hash, tokens, block_size);
         blk.tokens.assign(tokens, tokens + block_size);
         hash_to_block[blk.hash] = id;
+    }
+
+    // Drop a block's content hash: its rows are about to change.
+    void forget(int32_t id)
+    {
+        Block &blk = blocks[id];
+        auto it = hash_to_block.find(blk.hash);
+        if (blk.hash != kNoHash && it != hash_to_block.end() && it->second == id)
+            hash_to_block.erase(it);
+        blk.hash = kNoHash;
+        blk.tokens.clear();
     }
 
     uint64_t prefix_hash_before(const Sequence &s, size_t block_index) const
@@ -274,7 +286,7 @@ pkv_status pkv_bm_append(pkv_block_manager *bm, int64_t seq_id, int32_t token, i
     s.tokens.push_back(token);
     if (n % bs == 1 || bs == 1)
         s.table.push_back(bm->take_front());
-    if (n % bs == 0) {  // the last block just filled: hash and register it
+    if (n % bs == 0 && !s.trimmed) {  // the last block just filled: hash and register it
         const size_t last = s.table.size() - 1;
         bm->seal(s.table[last], bm->prefix_hash_before(s, last), s.tokens.data() + (n - bs));
     }
@@ -318,6 +330,41 @@ pkv_status pkv_bm_deallocate(pkv_block_manager *bm, int64_t seq_id)
     for (auto b = t.rbegin(); b != t.rend(); ++b)
         bm->release(*b);
     bm->seqs.erase(it);
+    return PKV_OK;
+}
+
+int pkv_bm_can_evict(const pkv_block_manager *bm, int64_t seq_id)
+{
+    const Sequence *s = bm ? find_seq(bm, seq_id) : nullptr;
+    if (!s)
+        return 0;
+    for (const int32_t id : s->table)
+        if (bm->blocks[id].ref_count != 1)
+            return 0;
+    return 1;
+}
+
+pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget)
+{
+    if (!bm || budget < 1)
+        return err(PKV_ERR_INVALID_ARG, "bm_evict: null manager or budget < 1");
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end())
+        return err(PKV_ERR_INVALID_ARG, "bm_evict: unknown sequence id");
+    Sequence &s = it->second;
+    if ((int64_t)s.tokens.size() <= budget)
+        return PKV_OK;
+    if (!pkv_bm_can_evict(bm, seq_id))
+        return err(PKV_ERR_INVALID_ARG, "bm_evict: the sequence shares blocks with another one");
+    for (const int32_t id : s.table)
+        bm->forget(id);
+    const size_t blocks = (size_t)((budget + bm->block_size - 1) / bm->block_size);
+    while (s.table.size() > blocks) {
+        bm->release(s.table.back());
+        s.table.pop_back();
+    }
+    s.tokens.resize((size_t)budget);
+    s.trimmed = true;
     return PKV_OK;
 }
 

@@ -40,6 +40,11 @@
 //    piece is the whole stream) or a partial (acc, max, sum) into one of its
 //    two workspace slots (first / last piece of its slice); a second kernel
 //    merges the partials of streams that straddle workers by log-sum-exp.
+//  * With WT (the calls that record attention weights) every box's scores
+//    (log2 domain) go to the workspace as [G][BT] floats with a descriptor of
+//    the box, and every finished (sequence, query head) leaves its log-sum-exp;
+//    pkv_weights.cu turns them into weights once all of those are known.  The
+//    scores are 4 G bytes per token and KV head beside 4 D (bf16) of K and V.
 //  * Masking selects out tokens at or past context_len (scores -> -inf and
 //    the P.V loop stops at the last valid token), so whatever the unused
 //    slots of the last block hold (even NaN) never reaches the output.
@@ -57,7 +62,7 @@ constexpr int kLookahead = 4;  // boxes per worker whose block ids are loaded ah
 // Per-worker box descriptor of a stage, written by the producer.
 struct __align__(16) BoxMeta {
     int b, h, tok0, nvalid;
-    int flags, blk, pad0, pad1;
+    int flags, blk, off, box;  // off: tok0's offset in the block; box: position in the streams
 };
 constexpr int kBoxValid = 1;     // the worker has a box in this stage
 constexpr int kBoxLoaded = 2;    // its K/V were copied (the block id was valid)
@@ -160,7 +165,7 @@ __device__ __forceinline__ int box_block(const DecodeParams &p, int b, int j)
 // register queue, so a copy never waits on a block-table read.  Per stage
 // every lane writes its worker's box descriptor and issues its own TMA
 // copies; lane 0 arms the stage's mbarrier with the summed byte count.
-template <int D, int G, int NW, bool F8, int BT>
+template <int D, int G, int NW, bool F8, int BT, bool WT>
 __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CUtensorMap *tmv,
                                                 const DecodeParams &p, uint8_t *smem,
                                                 const DecodeSmem &L, int lane, int R, int Tr,
@@ -253,6 +258,10 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
             m.nvalid = min(BT, len[b] - tok0);
             m.flags = flags;
             m.blk = blk;
+            if constexpr (WT) {
+                m.off = tok0 % p.bs;
+                m.box = pos;
+            }
             // advance both cursors
             next_box(pb, p.B, cb, ch, cj);
             ++pos;
@@ -313,6 +322,22 @@ __device__ __forceinline__ uint32_t box_chunk(int t, int c)
     return (uint32_t)((c >> 3) * kHalfBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
+// Descriptor of a box for the weights kernel (lane 0 of its worker).
+template <int BT>
+__device__ __forceinline__ void record_box(const DecodeParams &p, const BoxMeta &bm)
+{
+    const bool newest = (bm.flags & kStreamLast) != 0;  // its last valid token is the step's new one
+    p.ws_box[bm.box] = make_int4(bm.b, (bm.flags & kBoxLoaded) ? bm.blk : -1, bm.off,
+                                 bm.nvalid | (newest ? kBoxNewest : 0));
+}
+
+// Log-sum-exp (log2 units) of a row with running max m and sum l; +inf where
+// no key could be read, so that 2^(s - lse) is 0.
+__device__ __forceinline__ float row_lse(float m, float l)
+{
+    return l == 0.f ? INFINITY : m + log2f(l);
+}
+
 // Consumer warp (worker).  Per 16-token box, on the tensor cores
 // (mma.sync m16n8k16, bf16 in, fp32 accumulate), with the G query heads as
 // the M rows (zero-padded to 16):
@@ -321,7 +346,7 @@ __device__ __forceinline__ uint32_t box_chunk(int t, int c)
 //   O[G x D] += P . V             P split into bf16 hi + lo parts (2 MMAs per
 //                                 n-tile) so P keeps ~16 mantissa bits; V
 //                                 fragments by ldmatrix.trans
-template <int D, int G, int NW>
+template <int D, int G, int NW, bool WT>
 __device__ __forceinline__ void decode_consumer(const DecodeParams &p, uint8_t *smem,
                                                 const DecodeSmem &L, int warp, int lane)
 {
@@ -416,6 +441,13 @@ __device__ __forceinline__ void decode_consumer(const DecodeParams &p, uint8_t *
                 const int t = tq + (i & 1) + ((i >> 1) << 3);
                 sv[i] = t < nvw ? sv[i] * p.scale_log2 : -INFINITY;
             }
+            if constexpr (WT) {
+                if (real) {
+                    float *sp = p.ws_score + ((size_t)bm.box * G + hrow) * kBox + tq;
+                    *reinterpret_cast<float2 *>(sp) = make_float2(sv[0], sv[1]);
+                    *reinterpret_cast<float2 *>(sp + 8) = make_float2(sv[2], sv[3]);
+                }
+            }
             float mt = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
             mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 1));
             mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 2));
@@ -453,6 +485,10 @@ __device__ __forceinline__ void decode_consumer(const DecodeParams &p, uint8_t *
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&empty[stage]);
+        if constexpr (WT) {
+            if (lane == 0 && (bm.flags & kBoxValid))
+                record_box<kBox>(p, bm);
+        }
 
         if (bm.flags & kPieceLast) {
             // ---- finish this worker's piece of the stream ----
@@ -462,6 +498,10 @@ __device__ __forceinline__ void decode_consumer(const DecodeParams &p, uint8_t *
             if (real) {
                 const size_t hq = (size_t)bm.b * p.Hq + (size_t)bm.h * G + hrow;
                 if (complete) {
+                    if constexpr (WT) {
+                        if (quad == 0)
+                            p.ws_lse[hq] = row_lse(m_run, l_tot);
+                    }
                     uint16_t *orow = p.out + hq * D + 2 * quad;
 #pragma unroll
                     for (int n = 0; n < NT; n++)
@@ -520,7 +560,7 @@ template <int D> __device__ __forceinline__ uint32_t box8_chunk(int t, int c)
 //     max exceeds it by more than 2^8, which bounds P by 256 (exact range of
 //     f16) and skips the rescale on most boxes.
 // k_scale is folded into the score scale and v_scale into the output.
-template <int D, int G, int NW, int BT>
+template <int D, int G, int NW, int BT, bool WT>
 __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8_t *smem,
                                                     const DecodeSmem &L, int warp, int lane)
 {
@@ -720,6 +760,17 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                     if (g >= nv) { sv[u][0] = -INFINITY; sv[u][1] = -INFINITY; }
                     if (g + 8 >= nv) { sv[u][2] = -INFINITY; sv[u][3] = -INFINITY; }
                 }
+                if constexpr (WT) {
+                    float *sp = p.ws_score + ((size_t)bm.box * G + h0) * BT + 16 * u + g;
+                    if (h0 < G) {
+                        sp[0] = sv[u][0];
+                        sp[8] = sv[u][2];
+                    }
+                    if (h1 < G) {
+                        sp[BT] = sv[u][1];
+                        sp[BT + 8] = sv[u][3];
+                    }
+                }
             }
             // ---- online softmax per head column (log2 domain) ----
             float b0 = fmaxf(sv[0][0], sv[0][2]), b1 = fmaxf(sv[0][1], sv[0][3]);
@@ -780,6 +831,10 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
         }
         if (!released)
             release();
+        if constexpr (WT) {
+            if (lane == 0 && (bm.flags & kBoxValid))
+                record_box<BT>(p, bm);
+        }
 
         if (bm.flags & kPieceLast) {
             float t0 = l0, t1 = l1;
@@ -799,6 +854,10 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 const float lt = hh == 0 ? t0 : t1;
                 const float mr = hh == 0 ? m0 : m1;
                 if (complete) {
+                    if constexpr (WT) {
+                        if (g == 0)
+                            p.ws_lse[hq0 + head] = row_lse(mr, lt);
+                    }
                     const float f = lt > 0.f ? p.v_scale / lt : 0.f;
                     uint16_t *dst = p.out + (hq0 + head) * D + g * (D / 8);
 #pragma unroll
@@ -891,7 +950,7 @@ __device__ __forceinline__ void build_prefix(const DecodeParams &p, int *pb, int
 
 // BT: tokens per box (16; 32 for FP8 caches whose block size is a multiple
 // of 32, which halves the per-box work of the producer and the consumers).
-template <int D, int G, int NW, bool F8, int BT>
+template <int D, int G, int NW, bool F8, int BT, bool WT>
 __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 2) : 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const DecodeParams p)
@@ -930,7 +989,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
     const int P = Tr > 0 ? (Tr + Wr - 1) / Wr : 1;
 
     if (warp == NW) {
-        decode_producer<D, G, NW, F8, BT>(&tmk, &tmv, p, smem, L, lane, R, Tr, Wr, P);
+        decode_producer<D, G, NW, F8, BT, WT>(&tmk, &tmv, p, smem, L, lane, R, Tr, Wr, P);
     } else {
         if (blockIdx.x == 0) {
             // Publish the box layout for the merge kernel (after the previous
@@ -947,13 +1006,13 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
             }
         }
         if constexpr (F8)
-            decode_consumer_fp8<D, G, NW, BT>(p, smem, L, warp, lane);
+            decode_consumer_fp8<D, G, NW, BT, WT>(p, smem, L, warp, lane);
         else
-            decode_consumer<D, G, NW>(p, smem, L, warp, lane);
+            decode_consumer<D, G, NW, WT>(p, smem, L, warp, lane);
     }
 }
 
-template <int D, int NW, bool F8, int BT = kBox>
+template <int D, int NW, bool F8, int BT = kBox, bool WT = false>
 inline cudaError_t launch_decode_shape(int G, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                        const DecodeParams &p, int grid, size_t smem,
                                        cudaStream_t stream)
@@ -969,21 +1028,22 @@ inline cudaError_t launch_decode_shape(int G, const CUtensorMap *tmk, const CUte
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (G) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 1, NW, F8, BT>, *tmk, *tmv, p);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 2, NW, F8, BT>, *tmk, *tmv, p);
-    case 4: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 4, NW, F8, BT>, *tmk, *tmv, p);
-    case 8: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 8, NW, F8, BT>, *tmk, *tmv, p);
+    case 1: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 1, NW, F8, BT, WT>, *tmk, *tmv, p);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 2, NW, F8, BT, WT>, *tmk, *tmv, p);
+    case 4: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 4, NW, F8, BT, WT>, *tmk, *tmv, p);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 8, NW, F8, BT, WT>, *tmk, *tmv, p);
     default: return cudaErrorInvalidValue;
     }
 }
 
-template <int D, int NW, bool F8, int BT = kBox> inline const void *decode_kernel_shape(int G)
+template <int D, int NW, bool F8, int BT = kBox, bool WT = false>
+inline const void *decode_kernel_shape(int G)
 {
     switch (G) {
-    case 1: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 1, NW, F8, BT>);
-    case 2: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 2, NW, F8, BT>);
-    case 4: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 4, NW, F8, BT>);
-    case 8: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 8, NW, F8, BT>);
+    case 1: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 1, NW, F8, BT, WT>);
+    case 2: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 2, NW, F8, BT, WT>);
+    case 4: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 4, NW, F8, BT, WT>);
+    case 8: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 8, NW, F8, BT, WT>);
     default: return nullptr;
     }
 }

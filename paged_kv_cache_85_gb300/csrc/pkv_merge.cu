@@ -14,6 +14,9 @@
 //     M = max_i m_i,  out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
 // Sequences with context length 0 get zeros here.
 //
+// For the calls that record attention weights the row's log-sum-exp,
+// M + log2(sum_i 2^(m_i - M) l_i), is left in the workspace as well.
+//
 // One warp per (sequence, query head); each lane owns D/32 output columns.
 #include <cuda_bf16.h>
 
@@ -107,6 +110,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_pieces_kernel(const De
             }
         }
         const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+        if (p.ws_lse && lane == 0)
+            p.ws_lse[row] = Ls == 0.f ? INFINITY : M + log2f(Ls);
 #pragma unroll
         for (int c = 0; c < DPL; c++)
             o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[c] * inv));
@@ -123,6 +128,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_pieces_kernel(const De
 #pragma unroll
         for (int i = 0; i < DPL; i++)
             o[i] = 0;
+        if (p.ws_lse && lane == 0)
+            p.ws_lse[row] = INFINITY;
         return;
     }
     float Ls = 0.f;
@@ -131,6 +138,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_pieces_kernel(const De
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
+
+    if (p.ws_lse && lane == 0)
+        p.ws_lse[row] = M + log2f(Ls);
 
     // Weighted sum of the partial outputs; 8 pieces' loads in flight at once.
     float acc[DPL];

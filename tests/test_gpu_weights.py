@@ -1,0 +1,356 @@
+"""Attention that records the weight every cached token received, and the
+eviction by it, against plain 64-bit forms (budget_reference.py)."""
+
+import numpy as np
+import pytest
+
+import budget_reference as ref
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+FLAG_BAD_BLOCK, FLAG_BAD_CONTEXT_LEN = 0x2, 0x4
+
+
+@pytest.fixture(scope="module")
+def pkv(cuda_lib_path):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_kv_cache_85_gb300 as m
+
+    m.load_library()
+    return m
+
+
+def bf(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).cuda()
+
+
+def dev_cache(x):
+    return bf(x) if x.dtype == np.uint16 else torch.from_numpy(x).cuda()
+
+
+def host_cache(t):
+    return t.view(torch.int16).cpu().numpy().view(np.uint16) if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+class Dev:
+    """A Cache on the GPU."""
+
+    def __init__(self, c):
+        self.c = c
+        self.k, self.v = dev_cache(c.k), dev_cache(c.v)
+        self.w = torch.from_numpy(c.w.copy()).cuda()
+        self.tables = torch.from_numpy(c.tables).cuda()
+        self.lens = torch.from_numpy(c.lens).cuda()
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def decode(self, pkv, q, scale, out, **kw):
+        if self.c.fp8:
+            return pkv.paged_attn_decode_weights_fp8(q, self.k, self.v, self.tables, self.lens, scale, self.c.k_scale,
+                                                     self.c.v_scale, out, self.w, err_flag=self.err, **kw)
+        return pkv.paged_attn_decode_weights(q, self.k, self.v, self.tables, self.lens, scale, out, self.w,
+                                             err_flag=self.err, **kw)
+
+    def plain(self, pkv, q, scale, out, **kw):
+        if self.c.fp8:
+            return pkv.paged_attn_decode_fp8(q, self.k, self.v, self.tables, self.lens, scale, self.c.k_scale,
+                                             self.c.v_scale, out, **kw)
+        return pkv.paged_attn_decode(q, self.k, self.v, self.tables, self.lens, scale, out, **kw)
+
+
+def queries(n, Hq, D, seed, gain=1.5):
+    return ref.to_bf16(gain * np.random.default_rng(seed).standard_normal((n, Hq, D), dtype=np.float32))
+
+
+def check_decode(pkv, c, G, seed=0, max_ctas=0, scale=None, expect=0):
+    scale = 1 / np.sqrt(c.D) if scale is None else scale
+    qb = queries(len(c.lens), c.Hkv * G, c.D, seed)
+    q, d = bf(qb), Dev(c)
+    out, plain = torch.empty_like(q), torch.empty_like(q)
+    d.decode(pkv, q, scale, out, max_ctas=max_ctas)
+    d.plain(pkv, q, scale, plain, max_ctas=max_ctas)
+    torch.cuda.synchronize()
+    assert int(d.err.item()) == expect
+    assert torch.equal(out, plain), "recording changed the attention's output"
+    want, w, add, big = ref.decode(c, ref.from_bf16(qb), scale)
+    got = out.float().cpu().numpy().astype(np.float64)
+    # the framework's bar for its attention outputs, relative for FP8 values above 1
+    assert (np.abs(got - want) <= 1e-2 + 2.0 ** -8 * np.abs(want)).all()
+    ref.check_weights(d.w.cpu().numpy(), w, add, ref.weight_tolerance(c.D, big), "decode")
+    return d
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_decode_weights_shapes(pkv, fp8, D, G):
+    """Lengths of zero, one, around a box, a 32-token box and a block; every group size."""
+    for bs in (16, 32, 48):
+        c = ref.Cache([0, 1, 15, 16, 17, 31, 33, 47, 49, 95, 96, 97, 300], bs, 3, D, fp8=fp8, seed=bs + G, mbs_extra=1)
+        check_decode(pkv, c, G, seed=G)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("max_ctas", [0, 1, 3, 40])
+def test_decode_weights_long_contexts_split_over_workers(pkv, fp8, max_ctas):
+    c = ref.Cache([5000, 1, 333, 0, 2049], 256, 2, 128, fp8=fp8, seed=max_ctas)
+    check_decode(pkv, c, 4, max_ctas=max_ctas)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_weights_large_batch(pkv, fp8):
+    """Many sequences: larger shared-memory layouts, 32-token boxes for FP8."""
+    lens = np.random.default_rng(1).integers(0, 70, size=900)
+    check_decode(pkv, ref.Cache(lens, 32, 2, 64, fp8=fp8, seed=7), 2)
+    check_decode(pkv, ref.Cache(lens[:300], 32, 1, 128, fp8=fp8, seed=8), 8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
+def test_decode_weights_scales(pkv, fp8, scale):
+    """All weights equal, a negative scale, and a scale that leaves one heavy token."""
+    check_decode(pkv, ref.Cache([1, 40, 500], 16, 2, 128, fp8=fp8, seed=3), 2, scale=scale)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_weights_all_empty(pkv, fp8):
+    c = ref.Cache([0, 0, 0], 16, 2, 64, fp8=fp8, seed=0, mbs_extra=2)
+    d = check_decode(pkv, c, 2)
+    assert np.array_equal(d.w.cpu().numpy(), c.w, equal_nan=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_weights_bad_block_gets_none(pkv, fp8):
+    c = ref.Cache([200, 64, 100], 32, 2, 128, fp8=fp8, seed=5)
+    c.tables[0, 2] = c.NB + 3   # in the middle
+    c.tables[1, 1] = -1         # the newest token's block
+    check_decode(pkv, c, 2, expect=FLAG_BAD_BLOCK)
+
+
+def test_decode_weights_bad_length_is_clamped(pkv):
+    c = ref.Cache([64, 64], 32, 2, 64, seed=5)
+    d = Dev(c)
+    d.lens[1] = 1000
+    qb = queries(2, 4, 64, 0)
+    q = bf(qb)
+    d.decode(pkv, q, 0.125, torch.empty_like(q))
+    assert int(d.err.item()) == FLAG_BAD_CONTEXT_LEN
+    _, w, add, big = ref.decode(c, ref.from_bf16(qb), 0.125)  # 64 = the table's 2 blocks of 32
+    ref.check_weights(d.w.cpu().numpy(), w, add, ref.weight_tolerance(64, big))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_weights_shared_prefix_blocks(pkv, fp8):
+    """Sequences that share prefix blocks all add to them."""
+    c = ref.Cache([300] * 6, 32, 2, 128, fp8=fp8, seed=9)
+    c.tables[:, :4] = c.tables[0, :4]
+    check_decode(pkv, c, 4)
+
+
+def test_decode_weights_accumulate_over_steps(pkv):
+    """Two steps on the same slots: the second adds, except on the newest token."""
+    c = ref.Cache([50, 260], 16, 2, 64, seed=2)
+    d = Dev(c)
+    for step in range(2):
+        qb = queries(2, 4, 64, step)
+        q = bf(qb)
+        d.decode(pkv, q, 0.125, torch.empty_like(q))
+        _, w, add, big = ref.decode(c, ref.from_bf16(qb), 0.125)
+        got = d.w.cpu().numpy()
+        ref.check_weights(got, w, add, ref.weight_tolerance(64, big), f"step {step}")
+        c.w = got
+
+
+def test_decode_weights_repeat_bit_for_bit(pkv):
+    c = ref.Cache(np.random.default_rng(0).integers(1, 3000, size=40), 16, 8, 128, seed=4)
+    q = bf(queries(40, 16, 128, 1))
+    got = []
+    for _ in range(3):
+        d = Dev(c)
+        d.decode(pkv, q, 0.09, torch.empty_like(q))
+        got.append(d.w.view(torch.int32))
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+# ------------------------------------------------------------------ prefill
+
+
+def check_prompt(pkv, c, q_lens, G, window=0, seed=0, scale=None, expect=0, pad_rows=0, max_q=None):
+    scale = 1 / np.sqrt(c.D) if scale is None else scale
+    cu_q = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    cu_k = np.concatenate([[0], np.cumsum(c.lens)]).astype(np.int32)
+    qb = queries(int(cu_q[-1]) + pad_rows, c.Hkv * G, c.D, seed)
+    q, d = bf(qb), Dev(c)
+    if pad_rows:
+        q[-pad_rows:] = float("nan")
+    out, plain = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    cq, ck = torch.from_numpy(cu_q).cuda(), torch.from_numpy(cu_k).cuda()
+    most = int(max(q_lens)) if max_q is None else max_q
+    pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cq, ck, most, scale, out, d.w, window=window, err_flag=d.err)
+    pkv.paged_prefill(q, d.k, d.v, d.tables, cq, ck, most, scale, plain)
+    torch.cuda.synchronize()
+    assert int(d.err.item()) == expect
+    assert torch.equal(out, plain), "recording changed the attention's output"
+    want, w, add, big = ref.prompt(c, ref.from_bf16(qb), cu_q, scale, window)
+    if pad_rows:
+        assert (out[-pad_rows:] == 7.0).all(), "rows behind the last sequence were written"
+        out, want = out[:-pad_rows], want[:-pad_rows]
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= 1e-2 + 2.0 ** -8 * np.abs(want)).all()
+    ref.check_weights(d.w.cpu().numpy(), w, add, ref.weight_tolerance(c.D, big), "prefill")
+    return d
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("window", [0, 1, 5, 64])
+def test_prompt_weights_shapes(pkv, D, G, window):
+    """Chunks of 1 to 150 tokens after prefixes of none to 200, odd lengths, small blocks."""
+    q_lens = [1, 7, 16, 65, 150, 3, 130]
+    prefix = [0, 33, 128, 1, 0, 200, 127]
+    for bs in (16, 48, 64):
+        c = ref.Cache(np.add(q_lens, prefix), bs, 2, D, seed=bs + G, mbs_extra=1)
+        check_prompt(pkv, c, q_lens, G, window, seed=G, pad_rows=3)
+
+
+def test_prompt_weights_long(pkv):
+    """More than one tile of everything: long prefix, long chunk."""
+    check_prompt(pkv, ref.Cache([1500, 700], 256, 2, 128, seed=1), [600, 700], 2)
+    check_prompt(pkv, ref.Cache([1500, 700], 16, 1, 64, seed=2), [600, 700], 8, window=33)
+
+
+def test_prompt_weights_empty_sequences_and_loose_bound(pkv):
+    c = ref.Cache([40, 64, 0, 90], 16, 2, 64, seed=3)
+    check_prompt(pkv, c, [5, 0, 0, 90], 2, max_q=500)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
+def test_prompt_weights_scales(pkv, scale):
+    check_prompt(pkv, ref.Cache([100, 260], 16, 2, 128, seed=3), [50, 200], 2, scale=scale)
+
+
+def test_prompt_weights_bad_block_gets_none(pkv):
+    c = ref.Cache([200, 64, 100], 32, 2, 128, seed=5)
+    c.tables[0, 2] = c.NB + 3
+    c.tables[1, 0] = -1      # the first tokens: their queries see nothing at all
+    check_prompt(pkv, c, [100, 64, 100], 2, expect=FLAG_BAD_BLOCK)
+
+
+def test_prompt_weights_bad_lengths_record_nothing(pkv):
+    """A sequence with more new tokens than context is skipped, the others are not."""
+    c = ref.Cache([50, 60, 70], 16, 2, 64, seed=6)
+    d = Dev(c)
+    cu_q = torch.tensor([0, 20, 100, 130], dtype=torch.int32, device="cuda")  # 80 new tokens > 60
+    cu_k = torch.tensor([0, 50, 110, 180], dtype=torch.int32, device="cuda")
+    qb = queries(130, 4, 64, 0)
+    q = bf(qb)
+    pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cu_q, cu_k, 100, 0.125, torch.zeros_like(q), d.w, err_flag=d.err)
+    assert int(d.err.item()) == FLAG_BAD_CONTEXT_LEN
+    ok = ref.Cache([50, 60, 70], 16, 2, 64, seed=6)
+    ok.lens = np.array([50, 0, 70], dtype=np.int32)
+    qs = np.concatenate([ref.from_bf16(qb)[:20], ref.from_bf16(qb)[100:]])
+    _, w, add, big = ref.prompt(ok, qs, np.array([0, 20, 20, 50]), 0.125)
+    ref.check_weights(d.w.cpu().numpy(), w, add, ref.weight_tolerance(64, big))
+
+
+def test_prompt_weights_neighbour_nan_stays_out(pkv):
+    """NaN queries of one sequence do not reach the weights of its neighbours."""
+    c = ref.Cache([30, 45, 77], 16, 2, 64, seed=8)
+    d = Dev(c)
+    cu = torch.tensor([0, 30, 75, 152], dtype=torch.int32, device="cuda")
+    qb = queries(152, 4, 64, 0)
+    q = bf(qb)
+    q[30:75] = float("nan")
+    pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cu, cu, 77, 0.125, torch.zeros_like(q), d.w, err_flag=d.err)
+    got = d.w.cpu().numpy()
+    _, w, add, big = ref.prompt(c, ref.from_bf16(qb), cu.cpu().numpy(), 0.125)
+    for b in (0, 2):
+        s = c.slots(b)
+        pick = np.zeros_like(c.w, dtype=bool)
+        pick[s // 16, :, s % 16] = True
+        ref.check_weights(np.where(pick, got, 0), np.where(pick, w, 0), np.where(pick, add, 0),
+                          ref.weight_tolerance(64, big), f"sequence {b}")
+
+
+# ------------------------------------------------------------------ eviction
+
+
+def check_evict(pkv, c, budget, recent, in_place=False, expect=0, want=None):
+    d = Dev(c)
+    out = d.lens if in_place else torch.full_like(d.lens, -5)
+    pkv.evict_kvcache(d.k, d.v, d.w, d.tables, d.lens, budget, recent, out, err_flag=d.err)
+    torch.cuda.synchronize()
+    assert int(d.err.item()) == expect
+    k, v, w, lens = want or ref.evict(c, budget, recent)
+    np.testing.assert_array_equal(out.cpu().numpy(), lens)
+    np.testing.assert_array_equal(host_cache(d.k), k)
+    np.testing.assert_array_equal(host_cache(d.v), v)
+    np.testing.assert_array_equal(d.w.cpu().numpy(), w)
+    return d
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("budget,recent", [(1, 0), (1, 1), (17, 5), (64, 64), (64, 0), (100, 99), (299, 32), (5000, 7)])
+def test_evict_shapes(pkv, fp8, D, budget, recent):
+    for bs, Hkv in ((16, 3), (48, 1)):
+        c = ref.Cache([0, 1, 2, 16, 17, 18, 63, 64, 65, 100, 300], bs, Hkv, D, fp8=fp8, seed=budget, mbs_extra=1)
+        check_evict(pkv, c, budget, recent, in_place=bs == 16)
+
+
+@pytest.mark.parametrize("budget,recent", [(1000, 100), (2500, 0), (4999, 2000)])
+def test_evict_long(pkv, budget, recent):
+    check_evict(pkv, ref.Cache([5000, 3001, 1024, 1025], 256, 2, 128, seed=1), budget, recent)
+
+
+def test_evict_many_sequences(pkv):
+    lens = np.random.default_rng(1).integers(0, 200, size=400)
+    check_evict(pkv, ref.Cache(lens, 16, 4, 64, fp8=True, seed=2), 60, 20)
+
+
+def fill(c, b, h, x):
+    s = c.slots(b)
+    c.w[s // c.bs, h, s % c.bs] = x
+
+
+@pytest.mark.parametrize("kind", ["equal", "zeros", "few values", "negative", "infinite", "nan", "signed zero", "subnormal", "ascending", "descending"])
+def test_evict_weights_of_every_kind(pkv, kind):
+    c = ref.Cache([2300, 700], 64, 2, 64, seed=4)
+    r = np.random.default_rng(5)
+    for b in range(2):
+        n = int(c.lens[b])
+        for h in range(2):
+            x = {"equal": lambda: np.full(n, 0.25), "zeros": lambda: np.zeros(n), "few values": lambda: r.integers(0, 4, n) * 0.5,
+                 "negative": lambda: r.standard_normal(n), "infinite": lambda: r.choice([np.inf, -np.inf, 1.0, 2.0], n),
+                 "nan": lambda: r.choice([np.nan, -np.nan, 1.0, np.inf, 0.0], n), "signed zero": lambda: r.choice([-0.0, 0.0], n),
+                 "subnormal": lambda: r.integers(0, 50, n) * 1e-45, "ascending": lambda: np.arange(n) * 0.1,
+                 "descending": lambda: n - np.arange(n) * 0.1}[kind]()
+            fill(c, b, h, x.astype(np.float32))
+    check_evict(pkv, c, 300, 30)
+    check_evict(pkv, c, 300, 300)
+
+
+def test_evict_bad_sequences_are_left_alone(pkv):
+    c = ref.Cache([200, 150, 100], 32, 2, 64, seed=3)
+    good = ref.evict(c, 40, 8)
+    k, v, w, lens = (x.copy() for x in good)
+    s = c.slots(1)
+    for x, y in ((k, c.k), (v, c.v)):
+        x.reshape(-1, 2, 64)[s] = y.reshape(-1, 2, 64)[s]
+    w[s // 32, :, s % 32] = c.w[s // 32, :, s % 32]
+    lens[1] = 150
+    c.tables[1, 4] = c.NB
+    check_evict(pkv, c, 40, 8, expect=FLAG_BAD_BLOCK, want=(k, v, w, lens))
+
+
+def test_evict_bad_length_is_left_alone(pkv):
+    c = ref.Cache([100, 64], 32, 2, 64, seed=3)
+    k, v, w, lens = ref.evict(c, 70, 8)
+    c.lens = np.array([100, 129], dtype=np.int32)  # the table holds 4 blocks of 32
+    lens[1] = 129
+    check_evict(pkv, c, 70, 8, expect=FLAG_BAD_CONTEXT_LEN, want=(k, v, w, lens))
+    c.lens = np.array([100, -1], dtype=np.int32)
+    lens[1] = -1
+    check_evict(pkv, c, 70, 8, expect=FLAG_BAD_CONTEXT_LEN, want=(k, v, w, lens))

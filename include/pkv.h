@@ -385,7 +385,10 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
  *              query sees them
  *   workspace  device scratch of pkv_prefill_weights_workspace_bytes(Tq, Hq)
  *              bytes, 16-byte aligned (every row's log-sum-exp)
- * Hkv <= 65535.  A sequence that the attention skips records nothing.
+ * B * Hkv * MBS * bs / 128 < 2^31.  A sequence that the attention skips
+ * records nothing.  The scores of the recorded queries are made a second time
+ * (their weights need each row's final sum), so recording every query adds
+ * half of the attention's multiplications; a window adds little.
  */
 size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq);
 

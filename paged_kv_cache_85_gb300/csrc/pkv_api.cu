@@ -157,6 +157,7 @@ struct DeviceState {
     int sms = 0;
     bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
     bool pf_smem_set[2][9] = {};     // prefill: [D == 128][G]
+    bool pw_smem_set[2][9] = {};     // its weights kernel: [D == 128][G]
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -235,14 +236,16 @@ pkv_status occupancy(int dev, const void *fn, int threads, size_t smem, int *occ
 // 4-D view of a cache [NB*bs tokens, Hkv, D] as (64 columns, D/64 halves,
 // Hkv, tokens); a box is 64 columns x 1 half x 1 head x 16 tokens, landing as
 // 16 rows of 128 B with the 128-byte swizzle (conflict-free ldmatrix reads).
-pkv_status make_cache_map(CUtensorMap *map, const void *cache, long long tokens, int Hkv, int D)
+// rows = 64: a run of 64 tokens at once, for block sizes that hold whole runs.
+pkv_status make_cache_map(CUtensorMap *map, const void *cache, long long tokens, int Hkv, int D,
+                          int rows = pkv::kBox)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc)
         return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     cuuint64_t dims[4] = {64, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)tokens};
     cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
-    cuuint32_t box[4] = {64, 1, 1, (cuuint32_t)pkv::kBox};
+    cuuint32_t box[4] = {64, 1, 1, (cuuint32_t)rows};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(cache), dims,
                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -320,8 +323,9 @@ pkv_status make_cache_map8(CUtensorMap *map, const void *cache, long long tokens
 // the same cache pointer and shape always encode the same map).
 // Map kinds: 16-token boxes of a bf16 cache (one half per copy), 16- or
 // 32-token boxes of an FP8 cache, or, for the prefill kernel, whole 64-token
-// tiles or 16-token boxes of a bf16 cache with both halves per copy.
-enum MapKind { kMapBox = 0, kMapBox8 = 1, kMapTile = 2, kMapBoxHalves = 3, kMapBox8Wide = 4 };
+// tiles or 16-token boxes of a bf16 cache with both halves per copy; for its
+// weights kernel 64-token runs of one half.
+enum MapKind { kMapBox = 0, kMapBox8 = 1, kMapTile = 2, kMapBoxHalves = 3, kMapBox8Wide = 4, kMapRun = 5 };
 struct MapEntry {
     const void *ptr = nullptr;
     long long tokens = 0;
@@ -344,6 +348,7 @@ pkv_status cached_cache_map(CUtensorMap *map, const void *cache, long long token
     const pkv_status ps = kind == kMapBox8   ? make_cache_map8(map, cache, tokens, Hkv, D, pkv::kBox)
                           : kind == kMapBox8Wide ? make_cache_map8(map, cache, tokens, Hkv, D, 2 * pkv::kBox)
                           : kind == kMapTile ? make_cache_tile_map(map, cache, tokens, Hkv, D, pkv::kPrefillKeys)
+                          : kind == kMapRun ? make_cache_map(map, cache, tokens, Hkv, D, pkv::kPrefillKeys)
                           : kind == kMapBoxHalves ? make_cache_tile_map(map, cache, tokens, Hkv, D, pkv::kBox)
                                                   : make_cache_map(map, cache, tokens, Hkv, D);
     if (ps != PKV_OK)
@@ -739,8 +744,8 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         return fail(PKV_ERR_UNSUPPORTED, "paged_prefill: Tq must be < 2^31 and B <= 65535");
     if (record && window < 0)
         return fail(PKV_ERR_INVALID_ARG, "paged_prefill_weights: window=%d is negative", window);
-    if (record && Hkv > 65535)
-        return fail(PKV_ERR_UNSUPPORTED, "paged_prefill_weights: Hkv must be <= 65535");
+    if (record && ((long long)MBS * bs / 128 + 1) * Hkv * B >= 0x7fff0000LL)
+        return fail(PKV_ERR_UNSUPPORTED, "paged_prefill_weights: B*Hkv*MBS*bs/128 must be < 2^31");
     if (B == 0 || Tq == 0 || max_seqlen_q == 0)
         return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !cu_seqlens_k || !out)
@@ -813,8 +818,24 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
     p.neg_scale = scale < 0.f;
     p.tile_copies = tile_copies ? 1 : 0;
-    if (record)
+    CUtensorMap tmw;  // the weights kernel's view of K
+    if (record) {
         p.lse = static_cast<float *>(workspace);
+        p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
+        const void *wfn = pkv::prompt_weights_kernel_fn(D, G);
+        std::lock_guard<std::mutex> lk(g_mu);
+        bool &set = st->pw_smem_set[D == 128][G];
+        if (!set) {
+            cudaError_t e = cudaFuncSetAttribute(wfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)pkv::prompt_weights_smem_bytes(D));
+            if (e != cudaSuccess)
+                return fail(PKV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            set = true;
+        }
+    }
+    if (record &&
+        (ps = cached_cache_map(&tmw, k_cache, tokens, Hkv, D, tile_copies ? kMapRun : kMapBox)) != PKV_OK)
+        return ps;
     // Persistent grid: one CTA per SM (each holds all of the SM's TMEM
     // columns, and asks for more than half of its shared memory so that no
     // second CTA lands beside it), each walking its share of the work items.
@@ -829,7 +850,8 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_prefill launch: %s", cudaGetErrorString(e));
     if (record) {
-        e = pkv::launch_prompt_weights(D, p, k_cache, weights, window, static_cast<cudaStream_t>(stream));
+        e = pkv::launch_prompt_weights(D, G, &tmq, &tmw, p, weights, window, st->sms,
+                                       static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
             return fail(PKV_ERR_CUDA, "paged_prefill_weights launch: %s", cudaGetErrorString(e));
     }
@@ -850,7 +872,8 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
 
 size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq)
 {
-    return Tq < 1 || Hq < 1 ? 0 : pkv::align_up((size_t)Tq * Hq * sizeof(float), 256);
+    // every row's log-sum-exp, and the weights kernel's work counter
+    return Tq < 1 || Hq < 1 ? 0 : pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
 }
 
 pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const void *v_cache,

@@ -25,13 +25,17 @@ struct PrefillParams {
     int neg_scale;                // scale < 0: the score MMA negates Q
     int tile_copies;              // bs % 64 == 0: K/V maps copy whole 64-token tiles
     float *lse = nullptr;         // nullable: [Hkv, Tq, G] log-sum-exp of every row (log2 units)
+    int32_t *ticket = nullptr;    // nullable: work counter of the weights kernel, cleared here
 };
 
 cudaError_t launch_prefill(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
                            const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
                            cudaStream_t stream);
-cudaError_t launch_prompt_weights(int D, const PrefillParams &p, const void *k_cache, float *weights,
-                                  int window, cudaStream_t stream);
+cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                  const PrefillParams &p, float *weights, int window, int sms,
+                                  cudaStream_t stream);
+const void *prompt_weights_kernel_fn(int D, int G);
+size_t prompt_weights_smem_bytes(int D);
 const void *prefill_kernel(int D, int G);
 size_t prefill_smem_bytes(int D);
 constexpr int kPrefillRows = 128;  // (token, head) rows per query tile (two tiles per work item)

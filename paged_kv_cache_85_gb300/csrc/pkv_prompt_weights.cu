@@ -1,128 +1,526 @@
-// Attention weights of a prefill step, added to the cache's weight table.
+// Attention weights of a prefill step, added to the cache's weight table, on
+// the 5th-generation tensor cores.
 //
 // The prefill kernel left every (new token, query head)'s log-sum-exp lse of
 // its scores (log2 units).  The weight that token t of a sequence received
-// from the observing queries is
-//     w[t] = sum over observing new tokens i that see t, and over the G heads
+// from the recorded queries is
+//     w[t] = sum over recorded new tokens i that see t, and over the G heads
 //            of the group, of 2^(s[i, g, t] - lse[i, g]),
 // which needs the final lse of every row, so the scores are made again here.
 // It is added to weights[block, kv head, offset], or stored there for the
 // step's new tokens, whose slots may hold what an earlier owner left.
 //
-// One thread per cached token: its K row stays in registers and the query rows
-// pass by in shared memory.
+// The scores are made transposed, S^T = K Q^T with the 128 cached tokens of an
+// item as the MMA's rows, so that a thread owns one token (a TMEM lane) and
+// the sum over queries runs along its own columns: no reduction over threads,
+// one addition to memory per token and KV head, and the same result in every
+// run.  An item is 128 tokens of one sequence and KV head; the (new token,
+// head) rows that see any of them pass by in tiles of 128.  A persistent CTA
+// per SM takes items by ticket (sequences in order, early tokens first, which
+// are the long items of a causal chunk); the sum does not depend on who takes
+// what.  Warps:
+//   0..3, 4..7  two groups of 128 threads that take turns over the query
+//         tiles: load 128 scores per token from TMEM, exponentiate against the
+//         tile's lse (shared memory, read as broadcasts), add up.  Partial sums
+//         per tile, then per item: no long sequential fp32 sum
+//   8     producer: ticket, item, TMA of the K tile (two stages, so the next
+//         item's K is on its way) and of the query tiles (four stages)
+//   9     MMA: per query tile D / 16 steps of M = 128 (tokens), N = 128
+//         (queries) into one of four TMEM buffers
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
 #include "pkv_kernels.h"
 #include "pkv_prefill.h"
 #include "pkv_ptx.cuh"
+#include "pkv_tc.cuh"
 
 namespace pkv {
 
-constexpr int kPwTokens = 128;  // tokens (threads) per CTA
-constexpr int kPwRows = 32;     // (new token, head) rows in shared memory at a time
+constexpr int kPwTokens = 128;  // cached tokens per item (MMA M)
+constexpr int kPwRows = 128;    // (new token, head) rows per query tile (MMA N)
+constexpr int kPwKStages = 2;
+constexpr int kPwQStages = 4;
+constexpr int kPwSBufs = 4;     // TMEM score buffers of 128 columns
+constexpr int kPwItems = 4;     // published items
+constexpr int kPwThreads = 10 * 32;
+constexpr int kPwProducerWarp = 8;
+constexpr int kPwMmaWarp = 9;
 
-template <int D>
-__global__ void __launch_bounds__(kPwTokens)
-    prompt_weights_kernel(const PrefillParams p, const uint16_t *k_cache, float *weights, int window)
+// 128 tokens of one sequence and KV head, and the query tiles that see them
+struct PwItem {
+    int b, kvh, t0;     // b < 0: no more work
+    int cq0, q_len, k_len;
+    int i0;             // first recorded new token that sees a token of the item
+    int tiles;          // query tiles from i0 on
+};
+
+struct PwSmem {
+    size_t q, k, lse, part, bars, items, slot, total;
+};
+
+constexpr int kPwBars = 2 * kPwKStages + 2 * kPwQStages + 2 * kPwSBufs + 2 * kPwItems + 16 + 1;
+
+__host__ __device__ inline PwSmem pw_smem_layout(int D)
 {
-    __shared__ __align__(16) float sq[kPwRows][D];
-    __shared__ float slse[kPwRows];
-    grid_dependency_wait();
-    const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-    const int G = p.Hq / p.Hkv;
-    const int cq0 = p.cu_q[b], cq1 = p.cu_q[b + 1], ck0 = p.cu_k[b], ck1 = p.cu_k[b + 1];
-    const int q_len = cq1 - cq0, k_len = ck1 - ck0, base = k_len - q_len;
-    if (cq0 < 0 || q_len < 0 || (long long)cq1 > p.Tq || k_len < q_len ||
-        (long long)k_len > (long long)p.MBS * p.bs || q_len > p.max_q)
-        return;  // skipped by the attention as well, which reports it
-    const int t0 = blockIdx.x * kPwTokens, t = t0 + tid;
-    if (q_len == 0 || t0 >= k_len)
-        return;
-    int blk = -1, off = 0;
-    if (t < k_len) {
-        blk = p.block_tables[(size_t)b * p.MBS + t / p.bs];
-        off = t % p.bs;
-        if (blk < 0 || blk >= p.NB)
-            blk = -1;
+    PwSmem L;
+    size_t o = 0;
+    L.q = o;  // stages of [D/64 halves][128 rows][128 B]
+    o += (size_t)kPwQStages * (D / 64) * kPwRows * 128;
+    L.k = o;  // stages alike
+    o += (size_t)kPwKStages * (D / 64) * kPwTokens * 128;
+    L.lse = o;  // [softmax warp][2][128] negated log-sum-exps of a query tile
+    o += 8 * 2 * kPwRows * sizeof(float);
+    L.part = o;  // [2][128] the second group's sums on their way to the first
+    o += 2 * kPwTokens * sizeof(float);
+    L.bars = o;
+    o += 8 * kPwBars;
+    L.items = align_up(o, 16);
+    o = L.items + kPwItems * sizeof(PwItem);
+    L.slot = o;
+    o += 16;
+    L.total = align_up(o, 16) + 1024;
+    // more than half an SM's shared memory: one CTA, which holds all of the
+    // SM's TMEM columns, per SM
+    if (L.total < kSmemPerSm / 2 + 4 * 1024)
+        L.total = kSmemPerSm / 2 + 4 * 1024;
+    return L;
+}
+
+struct PwParams {
+    PrefillParams f;   // the prefill call's (q, lengths, tables, lse, scale)
+    float *weights;
+    int window;        // 0: every new token records
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kPwThreads, 1)
+    prompt_weights_kernel(const __grid_constant__ CUtensorMap tmq,
+                          const __grid_constant__ CUtensorMap tmk, const PwParams P)
+{
+    constexpr int HALVES = D / 64;
+    constexpr int TPC = kPwRows / G;                  // new tokens per query tile
+    constexpr uint32_t kHalf = kPwRows * 128;         // 128 rows of 64 columns
+    constexpr uint32_t kTile = HALVES * kHalf;
+    constexpr unsigned FULL = 0xffffffffu;
+    static_assert(kPwRows == kPwTokens, "Q and K tiles share their layout");
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const PwSmem L = pw_smem_layout(D);
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L.bars);
+    uint64_t *k_empty = k_full + kPwKStages;   // the item's MMAs completed
+    uint64_t *q_full = k_empty + kPwKStages;
+    uint64_t *q_empty = q_full + kPwQStages;   // the tile's MMAs completed
+    uint64_t *s_full = q_empty + kPwQStages;
+    uint64_t *s_empty = s_full + kPwSBufs;     // the scores are in registers (4 warps)
+    uint64_t *item_ready = s_empty + kPwSBufs;
+    uint64_t *item_free = item_ready + kPwItems;  // 8 softmax warps and the MMA warp
+    uint64_t *part_full = item_free + kPwItems;   // [2][4] a warp's part written ...
+    uint64_t *part_empty = part_full + 8;         // ... and taken over by its partner
+    uint64_t *mma_done = part_empty + 8;
+    PwItem *items = reinterpret_cast<PwItem *>(smem + L.items);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
+    uint8_t *sQ = smem + L.q, *sK = smem + L.k;
+    const PrefillParams &p = P.f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    grid_launch_dependents();
+    if (warp == kPwProducerWarp && lane == 0) {
+        for (int s = 0; s < kPwKStages; s++) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < kPwQStages; s++) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+        }
+        for (int s = 0; s < kPwSBufs; s++) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&s_empty[s], 4);
+        }
+        for (int s = 0; s < kPwItems; s++) {
+            mbar_init(&item_ready[s], 1);
+            mbar_init(&item_free[s], 9);
+        }
+        for (int s = 0; s < 8; s++) {
+            mbar_init(&part_full[s], 1);
+            mbar_init(&part_empty[s], 1);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbarrier_init();
+    } else if (warp == kPwMmaWarp) {
+        tc::alloc(smem_u32(slot), 512);
+        tc::relinquish();
     }
-    uint32_t kr[D / 2];
-#pragma unroll
-    for (int i = 0; i < D / 2; i++)
-        kr[i] = 0;
-    if (blk >= 0) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            k_cache + (((size_t)blk * p.bs + off) * p.Hkv + h) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; i++) {
-            const uint4 x = src[i];
-            kr[4 * i] = x.x;
-            kr[4 * i + 1] = x.y;
-            kr[4 * i + 2] = x.z;
-            kr[4 * i + 3] = x.w;
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *slot;
+
+    if (warp == kPwProducerWarp) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tensormap(&tmq);
+            prefetch_tensormap(&tmk);
         }
-    }
-    const float sl = p.neg_scale ? -p.scale_log2 : p.scale_log2;
-    int i0 = max(0, t0 - base);  // first new token that sees any of these tokens
-    if (window > 0)
-        i0 = max(i0, q_len - window);
-    float w = 0.f;
-    for (int r0 = i0 * G; r0 < q_len * G; r0 += kPwRows) {
-        const int nr = min(kPwRows, q_len * G - r0);
-        __syncthreads();
-        for (int e = tid; e < nr * (D / 2); e += kPwTokens) {
-            const int r = e / (D / 2), c = e % (D / 2);
-            const int i = (r0 + r) / G, g = (r0 + r) % G;
-            const uint32_t x = reinterpret_cast<const uint32_t *>(
-                p.q + ((size_t)(cq0 + i) * p.Hq + (size_t)h * G + g) * D)[c];
-            const float2 f = bf16x2_to_float2(x);
-            sq[r][2 * c] = f.x;
-            sq[r][2 * c + 1] = f.y;
-        }
-        if (tid < nr) {
-            const int i = (r0 + tid) / G, g = (r0 + tid) % G;
-            slse[tid] = p.lse[((size_t)h * p.Tq + cq0 + i) * G + g];
-        }
-        __syncthreads();
-        for (int r = 0; r < nr; r++) {
-            if (t > base + (r0 + r) / G)
-                continue;  // that query does not see this token
-            float s = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 4; c++) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sq[r][4 * c]);
-                const float2 k0 = bf16x2_to_float2(kr[2 * c]), k1 = bf16x2_to_float2(kr[2 * c + 1]);
-                s = fmaf(x.x, k0.x, s);
-                s = fmaf(x.y, k0.y, s);
-                s = fmaf(x.z, k1.x, s);
-                s = fmaf(x.w, k1.y, s);
+        grid_dependency_wait();  // lse, caches and the cleared ticket
+        bool ok = true;
+        int n = 0, gq = 0, nk = 0;  // items published, Q tiles and K tiles issued
+        // cursor over the sequences: lane l looks at sequence b0 + l, `before`
+        // items lie in the sequences before b0
+        int b0 = 0;
+        long long before = 0;
+        int cq0 = 0, q_len = 0, k_len = 0;  // of sequence b0 + lane
+        long long mine = 0, incl = 0;       // its items, and those up to it in this group of 32
+        auto look = [&]() {
+            cq0 = q_len = k_len = 0;
+            const int b = b0 + lane;
+            if (b < p.B) {
+                const int a0 = __ldg(p.cu_q + b), a1 = __ldg(p.cu_q + b + 1);
+                const int c0 = __ldg(p.cu_k + b), c1 = __ldg(p.cu_k + b + 1);
+                const int ql = a1 - a0, kl = c1 - c0;
+                // the sequences that the attention takes (it reports the others)
+                if (a0 >= 0 && ql > 0 && (long long)a1 <= p.Tq && kl >= ql && kl <= p.MBS * p.bs &&
+                    ql <= p.max_q) {
+                    cq0 = a0;
+                    q_len = ql;
+                    k_len = kl;
+                }
             }
-            w += fast_exp2(fmaf(s, sl, -slse[r]));
+            mine = (long long)((k_len + kPwTokens - 1) / kPwTokens) * p.Hkv;
+            incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(FULL, incl, off);
+                if (lane >= off)
+                    incl += y;
+            }
+        };
+        look();
+        int ticket = 0;
+        if (lane == 0)
+            ticket = atomicAdd(p.ticket, 1);
+        for (;;) {
+            // ---- the ticket's item
+            PwItem it{-1, 0, 0, 0, 0, 0, 0, 0};
+            const long long pos = __shfl_sync(FULL, ticket, 0);
+            if (ok) {
+                while (b0 < p.B && pos - before >= __shfl_sync(FULL, incl, 31)) {
+                    before += __shfl_sync(FULL, incl, 31);
+                    b0 += 32;
+                    if (b0 < p.B)
+                        look();
+                }
+                if (b0 < p.B) {
+                    const long long r = pos - before;
+                    const unsigned in = __ballot_sync(FULL, r >= incl - mine && r < incl);
+                    const int src = __ffs(in) - 1;
+                    const int rr = (int)(r - __shfl_sync(FULL, incl - mine, src));
+                    it.b = b0 + src;
+                    it.kvh = rr % p.Hkv;
+                    it.t0 = rr / p.Hkv * kPwTokens;
+                    it.cq0 = __shfl_sync(FULL, cq0, src);
+                    it.q_len = __shfl_sync(FULL, q_len, src);
+                    it.k_len = __shfl_sync(FULL, k_len, src);
+                    it.i0 = max(0, it.t0 - (it.k_len - it.q_len));
+                    if (P.window > 0)
+                        it.i0 = max(it.i0, it.q_len - P.window);
+                    it.tiles = ((it.q_len - it.i0) + TPC - 1) / TPC;
+                }
+            }
+            // the next ticket, on its way while this item is copied
+            if (it.b >= 0 && lane == 0)
+                ticket = atomicAdd(p.ticket, 1);
+            const int sl = n % kPwItems;
+            if (n >= kPwItems &&
+                !(ok = ok && __all_sync(FULL, mbar_wait(&item_free[sl], ((n / kPwItems) & 1) ^ 1))))
+                break;  // the other warps time out on item_ready and stop
+            if (lane == 0) {
+                items[sl] = it;
+                mbar_arrive(&item_ready[sl]);
+            }
+            __syncwarp();
+            if (it.b < 0)
+                break;
+            // ---- K tile: lanes 0..7 resolve one 16-token box each; where blocks
+            // hold whole 64-token runs one copy per run and half, else per box
+            {
+                const int t = it.t0 + lane * kBox;
+                int row = -1;
+                if (lane < kPwTokens / kBox && t < it.k_len) {
+                    const int blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
+                    if (blk >= 0 && blk < p.NB)
+                        row = blk * p.bs + t % p.bs;
+                }
+                const int per = p.tile_copies ? kPrefillKeys : kBox;  // tokens per copy
+                const bool copies = row >= 0 && (lane * kBox) % per == 0;
+                const int s = nk % kPwKStages;
+                if (!(ok = __all_sync(FULL, mbar_wait(&k_empty[s], ((nk / kPwKStages) & 1) ^ 1))))
+                    break;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, copies)) * per * D * 2;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&k_full[s], bytes);
+                __syncwarp();
+                if (copies) {
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; hf++)
+                        tma_load_4d(sK + (size_t)s * kTile + hf * kHalf + lane * kBox * 128, &tmk, 0, hf,
+                                    it.kvh, row, &k_full[s]);
+                }
+                nk++;
+            }
+            // ---- query tiles
+            for (int j = 0; j < it.tiles && ok; j++) {
+                const int s = gq % kPwQStages;
+                if (!(ok = __all_sync(FULL, mbar_wait(&q_empty[s], ((gq / kPwQStages) & 1) ^ 1))))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[s], kTile);
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; hf++)
+                        tma_load_4d(sQ + (size_t)s * kTile + hf * kHalf, &tmq, 0, hf, it.kvh * G,
+                                    it.cq0 + it.i0 + j * TPC, &q_full[s]);
+                }
+                gq++;
+            }
+            if (!ok)
+                break;
+            n++;
         }
+        if (lane == 0) {
+            if (!ok)
+                flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
+            // copies still in flight land before the CTA may exit
+            for (int g = max(0, nk - kPwKStages); g < nk; g++)
+                mbar_wait(&k_full[g % kPwKStages], (g / kPwKStages) & 1);
+            for (int g = max(0, gq - kPwQStages); g < gq; g++)
+                mbar_wait(&q_full[g % kPwQStages], (g / kPwQStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kPwMmaWarp) {
+        // ----------------------------------------------------------------- MMA
+        bool ok = true;
+        // A = K (negated for a negative scale: bit 13), B = Q, both K-major
+        const uint32_t idS = tc::idesc_bf16(kPwTokens, kPwRows, false) | (p.neg_scale ? 1u << 13 : 0u);
+        if (lane == 0) {
+            int gq = 0;
+            for (int n = 0; ok; n++) {
+                if (!(ok = mbar_wait(&item_ready[n % kPwItems], (n / kPwItems) & 1)))
+                    break;
+                const PwItem it = items[n % kPwItems];
+                if (it.b < 0)
+                    break;
+                const int ks = n % kPwKStages;
+                if (!(ok = mbar_wait(&k_full[ks], (n / kPwKStages) & 1)))
+                    break;
+                const uint32_t ka = smem_u32(sK + (size_t)ks * kTile);
+                for (int j = 0; j < it.tiles; j++, gq++) {
+                    const int s = gq % kPwQStages, buf = gq % kPwSBufs;
+                    if (!(ok = mbar_wait(&q_full[s], (gq / kPwQStages) & 1)))
+                        break;
+                    if (!(ok = mbar_wait(&s_empty[buf], ((gq / kPwSBufs) & 1) ^ 1)))
+                        break;
+                    tc::fence_after();
+                    const uint32_t qb = smem_u32(sQ + (size_t)s * kTile);
+#pragma unroll
+                    for (int kq = 0; kq < D / 16; kq++) {
+                        const uint32_t off = (uint32_t)(kq >> 2) * kHalf + (uint32_t)(kq & 3) * 32;
+                        tc::mma_ss(tmem + 128u * buf, tc::smem_desc(ka + off, 16, 1024),
+                                   tc::smem_desc(qb + off, 16, 1024), idS, kq > 0);
+                    }
+                    tc::commit(smem_u32(&s_full[buf]));
+                    tc::commit(smem_u32(&q_empty[s]));
+                }
+                if (!ok)
+                    break;
+                tc::commit(smem_u32(&k_empty[ks]));
+                mbar_arrive(&item_free[n % kPwItems]);
+            }
+            if (!ok)
+                flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
+            tc::commit(smem_u32(mma_done));  // every MMA completes before TMEM is released
+        }
+        __syncwarp();
+        mbar_wait(mma_done, 0);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int grp = warp >> 2;
+        const int r = threadIdx.x & 127;  // token of the item = TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float *nlse = reinterpret_cast<float *>(smem + L.lse) + warp * 2 * kPwRows;
+        float *part = reinterpret_cast<float *>(smem + L.part);
+        const float sl = p.scale_log2;
+        const float2 sl2 = make_float2(sl, sl);
+        grid_dependency_wait();
+        bool ok = true;
+        int gq = 0;    // query tiles before this item
+        int seen = 0;  // query tiles of this group so far
+        int parts = 0; // sums handed over so far
+        for (int n = 0; ok; n++) {
+            ok = __all_sync(FULL, mbar_wait(&item_ready[n % kPwItems], (n / kPwItems) & 1));
+            if (!ok)
+                break;
+            const PwItem it = items[n % kPwItems];
+            if (it.b < 0)
+                break;
+            const int j0 = (gq & 1) == grp ? 0 : 1;  // this group's first tile of the item
+            const int t = it.t0 + r;
+            const int base = it.k_len - it.q_len;
+            int blk = -1;
+            if (t < it.k_len)
+                blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
+            const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G;
+            float sum = 0.f;
+            for (int j = j0; j < it.tiles; j += 2) {
+                const int g = gq + j, buf = g % kPwSBufs;
+                const int i_first = it.i0 + j * TPC;
+                // the tile's log-sum-exps, a copy per warp; +inf (weight 0) past the sequence
+                float *nl = nlse + (seen & 1) * kPwRows;
+                seen++;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int c = lane + 32 * i;
+                    nl[c] = i_first + c / G < it.q_len ? -__ldg(lse + (size_t)i_first * G + c) : -INFINITY;
+                }
+                __syncwarp();
+                ok = __all_sync(FULL, mbar_wait(&s_full[buf], (g / kPwSBufs) & 1));
+                if (!ok)
+                    break;
+                tc::fence_after();
+                // columns c0 <= c < c1 are queries that see this token
+                const int c0 = (t - base - i_first) * G;
+                const int c1 = (it.q_len - i_first) * G;
+                const bool masked = __any_sync(FULL, c0 > 0 || c1 < kPwRows);
+                float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; q4++) {
+                    uint32_t x[32];
+                    tc::ld32(tl + 128u * buf + 32 * q4, x);
+                    tc::wait_ld();
+                    if (q4 == 3) {  // all scores of the buffer are in registers
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&s_empty[buf]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float4 m = *reinterpret_cast<const float4 *>(nl + 32 * q4 + 4 * i);
+                        float2 u = ffma2(make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
+                                         sl2, make_float2(m.x, m.y));
+                        float2 v = ffma2(make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])),
+                                         sl2, make_float2(m.z, m.w));
+                        if (masked) {
+                            const int c = 32 * q4 + 4 * i;
+                            u.x = c >= c0 && c < c1 ? u.x : -INFINITY;
+                            u.y = c + 1 >= c0 && c + 1 < c1 ? u.y : -INFINITY;
+                            v.x = c + 2 >= c0 && c + 2 < c1 ? v.x : -INFINITY;
+                            v.y = c + 3 >= c0 && c + 3 < c1 ? v.y : -INFINITY;
+                        }
+                        a0 = fadd2(a0, make_float2(fast_exp2(u.x), fast_exp2(u.y)));
+                        a1 = fadd2(a1, make_float2(fast_exp2(v.x), fast_exp2(v.y)));
+                    }
+                }
+                sum += (a0.x + a0.y) + (a1.x + a1.y);
+            }
+            if (!ok)
+                break;
+            // ---- the item's sums: with one tile the group that had it writes, else
+            // the second group hands its part to the first
+            const bool both = it.tiles > 1;
+            if (both) {
+                // warp w to warp w - 4, which has the same tokens
+                const int x = (parts & 1) * 4 + (warp & 3);
+                float *pt = part + (parts & 1) * kPwTokens + r;
+                if (grp == 1) {
+                    ok = __all_sync(FULL, mbar_wait(&part_empty[x], ((parts >> 1) & 1) ^ 1));
+                    if (!ok)
+                        break;
+                    *pt = sum;
+                } else {
+                    ok = __all_sync(FULL, mbar_wait(&part_full[x], (parts >> 1) & 1));
+                    if (!ok)
+                        break;
+                    sum += *pt;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(grp == 1 ? &part_full[x] : &part_empty[x]);
+                parts++;
+            }
+            if ((both ? grp == 0 : j0 == 0) && t < it.k_len && blk >= 0 && blk < p.NB) {
+                float *dst = P.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs;
+                if (t >= base)
+                    *dst = sum;
+                else
+                    atomicAdd(dst, sum);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&item_free[n % kPwItems]);
+            gq += it.tiles;
+        }
+        if (!ok && lane == 0)
+            flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
     }
-    if (blk >= 0) {
-        float *dst = weights + ((size_t)blk * p.Hkv + h) * p.bs + off;
-        if (t >= base)
-            *dst = w;
-        else
-            atomicAdd(dst, w);
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kPwMmaWarp) {
+        tc::fence_after();
+        tc::dealloc(tmem, 512);
     }
 }
 
-cudaError_t launch_prompt_weights(int D, const PrefillParams &p, const void *k_cache, float *weights,
-                                  int window, cudaStream_t stream)
+template <int D>
+static const void *prompt_weights_fn(int G)
 {
+    switch (G) {
+    case 1: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 1>);
+    case 2: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 2>);
+    case 4: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 4>);
+    case 8: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 8>);
+    default: return nullptr;
+    }
+}
+
+const void *prompt_weights_kernel_fn(int D, int G)
+{
+    return D == 128 ? prompt_weights_fn<128>(G) : prompt_weights_fn<64>(G);
+}
+
+size_t prompt_weights_smem_bytes(int D) { return pw_smem_layout(D).total; }
+
+cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                  const PrefillParams &p, float *weights, int window, int sms,
+                                  cudaStream_t stream)
+{
+    PwParams P;
+    P.f = p;
+    P.weights = weights;
+    P.window = window;
+    // no more CTAs than items there can be
+    const long long tiles = ((long long)p.MBS * p.bs + kPwTokens - 1) / kPwTokens;
+    const long long most = tiles * p.Hkv * p.B;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(((long long)p.MBS * p.bs + kPwTokens - 1) / kPwTokens),
-                       (unsigned)p.Hkv, (unsigned)p.B);
-    cfg.blockDim = dim3(kPwTokens);
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(kPwThreads);
+    cfg.dynamicSmemBytes = pw_smem_layout(D).total;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const uint16_t *k = static_cast<const uint16_t *>(k_cache);
-    return D == 128 ? cudaLaunchKernelEx(&cfg, prompt_weights_kernel<128>, p, k, weights, window)
-                    : cudaLaunchKernelEx(&cfg, prompt_weights_kernel<64>, p, k, weights, window);
+#define PKV_PW(DD, GG) \
+    if (D == DD && G == GG) \
+        return cudaLaunchKernelEx(&cfg, prompt_weights_kernel<DD, GG>, *tmq, *tmk, P);
+    PKV_PW(64, 1) PKV_PW(64, 2) PKV_PW(64, 4) PKV_PW(64, 8)
+    PKV_PW(128, 1) PKV_PW(128, 2) PKV_PW(128, 4) PKV_PW(128, 8)
+#undef PKV_PW
+    return cudaErrorInvalidValue;
 }
 
 } // namespace pkv

@@ -63,7 +63,7 @@ def test_workspace_sizes(lib):
     (dict(D=96), UNSUPPORTED, b"head_dim"),
     (dict(bs=24), UNSUPPORTED, b"block_size"),
     (dict(scale=float("inf")), INVALID, b"scale"),
-    (dict(Hq=70000, Hkv=70000), UNSUPPORTED, b"65535"),
+    (dict(Hq=1 << 20, Hkv=1 << 20, B=2048), UNSUPPORTED, b"2^31"),
 ])
 def test_prefill_weights_refusals(lib, kw, status, text):
     assert prefill(lib, **kw) == status

@@ -158,6 +158,7 @@ struct DeviceState {
     bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
     bool pf_smem_set[2][9] = {};     // prefill: [D == 128][G]
     bool pw_smem_set[2][9] = {};     // its weights kernel: [D == 128][G]
+    bool evict_smem_set = false;
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -962,11 +963,30 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
     p.ws_dst = reinterpret_cast<int32_t *>(ws);
     ws += pkv::align_up((size_t)B * p.keep * sizeof(int32_t), 256);
     p.ws_src = reinterpret_cast<int32_t *>(ws);
-    // whole rows per CTA where the (sequence, KV head) pairs fill the GPU, else
-    // slices of them, down to one 32-byte sector
-    p.slices = 1;
-    while (p.slices < p.units && (long long)p.slices * B * Hkv < 4LL * st->sms)
+    p.block = pkv::fast_div((uint32_t)bs);
+    const long long pairs = (long long)B * Hkv;
+    // move: K and V rows by different CTAs, and slices of rows, down to 64
+    // bytes, until the (sequence, KV head) pairs fill the GPU
+    p.slices = 2;
+    while (4 * p.slices < 2 * p.units && p.slices * pairs < 8LL * st->sms)
         p.slices *= 2;
+    // selection: clusters where few pairs have long contexts
+    p.cluster = 1;
+    while (p.cluster < 8 && p.cluster * pairs < 2LL * st->sms && ctx / p.cluster > 2048)
+        p.cluster *= 2;
+    const long long seg = ((ctx + p.cluster - 1) / p.cluster + 3) / 4 * 4;
+    p.cap = (int)(seg < pkv::kSelCapMax ? seg : pkv::kSelCapMax);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!st->evict_smem_set) {
+            cudaError_t e = cudaFuncSetAttribute(pkv::evict_select_kernel_fn(),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)pkv::evict_select_smem_bytes(pkv::kSelCapMax));
+            if (e != cudaSuccess)
+                return fail(PKV_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            st->evict_smem_set = true;
+        }
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = pkv::launch_evict_select(p, s);
     if (e == cudaSuccess)

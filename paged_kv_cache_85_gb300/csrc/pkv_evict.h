@@ -8,6 +8,20 @@
 
 namespace pkv {
 
+// Division of n < 2^31 by a fixed d >= 1 as a multiplication by ceil-like
+// 2^32 (2^l - d) / d + 1 and a shift, with 2^l >= d (Granlund and Montgomery's
+// round-up method: exact for every 32-bit n; n < 2^31 keeps the sum in range).
+struct FastDiv {
+    uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d)
+{
+    uint32_t l = 0;
+    while ((1ull << l) < d)
+        l++;
+    return {(uint32_t)((((1ull << l) - d) << 32) / d + 1), l, d};
+}
+
 struct EvictParams {
     uint4 *k_cache, *v_cache;     // [NB, bs, Hkv, D], D elements = 16 * units bytes
     float *weights;               // [NB, Hkv, bs]
@@ -22,9 +36,15 @@ struct EvictParams {
     int units;                    // 16-byte units of one head's row (D * element bytes / 16)
     int budget, recent;
     int keep;                     // min(budget, MBS * bs): tokens of a trimmed context at most
-    int slices;                   // CTAs per (sequence, KV head) in the move, each a run of units
+    int slices;                   // CTAs per (sequence, KV head) that move rows, each a run of units
+    int cluster;                  // CTAs per (sequence, KV head) in the selection: 1, 2, 4 or 8
+    int cap;                      // keys each of them holds in shared memory (a multiple of 4)
+    FastDiv block;                // division by bs
 };
 
+constexpr int kSelCapMax = 12288;  // keys per CTA of the selection at most: three CTAs per SM fit
+size_t evict_select_smem_bytes(int cap);
+const void *evict_select_kernel_fn();
 cudaError_t launch_evict_select(const EvictParams &p, cudaStream_t stream);
 cudaError_t launch_evict_move(const EvictParams &p, cudaStream_t stream);
 

@@ -373,19 +373,32 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (t < it.k_len)
                 blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
             const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G;
+            // log-sum-exps of query tile j, negated, four per lane; -inf (weight 0)
+            // past the sequence.  Loaded one of the group's tiles ahead.
+            float ahead[4];
+            auto load_lse = [&](int j) {
+                const int i_first = it.i0 + j * TPC;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int c = lane + 32 * i;
+                    ahead[i] = j < it.tiles && i_first + c / G < it.q_len
+                                   ? -__ldg(lse + (size_t)i_first * G + c)
+                                   : -INFINITY;
+                }
+            };
+            load_lse(j0);
             float sum = 0.f;
             for (int j = j0; j < it.tiles; j += 2) {
                 const int g = gq + j, buf = g % kPwSBufs;
                 const int i_first = it.i0 + j * TPC;
-                // the tile's log-sum-exps, a copy per warp; +inf (weight 0) past the sequence
+                // the tile's log-sum-exps, a copy per warp
                 float *nl = nlse + (seen & 1) * kPwRows;
                 seen++;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int c = lane + 32 * i;
-                    nl[c] = i_first + c / G < it.q_len ? -__ldg(lse + (size_t)i_first * G + c) : -INFINITY;
-                }
+                for (int i = 0; i < 4; i++)
+                    nl[lane + 32 * i] = ahead[i];
                 __syncwarp();
+                load_lse(j + 2);
                 ok = __all_sync(FULL, mbar_wait(&s_full[buf], (g / kPwSBufs) & 1));
                 if (!ok)
                     break;

@@ -897,7 +897,6 @@ size_t pkv_evict_workspace_bytes(int B, int Hkv, int MBS, int bs, int budget)
     const long long ctx = (long long)MBS * bs;
     const size_t keep = (size_t)(budget < ctx ? budget : ctx);
     return pkv::align_up((size_t)B * Hkv * sizeof(int2), 256) +
-           pkv::align_up((size_t)B * keep * sizeof(int32_t), 256) +
            (size_t)B * Hkv * keep * sizeof(int32_t);
 }
 
@@ -960,8 +959,6 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.ws_moved = reinterpret_cast<int2 *>(ws);
     ws += pkv::align_up((size_t)B * Hkv * sizeof(int2), 256);
-    p.ws_dst = reinterpret_cast<int32_t *>(ws);
-    ws += pkv::align_up((size_t)B * p.keep * sizeof(int32_t), 256);
     p.ws_src = reinterpret_cast<int32_t *>(ws);
     p.block = pkv::fast_div((uint32_t)bs);
     const long long pairs = (long long)B * Hkv;
@@ -974,7 +971,7 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
     p.cluster = 1;
     while (p.cluster < 8 && p.cluster * pairs < 2LL * st->sms && ctx / p.cluster > 2048)
         p.cluster *= 2;
-    const long long seg = ((ctx + p.cluster - 1) / p.cluster + 3) / 4 * 4;
+    const long long seg = ((ctx + p.cluster - 1) / p.cluster + 7) / 8 * 8;
     p.cap = (int)(seg < pkv::kSelCapMax ? seg : pkv::kSelCapMax);
     {
         std::lock_guard<std::mutex> lk(g_mu);

@@ -60,10 +60,11 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct SelShared {
+struct __align__(16) SelShared {
     uint32_t hist[3][kSelBins];
     uint32_t scan[2][kSelWarps];
-    uint32_t over, border;  // this CTA's tokens over the border key and on it
+    uint32_t counts[8], borders[8];  // per CTA of the cluster: tokens over the border key, on it
+    uint32_t mine, mine_border;      // this CTA's
     uint32_t prefix, left, whole;
     int first, bad;
 };
@@ -83,6 +84,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         else
             __syncthreads();
     };
+    for (int i = tid; i < 3 * kSelBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(&S.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+        S.bad = 0;
+        S.first = p.budget - p.recent;
+        S.mine = S.mine_border = 0;
+    }
     grid_dependency_wait();
 
     const int n = p.context_lens[b];
@@ -100,44 +108,65 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     const int32_t *table = p.block_tables + (size_t)b * p.MBS;
     const int old = n - p.recent;         // tokens the weights decide on
     const int want = p.budget - p.recent; // of them, how many stay (< old)
-    // this CTA's tokens: [t0, t1), in quads of four (a quad never leaves its block)
-    const int seg = ((n + C - 1) / C + 3) & ~3;
-    const int t0 = min(n, rank * seg), t1 = min(n, t0 + seg);
-    const int quads = (t1 - t0 + 3) / 4;
-    auto load = [&](int q, bool &bad) -> uint4 {
-        const int t = t0 + 4 * q, j = divide(t, p.block);
+    // this CTA's part of them: [t0, t1), in runs of eight, which never leave
+    // their block
+    const int seg = ((old + C - 1) / C + 7) & ~7;
+    const int t0 = min(old, rank * seg), t1 = min(old, t0 + seg);
+    const int runs = (t1 - t0 + 7) / 8;
+    // the keys of a run; 0, below every weight's, past `old`
+    auto load = [&](int q, uint4 &k0, uint4 &k1) -> bool {
+        const int t = t0 + 8 * q, j = divide(t, p.block);
         const int blk = __ldg(table + j);
-        if (blk < 0 || blk >= p.NB) {
-            bad = true;
-            return make_uint4(0, 0, 0, 0);
-        }
-        const float4 w = *reinterpret_cast<const float4 *>(
+        k0 = k1 = make_uint4(0, 0, 0, 0);
+        if (blk < 0 || blk >= p.NB)
+            return false;
+        const float4 *w = reinterpret_cast<const float4 *>(
             p.weights + ((size_t)blk * p.Hkv + h) * p.bs + (t - j * p.bs));
-        return make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
+        const float4 a = w[0], c = w[1];
+        k0 = make_uint4(weight_key(a.x), weight_key(a.y), weight_key(a.z), weight_key(a.w));
+        k1 = make_uint4(weight_key(c.x), weight_key(c.y), weight_key(c.z), weight_key(c.w));
+        if (t + 8 > old) {
+            uint32_t *u = reinterpret_cast<uint32_t *>(&k0), *v = reinterpret_cast<uint32_t *>(&k1);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                u[i] = t + i < old ? u[i] : 0u;
+                v[i] = t + 4 + i < old ? v[i] : 0u;
+            }
+        }
+        return true;
     };
-    // keys of a quad: from shared memory, or again from the table where it is full
-    auto quad = [&](int q) -> uint4 {
-        bool bad = false;
-        return 4 * q < p.cap ? keys[q] : load(q, bad);
+    // from shared memory, or again from the table where that is full
+    auto run = [&](int q, uint4 &k0, uint4 &k1) {
+        if (8 * q < p.cap) {
+            k0 = keys[2 * q];
+            k1 = keys[2 * q + 1];
+        } else {
+            load(q, k0, k1);
+        }
     };
+    __syncthreads();  // the histograms are clear
     {
-        if (tid == 0) {
-            S.bad = 0;
-            S.first = p.budget;
-            S.over = S.border = 0;
-        }
         bool bad = false;
-#pragma unroll 4
-        for (int q = tid; q < quads; q += kSelThreads) {
-            const uint4 k = load(q, bad);
-            if (4 * q < p.cap)
-                keys[q] = k;
+#pragma unroll 2
+        for (int q = tid; q < runs; q += kSelThreads) {
+            uint4 k0, k1;
+            bad |= !load(q, k0, k1);
+            if (8 * q < p.cap) {
+                keys[2 * q] = k0;
+                keys[2 * q + 1] = k1;
+            }
+            const uint32_t u[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                atomicAdd(&S.hist[0][u[i] >> 21], 1u);
         }
-        __syncthreads();
+        // the recent tokens' blocks
+        for (int j = old / p.bs + tid; j <= (n - 1) / p.bs; j += kSelThreads) {
+            const int blk = __ldg(table + j);
+            bad |= blk < 0 || blk >= p.NB;
+        }
         if (bad)
             S.bad = 1;
-        for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
-            (&S.hist[0][0])[i] = 0;
         sync_all();
         int any = S.bad;
         if (C > 1) {
@@ -166,17 +195,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         for (int pass = 0; pass < 3; pass++) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t bins = pass == 2 ? 1024u : 2048u;
-            const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
             uint32_t *hist = S.hist[pass];
-            for (int q = tid; q < quads; q += kSelThreads) {
-                const uint4 k = quad(q);
-                const uint32_t u[4] = {k.x, k.y, k.z, k.w};
+            if (pass > 0) {  // the first one was counted while the weights came in
+                for (int q = tid; q < runs; q += kSelThreads) {
+                    uint4 k0, k1;
+                    run(q, k0, k1);
+                    const uint32_t u[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (t0 + 4 * q + i < min(old, t1) && (u[i] & above) == (prefix & above))
-                        atomicAdd(&hist[(u[i] >> shift) & (bins - 1)], 1u);
+                    for (int i = 0; i < 8; i++)
+                        if ((u[i] & mask) == prefix)
+                            atomicAdd(&hist[(u[i] >> shift) & (bins - 1)], 1u);
+                }
+                __syncthreads();
             }
-            __syncthreads();
             if (C > 1) {
                 if (rank > 0) {
                     uint32_t *sum = cluster.map_shared_rank(hist, 0);
@@ -189,38 +220,49 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             // thread i owns `per` bins counted from the top; the bin in which the
             // running count from the top reaches `left` holds the border key (in a
             // cluster the first CTA finds it and tells the others)
-            const int per = (int)bins / kSelThreads;  // 8 or 4
-            uint32_t own[kSelBins / kSelThreads], sum = 0;
+            if (rank == 0) {
+                constexpr int kMost = kSelBins / kSelThreads;
+                const int per = (int)bins / kSelThreads;  // 8 or 4
+                uint32_t own[kMost], sum = 0;  // ascending bins
 #pragma unroll
-            for (int i = 0; i < kSelBins / kSelThreads; i++) {
-                own[i] = i < per ? hist[bins - 1 - (uint32_t)(tid * per + i)] : 0u;
-                sum += own[i];
-            }
-            uint32_t incl = sum;
+                for (int i = 0; i < kMost; i += 4) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (i < per)
+                        x = *reinterpret_cast<const uint4 *>(hist + bins - per * (tid + 1) + i);
+                    own[i] = x.x;
+                    own[i + 1] = x.y;
+                    own[i + 2] = x.z;
+                    own[i + 3] = x.w;
+                    sum += x.x + x.y + x.z + x.w;
+                }
+                uint32_t incl = sum;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t y = __shfl_up_sync(FULL, incl, off);
-                if (lane >= off)
-                    incl += y;
-            }
-            if (lane == 31)
-                S.scan[0][warp] = incl;
-            __syncthreads();
-            uint32_t before = incl - sum;
-            for (int w = 0; w < warp; w++)
-                before += S.scan[0][w];
-            if (rank == 0 && before < left && left <= before + sum) {
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t y = __shfl_up_sync(FULL, incl, off);
+                    if (lane >= off)
+                        incl += y;
+                }
+                if (lane == 31)
+                    S.scan[0][warp] = incl;
+                __syncthreads();
+                uint32_t before = incl - sum;
 #pragma unroll
-                for (int i = 0; i < kSelBins / kSelThreads; i++) {
-                    if (before < left && left <= before + own[i]) {
-                        for (int c = 0; c < C; c++) {
-                            SelShared &to = C > 1 ? *cluster.map_shared_rank(&S, c) : S;
-                            to.prefix = prefix | ((bins - 1 - (uint32_t)(tid * per + i)) << shift);
-                            to.left = left - before;
-                            to.whole = left - before == own[i];
+                for (int w = 0; w < kSelWarps; w++)
+                    before += w < warp ? S.scan[0][w] : 0u;
+                if (before < left && left <= before + sum) {
+#pragma unroll
+                    for (int i = kMost - 1; i >= 0; i--) {
+                        if (before < left && left <= before + own[i]) {
+                            const uint32_t bin = bins - (uint32_t)(per * (tid + 1)) + (uint32_t)i;
+                            for (int c = 0; c < C; c++) {
+                                SelShared &to = C > 1 ? *cluster.map_shared_rank(&S, c) : S;
+                                to.prefix = prefix | (bin << shift);
+                                to.left = left - before;
+                                to.whole = left - before == own[i];
+                            }
                         }
+                        before += own[i];
                     }
-                    before += own[i];
                 }
             }
             sync_all();
@@ -235,127 +277,123 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
 
     // ---- rank the tokens that stay, in token order, and record their slots
-    auto classes = [&](int q, const uint4 &k, uint32_t &over, uint32_t &border) {  // 4-bit masks
-        const uint32_t u[4] = {k.x, k.y, k.z, k.w};
+    auto classes = [&](int q, uint32_t &over, uint32_t &border) {  // a bit per token
+        uint4 k0, k1;
+        run(q, k0, k1);
+        const uint32_t u[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
         over = border = 0;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int t = t0 + 4 * q + i;
-            if (t < t1) {
-                over |= (t >= old || (want > 0 && (u[i] & mask) > prefix) ? 1u : 0u) << i;
-                border |= (t < old && want > 0 && (u[i] & mask) == prefix ? 1u : 0u) << i;
-            }
+        for (int i = 0; i < 8; i++) {
+            over |= (u[i] & mask) > prefix ? 1u << i : 0u;
+            border |= (u[i] & mask) == prefix ? 1u << i : 0u;
         }
     };
-    uint32_t o_before = 0, b_before = 0;  // in the CTAs before this one
-    if (C > 1) {
-        uint32_t o = 0, e = 0;
-        for (int q = tid; q < quads; q += kSelThreads) {
-            uint32_t mo, mb;
-            classes(q, quad(q), mo, mb);
-            o += __popc(mo);
-            e += __popc(mb);
+    int32_t *src = p.ws_src + ((size_t)b * p.Hkv + h) * p.keep;
+    int first = want;  // first token that moves (the recent ones all do)
+    if (want > 0) {
+        uint32_t o_before = 0, b_before = 0;  // in the CTAs before this one
+        if (C > 1) {
+            uint32_t o = 0, e = 0;
+            for (int q = tid; q < runs; q += kSelThreads) {
+                uint32_t mo, mb;
+                classes(q, mo, mb);
+                o += __popc(mo);
+                e += __popc(mb);
+            }
+            o = __reduce_add_sync(FULL, o);
+            e = __reduce_add_sync(FULL, e);
+            if (lane == 0) {
+                atomicAdd(&S.mine, o);
+                atomicAdd(&S.mine_border, e);
+            }
+            __syncthreads();
+            if (tid < C) {
+                SelShared &to = *cluster.map_shared_rank(&S, tid);
+                to.counts[rank] = S.mine;
+                to.borders[rank] = S.mine_border;
+            }
+            cluster.sync();
+            for (int c = 0; c < rank; c++) {
+                o_before += S.counts[c];
+                b_before += S.borders[c];
+            }
         }
-        o = __reduce_add_sync(FULL, o);
-        e = __reduce_add_sync(FULL, e);
-        if (lane == 0) {
-            atomicAdd(&S.over, o);
-            atomicAdd(&S.border, e);
-        }
-        cluster.sync();
-        for (int c = 0; c < rank; c++) {
-            o_before += *cluster.map_shared_rank(&S.over, c);
-            b_before += *cluster.map_shared_rank(&S.border, c);
+        for (int q0 = 0, buf = 0; q0 < runs; q0 += kSelThreads, buf ^= 1) {
+            const int q = q0 + tid;
+            uint32_t mo = 0, mb = 0;
+            if (q < runs)
+                classes(q, mo, mb);
+            // both counts in one word: a step holds 2048 tokens
+            const uint32_t own = __popc(mo) | (__popc(mb) << 16);
+            uint32_t incl = own;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t y = __shfl_up_sync(FULL, incl, off);
+                if (lane >= off)
+                    incl += y;
+            }
+            if (lane == 31)
+                S.scan[buf][warp] = incl;
+            __syncthreads();
+            uint32_t before = incl - own, all = 0;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; w++) {
+                const uint32_t x = S.scan[buf][w];
+                before += w < warp ? x : 0u;
+                all += x;
+            }
+            if (mo | mb) {
+                uint32_t o = o_before + (before & 0xffffu), e = b_before + (before >> 16);
+                const int t = t0 + 8 * q, j = divide(t, p.block);
+                const int slot = __ldg(table + j) * p.bs + (t - j * p.bs);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    // of the border tokens the first `left` stay
+                    const bool over = (mo >> i) & 1u, border = (mb >> i) & 1u;
+                    if (over || (border && e < left)) {
+                        const int at = (int)(o + min(e, left));
+                        src[at] = slot + i;
+                        if (at != t + i)
+                            first = min(first, at);
+                    }
+                    o += over;
+                    e += border;
+                }
+            }
+            o_before += all & 0xffffu;
+            b_before += all >> 16;
         }
     }
-    int32_t *src = p.ws_src + ((size_t)b * p.Hkv + h) * p.keep;
-    int32_t *dst = p.ws_dst + (size_t)b * p.keep;
-    int first = p.budget;  // first token that moves
-    for (int q0 = 0; q0 < quads; q0 += kSelThreads) {
-        const int q = q0 + tid;
-        uint32_t mo = 0, mb = 0;
-        if (q < quads)
-            classes(q, quad(q), mo, mb);
-        const uint32_t no = __popc(mo), nb = __popc(mb);
-        uint32_t io = no, ib = nb;  // inclusive scans over the warp
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t yo = __shfl_up_sync(FULL, io, off), yb = __shfl_up_sync(FULL, ib, off);
-            if (lane >= off) {
-                io += yo;
-                ib += yb;
-            }
-        }
-        if (lane == 31) {
-            S.scan[0][warp] = io;
-            S.scan[1][warp] = ib;
-        }
-        __syncthreads();
-        uint32_t o = o_before + io - no, e = b_before + ib - nb;
-#pragma unroll
-        for (int w = 0; w < kSelWarps; w++) {
-            const uint32_t co = S.scan[0][w], cb = S.scan[1][w];
-            if (w < warp) {
-                o += co;
-                e += cb;
-            }
-            o_before += co;
-            b_before += cb;
-        }
-        const int t = t0 + 4 * q;
-        const bool to_dst = h == 0 && t < p.budget && q < quads;
-        if ((mo | mb) || to_dst) {
-            const int j = divide(t, p.block);
-            const int slot = __ldg(table + j) * p.bs + (t - j * p.bs);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                // of the border tokens the first `left` stay
-                const bool over = (mo >> i) & 1u, border = (mb >> i) & 1u;
-                if (over || (border && e < left)) {
-                    const int at = (int)(o + min(e, left));
-                    src[at] = slot + i;
-                    if (at != t + i)
-                        first = min(first, at);
-                }
-                o += over;
-                e += border;
-                if (to_dst && t + i < p.budget)
-                    dst[t + i] = slot + i;
-            }
-        }
-        __syncthreads();  // scan[] is free again
+    for (int i = rank * kSelThreads + tid; i < p.recent; i += C * kSelThreads) {
+        const int t = old + i, j = divide(t, p.block);
+        src[want + i] = __ldg(table + j) * p.bs + (t - j * p.bs);
     }
     first = __reduce_min_sync(FULL, first);
     if (lane == 0)
-        atomicMin(&S.first, first);
-    sync_all();
-    if (lead) {
-        first = S.first;
-        for (int c = 1; c < C; c++)
-            first = min(first, *cluster.map_shared_rank(&S.first, c));
-        *moved = make_int2(first, p.budget);
-    }
-    if (C > 1)
-        cluster.sync();  // the other CTAs' shared memory stays until it is read
+        atomicMin(C > 1 ? cluster.map_shared_rank(&S.first, 0) : &S.first, first);
+    sync_all();  // also: no CTA of a cluster leaves before the others are done with it
+    if (lead)
+        *moved = make_int2(S.first, p.budget);
 }
 
 // Copies tokens [first, end) of one (sequence, KV head): `lanes` threads take a
-// token, thread i of them its i-th unit; get reads a token's source, put writes
-// it.  Double-buffered tiles, indexes one tile further ahead.
-template <typename T, typename Get, typename Put>
+// token, thread i of them its i-th unit; src lists the slots they come from,
+// slot_of gives a position's slot; get reads a slot, put writes it.
+// Double-buffered tiles, sources looked up one tile further ahead.
+template <typename T, typename Slot, typename Get, typename Put>
 __device__ __forceinline__ void move_tiles(int first, int end, int lanes, const int32_t *src,
-                                           const int32_t *dst, Get get, Put put)
+                                           Slot slot_of, Get get, Put put)
 {
     const int rows = kMoveThreads / lanes;  // tokens per step
     const int tile = rows * kMoveDepth;
     const int r = (int)threadIdx.x / lanes;
     int si[kMoveDepth], di[kMoveDepth];
     T x[2][kMoveDepth];
-    auto index = [&](int j0, const int32_t *list, int (&to)[kMoveDepth]) {
+    auto sources = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < kMoveDepth; i++) {
             const int j = j0 + r + i * rows;
-            to[i] = j < end ? __ldg(list + j) : -1;
+            si[i] = j < end ? __ldg(src + j) : -1;
         }
     };
     auto read = [&](T (&to)[kMoveDepth]) {
@@ -364,18 +402,22 @@ __device__ __forceinline__ void move_tiles(int first, int end, int lanes, const 
             if (si[i] >= 0)
                 to[i] = get(si[i]);
     };
-    index(first, src, si);
+    sources(first);
     read(x[0]);
-    index(first + tile, src, si);
+    sources(first + tile);
     for (int j0 = first; j0 < end; j0 += 2 * tile) {
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             const int at = j0 + u * tile;
             if (at < end) {  // the same for the whole CTA
-                index(at, dst, di);
-                read(x[u ^ 1]);                  // tile at + tile: its sources lie past this tile
-                index(at + 2 * tile, src, si);
-                __syncthreads();                 // this tile is in every thread's registers
+#pragma unroll
+                for (int i = 0; i < kMoveDepth; i++) {
+                    const int j = at + r + i * rows;
+                    di[i] = j < end ? slot_of(j) : -1;
+                }
+                read(x[u ^ 1]);          // tile at + tile: its sources lie past this tile
+                sources(at + 2 * tile);
+                __syncthreads();         // this tile is in every thread's registers
 #pragma unroll
                 for (int i = 0; i < kMoveDepth; i++)
                     if (di[i] >= 0)
@@ -401,14 +443,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     if (moved.x >= moved.y)
         return;
     const int32_t *src = p.ws_src + ((size_t)b * p.Hkv + h) * p.keep;
-    const int32_t *dst = p.ws_dst + (size_t)b * p.keep;
+    const int32_t *table = p.block_tables + (size_t)b * p.MBS;
+    auto slot_of = [&](int t) {
+        const int j = divide(t, p.block);
+        return __ldg(table + j) * p.bs + (t - j * p.bs);
+    };
     if (slice == p.slices) {  // the weights, fp32 [NB, Hkv, bs]
         auto at = [&](int slot) {
             const int blk = divide(slot, p.block);
             return p.weights + ((size_t)blk * p.Hkv + h) * p.bs + (slot - blk * p.bs);
         };
         move_tiles<float>(
-            moved.x, moved.y, 1, src, dst, [&](int slot) { return *at(slot); },
+            moved.x, moved.y, 1, src, slot_of, [&](int slot) { return *at(slot); },
             [&](int slot, float w) { *at(slot) = w; });
         return;
     }
@@ -418,7 +464,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     uint4 *base = (u0 < p.units ? p.k_cache : p.v_cache) + (size_t)h * p.units + u0 % p.units;
     const size_t row = (size_t)p.Hkv * p.units;
     move_tiles<uint4>(
-        moved.x, moved.y, per, src, dst, [&](int slot) { return base[(size_t)slot * row]; },
+        moved.x, moved.y, per, src, slot_of, [&](int slot) { return base[(size_t)slot * row]; },
         [&](int slot, const uint4 &x) { base[(size_t)slot * row] = x; });
 }
 

@@ -29,7 +29,6 @@ struct EvictParams {
     const int32_t *context_lens;  // [B]
     int32_t *out_lens;            // [B], may be context_lens
     int32_t *ws_src;              // [B, Hkv, keep] slot that token j of the trimmed context comes from
-    int32_t *ws_dst;              // [B, keep] slot of token j
     int2 *ws_moved;               // [B, Hkv] (first, end): tokens j in [first, end) move
     int32_t *err_flag;            // nullable
     int B, Hkv, MBS, bs, NB;
@@ -38,7 +37,7 @@ struct EvictParams {
     int keep;                     // min(budget, MBS * bs): tokens of a trimmed context at most
     int slices;                   // CTAs per (sequence, KV head) that move rows, each a run of units
     int cluster;                  // CTAs per (sequence, KV head) in the selection: 1, 2, 4 or 8
-    int cap;                      // keys each of them holds in shared memory (a multiple of 4)
+    int cap;                      // keys each of them holds in shared memory (a multiple of 8)
     FastDiv block;                // division by bs
 };
 

@@ -43,8 +43,8 @@ def test_workspace_sizes(lib):
     assert lib.pkv_decode_weights_workspace_bytes(4, 6, 4, 64, 19, 16, 0) == 0
     assert lib.pkv_prefill_weights_workspace_bytes(100, 4) == up(1600)
     assert lib.pkv_prefill_weights_workspace_bytes(0, 4) == 0
-    # (first, end) pairs, the kept tokens' destinations and, per KV head, their sources
-    assert lib.pkv_evict_workspace_bytes(3, 2, 4, 16, 20) >= 3 * 2 * 8 + 3 * 20 * 4 + 3 * 2 * 20 * 4
+    # per (sequence, KV head) the range that moves, and where the kept tokens come from
+    assert lib.pkv_evict_workspace_bytes(3, 2, 4, 16, 20) == up(3 * 2 * 8) + 3 * 2 * 20 * 4
     # a budget above what the tables can name needs no more than that
     assert lib.pkv_evict_workspace_bytes(3, 2, 4, 16, 1 << 30) == lib.pkv_evict_workspace_bytes(3, 2, 4, 16, 64)
     assert lib.pkv_evict_workspace_bytes(0, 2, 4, 16, 20) == 0

@@ -967,6 +967,11 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
     p.slices = 2;
     while (4 * p.slices < 2 * p.units && p.slices * pairs < 8LL * st->sms)
         p.slices *= 2;
+    // with few CTAs larger ones, which have more loads in flight (whole call, 64
+    // sequences to 1024 tokens: 91 -> 87 us; 8 x 32768 to 4096: 77 -> 69 us); with
+    // many of short runs the smaller tiles end with less waste (256 sequences,
+    // E4M3, to 511 tokens: 96 us against 101 us)
+    p.move_threads = p.slices * pairs < 16LL * st->sms ? 256 : 128;
     // selection: clusters where few pairs have long contexts
     p.cluster = 1;
     while (p.cluster < 8 && p.cluster * pairs < 2LL * st->sms && ctx / p.cluster > 2048)

@@ -42,7 +42,7 @@ namespace pkv {
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 256;  // at most
 constexpr int kMoveDepth = 4;  // 16-byte loads per thread and tile; two tiles in flight
 
 __device__ __forceinline__ int divide(int n, FastDiv f)
@@ -384,7 +384,7 @@ template <typename T, typename Slot, typename Get, typename Put>
 __device__ __forceinline__ void move_tiles(int first, int end, int lanes, const int32_t *src,
                                            Slot slot_of, Get get, Put put)
 {
-    const int rows = kMoveThreads / lanes;  // tokens per step
+    const int rows = (int)blockDim.x / lanes;  // tokens per step
     const int tile = rows * kMoveDepth;
     const int r = (int)threadIdx.x / lanes;
     int si[kMoveDepth], di[kMoveDepth];
@@ -500,7 +500,7 @@ cudaError_t launch_evict_move(const EvictParams &p, cudaStream_t stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)p.slices + 1, (unsigned)p.Hkv, (unsigned)p.B);
-    cfg.blockDim = dim3(kMoveThreads);
+    cfg.blockDim = dim3((unsigned)p.move_threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -36,6 +36,7 @@ struct EvictParams {
     int budget, recent;
     int keep;                     // min(budget, MBS * bs): tokens of a trimmed context at most
     int slices;                   // CTAs per (sequence, KV head) that move rows, each a run of units
+    int move_threads;             // threads of such a CTA: 128 or 256
     int cluster;                  // CTAs per (sequence, KV head) in the selection: 1, 2, 4 or 8
     int cap;                      // keys each of them holds in shared memory (a multiple of 8)
     FastDiv block;                // division by bs

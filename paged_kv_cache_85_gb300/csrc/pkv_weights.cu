@@ -9,10 +9,12 @@
 // added to weights[block, kv head, offset], or stored there for the step's
 // newest token, whose slot may hold what an earlier owner of the block left.
 //
-// One thread per token.  Every (token, KV head) gets exactly one addition per
-// call, so the sums do not depend on the order of the threads; they are
-// atomic because two sequences of a batch may share a prefix block (then
-// their two additions may come in either order).
+// One thread per four tokens of a box (16-byte loads of the scores and one
+// 16-byte addition to the weights, which lie next to each other in a block).
+// Every (token, KV head) gets exactly one addition per call, so the sums do not
+// depend on the order of the threads; they are atomic because two sequences of
+// a batch may share a prefix block (then their two additions may come in either
+// order).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 
@@ -24,36 +26,55 @@ template <int G, int BT>
 __global__ void __launch_bounds__(kAddThreads)
     add_weights_kernel(const DecodeParams p, float *__restrict__ weights)
 {
+    constexpr int kQuads = BT / 4;  // threads per box
     // scores, descriptors and log-sum-exps come from the kernels just before
     grid_dependency_wait();
     const int per_head = p.ws_hdr[kWsHeaderInts + p.B];  // boxes per KV head
-    const long long n = (long long)per_head * p.Hkv * BT;
+    const long long n = (long long)per_head * p.Hkv * kQuads;
     for (long long idx = (long long)blockIdx.x * kAddThreads + threadIdx.x; idx < n;
          idx += (long long)gridDim.x * kAddThreads) {
-        const int box = (int)(idx / BT), i = (int)(idx % BT);
+        const int box = (int)(idx / kQuads), i = (int)(idx % kQuads) * 4;
         const int4 m = p.ws_box[box];
+        float4 s[G];
+        const float *sc = p.ws_score + (size_t)box * G * BT + i;
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            s[g] = *reinterpret_cast<const float4 *>(sc + g * BT);
         const int nvalid = m.w & (kBoxNewest - 1);
         if (m.y < 0 || i >= nvalid)
             continue;
         const int h = box / per_head;
         const float *lse = p.ws_lse + (size_t)m.x * p.Hq + (size_t)h * G;
-        const float *sc = p.ws_score + (size_t)box * G * BT + i;
-        float w = 0.f;
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int g = 0; g < G; g++)
-            w += fast_exp2(sc[g * BT] - lse[g]);
+        for (int g = 0; g < G; g++) {
+            const float l = lse[g];
+            w.x += fast_exp2(s[g].x - l);
+            w.y += fast_exp2(s[g].y - l);
+            w.z += fast_exp2(s[g].z - l);
+            w.w += fast_exp2(s[g].w - l);
+        }
         float *dst = weights + ((size_t)m.y * p.Hkv + h) * p.bs + m.z + i;
-        if ((m.w & kBoxNewest) && i == nvalid - 1)
-            *dst = w;
-        else
-            atomicAdd(dst, w);
+        const bool newest = (m.w & kBoxNewest) != 0;
+        if (i + 4 <= nvalid - (newest ? 1 : 0)) {
+            atomicAdd(reinterpret_cast<float4 *>(dst), w);
+        } else {  // the context's last tokens: none past it, and the newest one is set
+            const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (newest && i + k == nvalid - 1)
+                    dst[k] = x[k];
+                else if (i + k < nvalid)
+                    atomicAdd(dst + k, x[k]);
+            }
+        }
     }
 }
 
 cudaError_t launch_add_weights(int G, int bt, const DecodeParams &p, float *weights, long long max_boxes,
                                int sms, cudaStream_t stream)
 {
-    const long long need = (max_boxes * bt + kAddThreads - 1) / kAddThreads;
+    const long long need = (max_boxes * (bt / 4) + kAddThreads - 1) / kAddThreads;
     const long long most = (long long)sms * (2048 / kAddThreads);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -353,8 +353,8 @@ pkv_status pkv_paged_attn_decode_noalloc(const void *q, const void *k_cache, con
  * score until its row's sum is known: 4 * Hq bytes per token of the B * MBS *
  * bs the tables can name (134 MB for 512 sequences of 4096 tokens and 16
  * query heads), of which a call touches the part that its contexts fill.
- * A context of length 0 records nothing.  Three kernels on `stream`: decode,
- * merge, and one that turns the scores into weights.
+ * A context of length 0 records nothing.  Two kernels on `stream`: decode, and
+ * one that merges split contexts and turns the scores into weights.
  */
 size_t pkv_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas);
 

@@ -583,18 +583,17 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
                                        plan.smem, s);
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_attn_decode launch: %s", cudaGetErrorString(e));
-    e = pkv::launch_merge(D, plan.G, p, s);
-    if (e != cudaSuccess)
-        return fail(PKV_ERR_CUDA, "merge launch: %s", cudaGetErrorString(e));
-    if (record) {
+    if (!record) {
+        e = pkv::launch_merge(D, plan.G, p, s);
+    } else {
         DeviceState *st = nullptr;
         if ((ps = device_state(&st)) != PKV_OK)
             return ps;
         const long long boxes = (long long)B * Hkv * (((long long)MBS * bs + plan.bt - 1) / plan.bt);
-        e = pkv::launch_add_weights(plan.G, plan.bt, p, weights, boxes, st->sms, s);
-        if (e != cudaSuccess)
-            return fail(PKV_ERR_CUDA, "paged_attn_decode_weights launch: %s", cudaGetErrorString(e));
+        e = pkv::launch_merge_and_add(D, plan.G, plan.bt, f8, p, weights, boxes, st->sms, s);
     }
+    if (e != cudaSuccess)
+        return fail(PKV_ERR_CUDA, "merge launch: %s", cudaGetErrorString(e));
     return PKV_OK;
 }
 

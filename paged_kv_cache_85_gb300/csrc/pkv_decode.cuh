@@ -41,8 +41,9 @@
 //    two workspace slots (first / last piece of its slice); a second kernel
 //    merges the partials of streams that straddle workers by log-sum-exp.
 //  * With WT (the calls that record attention weights) every box's scores
-//    (log2 domain) go to the workspace as [G][BT] floats with a descriptor of
-//    the box, and every finished (sequence, query head) leaves its log-sum-exp;
+//    (log2 domain) go to the workspace as [G][BT] floats (FP8: [BT][G], the
+//    order in which the fragments hold them) with a descriptor of the box, which
+//    the producer writes, and every finished (sequence, query head) leaves its log-sum-exp;
 //    pkv_weights.cu turns them into weights once all of those are known.  The
 //    scores are 4 G bytes per token and KV head beside 4 D (bf16) of K and V.
 //  * Masking selects out tokens at or past context_len (scores -> -inf and
@@ -62,7 +63,7 @@ constexpr int kLookahead = 4;  // boxes per worker whose block ids are loaded ah
 // Per-worker box descriptor of a stage, written by the producer.
 struct __align__(16) BoxMeta {
     int b, h, tok0, nvalid;
-    int flags, blk, off, box;  // off: tok0's offset in the block; box: position in the streams
+    int flags, blk, box, pad;  // box: position in the streams (with WT)
 };
 constexpr int kBoxValid = 1;     // the worker has a box in this stage
 constexpr int kBoxLoaded = 2;    // its K/V were copied (the block id was valid)
@@ -178,6 +179,11 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
     BoxMeta *meta = reinterpret_cast<BoxMeta *>(smem + L.meta);
     const int *pb = reinterpret_cast<const int *>(smem + L.pb);
     const int *len = reinterpret_cast<const int *>(smem + L.len);
+    // with WT the scores written meanwhile are read again by the next kernel:
+    // K and V, read once, make way for them in L2
+    uint64_t once = 0;
+    if constexpr (WT)
+        once = l2_evict_first();
 
     if (lane == 0) {
         prefetch_tensormap(tmk);
@@ -259,8 +265,10 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
             m.flags = flags;
             m.blk = blk;
             if constexpr (WT) {
-                m.off = tok0 % p.bs;
                 m.box = pos;
+                // for the weights kernel; a stream's last box ends in the step's new token
+                p.ws_box[pos] = make_int4(b, loaded ? blk : -1, tok0 % p.bs,
+                                          m.nvalid | (j == nb - 1 ? kBoxNewest : 0));
             }
             // advance both cursors
             next_box(pb, p.B, cb, ch, cj);
@@ -284,15 +292,26 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
                       p.q + ((size_t)b * p.Hq + (size_t)h * G) * D, G * D * 2, &full[stage]);
         if ((flags & kBoxLoaded) && F8) {
             uint8_t *kd = smem + L.kv + ((size_t)stage * 2 * NW + lane) * kBoxBytes;
-            tma_load_3d(kd, tmk, 0, h, row, &full[stage]);
-            tma_load_3d(kd + (size_t)NW * kBoxBytes, tmv, 0, h, row, &full[stage]);
+            if constexpr (WT) {
+                tma_load_3d(kd, tmk, 0, h, row, &full[stage], once);
+                tma_load_3d(kd + (size_t)NW * kBoxBytes, tmv, 0, h, row, &full[stage], once);
+            } else {
+                tma_load_3d(kd, tmk, 0, h, row, &full[stage]);
+                tma_load_3d(kd + (size_t)NW * kBoxBytes, tmv, 0, h, row, &full[stage]);
+            }
         } else if (flags & kBoxLoaded) {
             uint8_t *kd = smem + L.kv + ((size_t)stage * 2 * NW + lane) * kBoxBytes;
 #pragma unroll
             for (int half = 0; half < D / 64; half++) {
-                tma_load_4d(kd + half * kHalfBytes, tmk, 0, half, h, row, &full[stage]);
-                tma_load_4d(kd + (size_t)NW * kBoxBytes + half * kHalfBytes, tmv, 0, half, h, row,
-                            &full[stage]);
+                if constexpr (WT) {
+                    tma_load_4d(kd + half * kHalfBytes, tmk, 0, half, h, row, &full[stage], once);
+                    tma_load_4d(kd + (size_t)NW * kBoxBytes + half * kHalfBytes, tmv, 0, half, h, row,
+                                &full[stage], once);
+                } else {
+                    tma_load_4d(kd + half * kHalfBytes, tmk, 0, half, h, row, &full[stage]);
+                    tma_load_4d(kd + (size_t)NW * kBoxBytes + half * kHalfBytes, tmv, 0, half, h, row,
+                                &full[stage]);
+                }
             }
         }
         if (++stage == p.stages) {
@@ -320,15 +339,6 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
 __device__ __forceinline__ uint32_t box_chunk(int t, int c)
 {
     return (uint32_t)((c >> 3) * kHalfBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
-}
-
-// Descriptor of a box for the weights kernel (lane 0 of its worker).
-template <int BT>
-__device__ __forceinline__ void record_box(const DecodeParams &p, const BoxMeta &bm)
-{
-    const bool newest = (bm.flags & kStreamLast) != 0;  // its last valid token is the step's new one
-    p.ws_box[bm.box] = make_int4(bm.b, (bm.flags & kBoxLoaded) ? bm.blk : -1, bm.off,
-                                 bm.nvalid | (newest ? kBoxNewest : 0));
 }
 
 // Log-sum-exp (log2 units) of a row with running max m and sum l; +inf where
@@ -485,10 +495,6 @@ __device__ __forceinline__ void decode_consumer(const DecodeParams &p, uint8_t *
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&empty[stage]);
-        if constexpr (WT) {
-            if (lane == 0 && (bm.flags & kBoxValid))
-                record_box<kBox>(p, bm);
-        }
 
         if (bm.flags & kPieceLast) {
             // ---- finish this worker's piece of the stream ----
@@ -761,14 +767,16 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                     if (g + 8 >= nv) { sv[u][2] = -INFINITY; sv[u][3] = -INFINITY; }
                 }
                 if constexpr (WT) {
-                    float *sp = p.ws_score + ((size_t)bm.box * G + h0) * BT + 16 * u + g;
-                    if (h0 < G) {
-                        sp[0] = sv[u][0];
-                        sp[8] = sv[u][2];
-                    }
-                    if (h1 < G) {
-                        sp[BT] = sv[u][1];
-                        sp[BT + 8] = sv[u][3];
+                    // token-major: a lane's two heads lie next to each other
+                    float *sp = p.ws_score + ((size_t)bm.box * BT + 16 * u + g) * G + h0;
+                    if (G == 1) {
+                        if (quad == 0) {
+                            sp[0] = sv[u][0];
+                            sp[8] = sv[u][2];
+                        }
+                    } else if (h1 < G) {
+                        *reinterpret_cast<float2 *>(sp) = make_float2(sv[u][0], sv[u][1]);
+                        *reinterpret_cast<float2 *>(sp + 8 * G) = make_float2(sv[u][2], sv[u][3]);
                     }
                 }
             }
@@ -831,10 +839,6 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
         }
         if (!released)
             release();
-        if constexpr (WT) {
-            if (lane == 0 && (bm.flags & kBoxValid))
-                record_box<BT>(p, bm);
-        }
 
         if (bm.flags & kPieceLast) {
             float t0 = l0, t1 = l1;

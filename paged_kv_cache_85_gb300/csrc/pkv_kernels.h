@@ -44,9 +44,9 @@ struct DecodeParams {
     float scale_log2;             // scale * log2(e) (FP8 caches: times k_scale)
     float v_scale;                // FP8 caches: dequant scale of V (1 for bf16)
     // The calls that record attention weights; null elsewhere.
-    float *ws_lse = nullptr;      // [B, Hq] log-sum-exp of every row (log2 units)
+    float *ws_lse = nullptr;      // [B, Hq] log-sum-exp (log2 units) of rows that one worker read whole
     int4 *ws_box = nullptr;       // per box: sequence, block (-1: not read), offset, valid tokens | kBoxNewest
-    float *ws_score = nullptr;    // per box: [G][box tokens] scores (log2 units)
+    float *ws_score = nullptr;    // per box: [G][box tokens] scores (log2 units; FP8: [box tokens][G])
 };
 constexpr int kBoxNewest = 1 << 16;  // the box's last valid token is the step's new token
 
@@ -59,7 +59,7 @@ cudaError_t launch_store_fp8(const void *k, const void *v, void *k_cache, void *
                              long long n_slots, float kinv, float vinv, int32_t *err_flag,
                              cudaStream_t stream);
 cudaError_t launch_merge(int D, int G, const DecodeParams &p, cudaStream_t stream);
-cudaError_t launch_add_weights(int G, int bt, const DecodeParams &p, float *weights, long long max_boxes,
-                               int sms, cudaStream_t stream);
+cudaError_t launch_merge_and_add(int D, int G, int bt, bool token_major, const DecodeParams &p,
+                                 float *weights, long long max_boxes, int sms, cudaStream_t stream);
 
 } // namespace pkv

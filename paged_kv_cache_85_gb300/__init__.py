@@ -399,73 +399,109 @@ def evict_workspace_bytes(B, Hkv, MBS, bs, budget) -> int:
     return int(load_library().pkv_evict_workspace_bytes(B, Hkv, MBS, bs, budget))
 
 
-def _scratch(workspace, nbytes, device):
-    """The caller's workspace, or one for this call alone: the caching allocator
-    hands it out on the current stream (inside a capture, from the graph's own
-    pool), so neither another call nor another graph shares it."""
-    import torch
-
-    if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.device != device:
-        raise ValueError(f"workspace must be a CUDA tensor on {device}")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace
+def _tensors(torch, dev, *specs):
+    """Check (tensor, name, dtype, dims) for each spec, all contiguous on CUDA device ``dev``."""
+    for t, name, dtype, ndim in specs:
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == ndim
+                and t.get_device() == dev and t.is_contiguous()):
+            _require(t, name, dtype, ndim)
+            raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{dev}")
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.is_cuda and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {first.device}")
-
-
-def _require_weights(weights, k_cache):
-    import torch
-
-    _require(weights, "weights", torch.float32, 3)
-    NB, bs, Hkv, _ = k_cache.shape
-    if tuple(weights.shape) != (NB, Hkv, bs):
-        raise ValueError(f"weights must be [NB, Hkv, bs] = {(NB, Hkv, bs)} for these caches; got "
-                         f"{tuple(weights.shape)}")
-
-
-def _decode_weights(name, fp8, q, k_cache, v_cache, block_tables, context_lens, scale, scales, out,
-                    weights, max_ctas, workspace, err_flag):
-    import torch
-
-    _require(q, "q", torch.bfloat16, 3)
+def _caches(torch, k_cache, v_cache, weights, fp8):
+    """Check the caches and their weights; returns (device index, NB, bs, Hkv, D)."""
     if fp8:
-        _require_fp8_cache(k_cache, "k_cache")
-        _require_fp8_cache(v_cache, "v_cache")
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            _require_fp8_cache(t, name)
     else:
         _require(k_cache, "k_cache", torch.bfloat16, 4)
         _require(v_cache, "v_cache", torch.bfloat16, 4)
-    _require(block_tables, "block_tables", torch.int32, 2)
-    _require(context_lens, "context_lens", torch.int32, 1)
+    dev = k_cache.get_device()
+    if v_cache.get_device() != dev:
+        raise ValueError(f"v_cache is on {v_cache.device}, k_cache on {k_cache.device}")
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError(f"the caches' shapes differ: {tuple(shape)} and {tuple(v_cache.shape)}")
+    NB, bs, Hkv, D = shape
+    _tensors(torch, dev, (weights, "weights", torch.float32, 3))
+    if weights.shape != (NB, Hkv, bs):
+        raise ValueError(f"weights must be [NB, Hkv, bs] = {(NB, Hkv, bs)} for these caches; got "
+                         f"{tuple(weights.shape)}")
+    return dev, NB, bs, Hkv, D
+
+
+def _result(torch, dev, out, q):
+    """Check ``out``: q's shape, on the same device or in pinned host memory."""
     _require(out, "out", torch.bfloat16, 3, host_ok=True)
-    _require_weights(weights, k_cache)
-    if err_flag is not None:
-        _require(err_flag, "err_flag", torch.int32, 1)
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, out=out, weights=weights, err_flag=err_flag)
-    B, Hq, D = q.shape
-    NB, bs, Hkv, D2 = k_cache.shape
-    if v_cache.shape != k_cache.shape or D2 != D or out.shape != q.shape:
-        raise ValueError(f"{name}: shapes do not match")
+    if out.is_cuda and out.get_device() != dev:
+        raise ValueError(f"out is on {out.device}, the other tensors on cuda:{dev}")
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}; got {tuple(out.shape)}")
+
+
+def _scratch(torch, workspace, nbytes, dev):
+    """The caller's workspace, or one for this call alone: the caching allocator
+    hands it out on the current stream (inside a capture, from the graph's own
+    pool), so neither another call nor another graph shares it.  Returns the
+    tensor (kept until the launch), its address and its size."""
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), nbytes
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a tensor on cuda:{dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _flag(torch, dev, err_flag):
+    if err_flag is None:
+        return None
+    _tensors(torch, dev, (err_flag, "err_flag", torch.int32, 1))
+    if err_flag.numel() < 1:
+        raise ValueError("err_flag must hold one element")
+    return err_flag.data_ptr()
+
+
+_sizes: dict = {}  # workspace bytes by call and sizes (they depend on nothing else)
+
+
+def _bytes(function, *sizes):
+    key = (function, sizes)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[key] = int(getattr(_lib, function)(*sizes))
+    return n
+
+
+def _decode_weights(fp8, q, k_cache, v_cache, block_tables, context_lens, scale, scales, out, weights,
+                    max_ctas, workspace, err_flag):
+    import torch
+
+    dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, fp8)
+    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", torch.int32, 2),
+             (context_lens, "context_lens", torch.int32, 1))
+    B, Hq, D2 = q.shape
+    if D2 != D:
+        raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
     if block_tables.shape[0] != B or context_lens.shape[0] != B:
-        raise ValueError(f"{name}: block_tables/context_lens batch != q batch")
-    MBS = max(block_tables.shape[1], 1)
+        raise ValueError("block_tables/context_lens batch != q batch")
+    _result(torch, dev, out, q)
+    flag = _flag(torch, dev, err_flag)
+    MBS, max_ctas = max(block_tables.shape[1], 1), int(max_ctas)
     lib = _lib or load_library()
-    idx = q.get_device()
-    with _on_device(idx):
-        ws = _scratch(workspace, int(lib.pkv_decode_weights_workspace_bytes(
-            B, Hq, Hkv, D, MBS, bs, max_ctas)), q.device)
-        args = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MBS,
-                context_lens.data_ptr(), B, Hq, Hkv, D, NB, bs, float(scale), *scales,
-                out.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                int(max_ctas), err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)]
-        _check((lib.pkv_paged_attn_decode_weights_fp8 if fp8 else lib.pkv_paged_attn_decode_weights)(*args))
+    with _on_device(dev):
+        ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
+            "pkv_decode_weights_workspace_bytes", B, Hq, Hkv, D, MBS, bs, max_ctas), dev)
+        call = lib.pkv_paged_attn_decode_weights_fp8 if fp8 else lib.pkv_paged_attn_decode_weights
+        _check(call(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), MBS,
+                    context_lens.data_ptr(), B, Hq, Hkv, D, NB, bs, float(scale), *scales,
+                    out.data_ptr(), weights.data_ptr(), ws_ptr, ws_bytes, max_ctas, flag,
+                    _raw_stream(dev)))
     return out
 
 
@@ -479,16 +515,15 @@ def paged_attn_decode_weights(q, k_cache, v_cache, block_tables, context_lens, s
     weight set rather than added to, so freshly stored slots need no clearing.
     Writes ``out`` and returns it.
     """
-    return _decode_weights("paged_attn_decode_weights", False, q, k_cache, v_cache, block_tables,
-                           context_lens, scale, (), out, weights, max_ctas, workspace, err_flag)
+    return _decode_weights(False, q, k_cache, v_cache, block_tables, context_lens, scale, (), out,
+                           weights, max_ctas, workspace, err_flag)
 
 
 def paged_attn_decode_weights_fp8(q, k_cache, v_cache, block_tables, context_lens, scale, k_scale,
                                   v_scale, out, weights, max_ctas=0, workspace=None, err_flag=None):
     """``paged_attn_decode_weights`` over FP8 (E4M3) caches."""
-    return _decode_weights("paged_attn_decode_weights_fp8", True, q, k_cache, v_cache, block_tables,
-                           context_lens, scale, (float(k_scale), float(v_scale)), out, weights,
-                           max_ctas, workspace, err_flag)
+    return _decode_weights(True, q, k_cache, v_cache, block_tables, context_lens, scale,
+                           (float(k_scale), float(v_scale)), out, weights, max_ctas, workspace, err_flag)
 
 
 def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
@@ -502,36 +537,27 @@ def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_se
     """
     import torch
 
-    _require(q, "q", torch.bfloat16, 3)
-    _require(k_cache, "k_cache", torch.bfloat16, 4)
-    _require(v_cache, "v_cache", torch.bfloat16, 4)
-    _require(block_tables, "block_tables", torch.int32, 2)
-    _require(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    _require(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    _require(out, "out", torch.bfloat16, 3, host_ok=True)
-    _require_weights(weights, k_cache)
-    if err_flag is not None:
-        _require(err_flag, "err_flag", torch.int32, 1)
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, out=out,
-                 cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, weights=weights,
-                 err_flag=err_flag)
-    Tq, Hq, D = q.shape
-    NB, bs, Hkv, D2 = k_cache.shape
-    if v_cache.shape != k_cache.shape or D2 != D or out.shape != q.shape:
-        raise ValueError("paged_prefill_weights: shapes do not match")
+    dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, False)
+    i32 = torch.int32
+    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", i32, 2),
+             (cu_seqlens_q, "cu_seqlens_q", i32, 1), (cu_seqlens_k, "cu_seqlens_k", i32, 1))
+    Tq, Hq, D2 = q.shape
+    if D2 != D:
+        raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
     B = cu_seqlens_q.shape[0] - 1
     if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError("paged_prefill_weights: cu_seqlens / block_tables batch sizes differ")
+        raise ValueError("cu_seqlens / block_tables batch sizes differ")
+    _result(torch, dev, out, q)
+    flag = _flag(torch, dev, err_flag)
     lib = _lib or load_library()
-    idx = q.get_device()
-    with _on_device(idx):
-        ws = _scratch(workspace, int(lib.pkv_prefill_weights_workspace_bytes(Tq, Hq)), q.device)
+    with _on_device(dev):
+        ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
+            "pkv_prefill_weights_workspace_bytes", Tq, Hq), dev)
         _check(lib.pkv_paged_prefill_weights(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
             max(block_tables.shape[1], 1), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
             int(max_seqlen_q), Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), weights.data_ptr(),
-            int(window), ws.data_ptr(), ws.numel() * ws.element_size(),
-            err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)))
+            int(window), ws_ptr, ws_bytes, flag, _raw_stream(dev)))
     return out
 
 
@@ -549,34 +575,21 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
     import torch
 
     fp8 = isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.bfloat16
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if fp8:
-            _require_fp8_cache(t, name)
-        else:
-            _require(t, name, torch.bfloat16, 4)
-    _require_weights(weights, k_cache)
-    _require(block_tables, "block_tables", torch.int32, 2)
-    _require(context_lens, "context_lens", torch.int32, 1)
-    _require(out_lens, "out_lens", torch.int32, 1)
-    if err_flag is not None:
-        _require(err_flag, "err_flag", torch.int32, 1)
-    _same_device(k_cache, v_cache=v_cache, weights=weights, block_tables=block_tables,
-                 context_lens=context_lens, out_lens=out_lens, err_flag=err_flag)
-    NB, bs, Hkv, D = k_cache.shape
+    dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, fp8)
+    i32 = torch.int32
+    _tensors(torch, dev, (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1),
+             (out_lens, "out_lens", i32, 1))
     B = context_lens.shape[0]
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("evict_kvcache: cache shapes differ")
     if block_tables.shape[0] != B or out_lens.shape[0] != B:
-        raise ValueError("evict_kvcache: block_tables/out_lens batch != context_lens batch")
-    MBS = max(block_tables.shape[1], 1)
+        raise ValueError("block_tables/out_lens batch != context_lens batch")
+    flag = _flag(torch, dev, err_flag)
+    MBS, budget = max(block_tables.shape[1], 1), int(budget)
     lib = _lib or load_library()
-    idx = k_cache.get_device()
-    with _on_device(idx):
-        ws = _scratch(workspace, int(lib.pkv_evict_workspace_bytes(B, Hkv, MBS, bs, int(budget))),
-                      k_cache.device)
+    with _on_device(dev):
+        ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
+            "pkv_evict_workspace_bytes", B, Hkv, MBS, bs, budget), dev)
         _check(lib.pkv_evict_kvcache(
             k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(), MBS,
-            context_lens.data_ptr(), B, Hkv, D, k_cache.element_size(), NB, bs, int(budget),
-            int(recent), out_lens.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-            err_flag.data_ptr() if err_flag is not None else None, _raw_stream(idx)))
+            context_lens.data_ptr(), B, Hkv, D, 1 if fp8 else 2, NB, bs, budget, int(recent),
+            out_lens.data_ptr(), ws_ptr, ws_bytes, flag, _raw_stream(dev)))
     return out_lens

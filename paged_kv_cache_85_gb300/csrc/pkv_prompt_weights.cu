@@ -10,26 +10,34 @@
 // It is added to weights[block, kv head, offset], or stored there for the
 // step's new tokens, whose slots may hold what an earlier owner left.
 //
-// The scores are made transposed, S^T = K Q^T with the 128 cached tokens of an
-// item as the MMA's rows, so that a thread owns one token (a TMEM lane) and
-// the sum over queries runs along its own columns: no reduction over threads,
-// one addition to memory per token and KV head, and the same result in every
-// run.  An item is 128 tokens of one sequence and KV head; the (new token,
-// head) rows that see any of them pass by in tiles of 128.  A persistent CTA
-// per SM takes items by ticket (sequences in order, early tokens first, which
-// are the long items of a causal chunk); the sum does not depend on who takes
-// what.  Warps:
-//   0..3, 4..7  two groups of 128 threads that take turns over the query
-//         tiles: load 128 scores per token from TMEM, exponentiate against the
-//         tile's lse (shared memory, read as broadcasts), add up.  Partial sums
-//         per tile, then per item: no long sequential fp32 sum
-//   8     producer: ticket, item, TMA of the K tile (two stages, so the next
-//         item's K is on its way) and of the query tiles (four stages)
-//   9     MMA: per query tile D / 16 steps of M = 128 (tokens), N = 128
-//         (queries) into one of four TMEM buffers
+// The scores are made transposed, S^T = K Q^T with the cached tokens as the
+// MMA's rows, so that a thread owns one token (a TMEM lane) and the sum over
+// queries runs along its own columns: no reduction over threads, one addition
+// to memory per token and KV head, and the same result in every run.  An item is
+// 256 tokens (two MMA tiles A and B) of one sequence and KV head; the (new
+// token, head) rows that see any of them pass by in tiles of 128.  Two token
+// tiles per query tile halve the query rows read from L2, which bound the
+// kernel with one (32 KB per 128 x 128 scores, 9 TB/s: 143 us of the 16k step).
+// A persistent CTA per SM takes items by ticket (sequences in order, early
+// tokens first, which are the long items of a causal chunk); the sum does not
+// depend on who takes what.  Warps:
+//   0..15 four groups of 128 threads, one per token tile and half of a query
+//         tile's columns: load 64 scores per token from TMEM, exponentiate
+//         against the tile's lse (shared memory, read as broadcasts), add up.
+//         Partial sums per tile, then per item: no long sequential fp32 sum.
+//         At the item's end the second half's sums go to the first's
+//   16    producer: ticket, item, TMA of the K tiles (a ring of three, so that
+//         the next item's are on their way) and of the query tiles (three)
+//   17, 18 MMA, one warp per token tile (one thread cannot issue for both
+//         without leaving the pipe idle): per query tile D / 16 steps of M = 128
+//         (tokens), N = 128 (queries) into one of two TMEM buffers
+// Work per pair of 128 x 128 tiles and SM: 1024 cycles of 2^x (32 per cycle) and
+// as many of MMA.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "pkv_kernels.h"
 #include "pkv_prefill.h"
@@ -38,29 +46,30 @@
 
 namespace pkv {
 
-constexpr int kPwTokens = 128;  // cached tokens per item (MMA M)
+constexpr int kPwTokens = 128;  // cached tokens per token tile (MMA M); two per item
 constexpr int kPwRows = 128;    // (new token, head) rows per query tile (MMA N)
-constexpr int kPwKStages = 2;
-constexpr int kPwQStages = 4;
-constexpr int kPwSBufs = 4;     // TMEM score buffers of 128 columns
+constexpr int kPwKStages = 3;
+constexpr int kPwQStages = 3;
 constexpr int kPwItems = 4;     // published items
-constexpr int kPwThreads = 10 * 32;
-constexpr int kPwProducerWarp = 8;
-constexpr int kPwMmaWarp = 9;
+constexpr int kPwSoftWarps = 16;
+constexpr int kPwThreads = (kPwSoftWarps + 3) * 32;
+constexpr int kPwProducerWarp = kPwSoftWarps;
+constexpr int kPwMmaWarp = kPwSoftWarps + 1;  // and the next, for token tile B
 
-// 128 tokens of one sequence and KV head, and the query tiles that see them
+// 256 tokens of one sequence and KV head, and the query tiles that see them
 struct PwItem {
     int b, kvh, t0;     // b < 0: no more work
     int cq0, q_len, k_len;
     int i0;             // first recorded new token that sees a token of the item
     int tiles;          // query tiles from i0 on
+    int first1;         // the first of them that sees token tile B (tiles: none does)
 };
 
 struct PwSmem {
     size_t q, k, lse, part, bars, items, slot, total;
 };
 
-constexpr int kPwBars = 2 * kPwKStages + 2 * kPwQStages + 2 * kPwSBufs + 2 * kPwItems + 16 + 1;
+constexpr int kPwBars = 2 * kPwKStages + 2 * kPwQStages + 8 + 2 * kPwItems + 32 + 1;
 
 __host__ __device__ inline PwSmem pw_smem_layout(int D)
 {
@@ -70,10 +79,10 @@ __host__ __device__ inline PwSmem pw_smem_layout(int D)
     o += (size_t)kPwQStages * (D / 64) * kPwRows * 128;
     L.k = o;  // stages alike
     o += (size_t)kPwKStages * (D / 64) * kPwTokens * 128;
-    L.lse = o;  // [softmax warp][2][128] negated log-sum-exps of a query tile
-    o += 8 * 2 * kPwRows * sizeof(float);
-    L.part = o;  // [2][128] the second group's sums on their way to the first
-    o += 2 * kPwTokens * sizeof(float);
+    L.lse = o;  // [softmax warp][2][64] negated log-sum-exps of half a query tile
+    o += kPwSoftWarps * 2 * (kPwRows / 2) * sizeof(float);
+    L.part = o;  // [token tile][2][128] the second half's sums on their way to the first
+    o += 2 * 2 * kPwTokens * sizeof(float);
     L.bars = o;
     o += 8 * kPwBars;
     L.items = align_up(o, 16);
@@ -110,16 +119,16 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const PwSmem L = pw_smem_layout(D);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L.bars);
-    uint64_t *k_empty = k_full + kPwKStages;   // the item's MMAs completed
+    uint64_t *k_empty = k_full + kPwKStages;   // the item's MMAs of the token tile completed
     uint64_t *q_full = k_empty + kPwKStages;
-    uint64_t *q_empty = q_full + kPwQStages;   // the tile's MMAs completed
-    uint64_t *s_full = q_empty + kPwQStages;
-    uint64_t *s_empty = s_full + kPwSBufs;     // the scores are in registers (4 warps)
-    uint64_t *item_ready = s_empty + kPwSBufs;
-    uint64_t *item_free = item_ready + kPwItems;  // 8 softmax warps and the MMA warp
-    uint64_t *part_full = item_free + kPwItems;   // [2][4] a warp's part written ...
-    uint64_t *part_empty = part_full + 8;         // ... and taken over by its partner
-    uint64_t *mma_done = part_empty + 8;
+    uint64_t *q_empty = q_full + kPwQStages;   // both token tiles' MMAs with the query tile completed
+    uint64_t *s_full = q_empty + kPwQStages;   // [token tile][2 buffers]
+    uint64_t *s_empty = s_full + 4;            // the scores are in registers (8 warps)
+    uint64_t *item_ready = s_empty + 4;
+    uint64_t *item_free = item_ready + kPwItems;  // the softmax and the MMA warps
+    uint64_t *part_full = item_free + kPwItems;   // [2][token tile][4] a warp's part written ...
+    uint64_t *part_empty = part_full + 16;        // ... and taken over by its partner
+    uint64_t *mma_done = part_empty + 16;
     PwItem *items = reinterpret_cast<PwItem *>(smem + L.items);
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
     uint8_t *sQ = smem + L.q, *sK = smem + L.k;
@@ -134,21 +143,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
         for (int s = 0; s < kPwQStages; s++) {
             mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
+            mbar_init(&q_empty[s], 2);
         }
-        for (int s = 0; s < kPwSBufs; s++) {
+        for (int s = 0; s < 4; s++) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&s_empty[s], 4);
+            mbar_init(&s_empty[s], 8);
         }
         for (int s = 0; s < kPwItems; s++) {
             mbar_init(&item_ready[s], 1);
-            mbar_init(&item_free[s], 9);
+            mbar_init(&item_free[s], kPwSoftWarps + 2);
         }
-        for (int s = 0; s < 8; s++) {
+        for (int s = 0; s < 16; s++) {
             mbar_init(&part_full[s], 1);
             mbar_init(&part_empty[s], 1);
         }
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);
         fence_mbarrier_init();
     } else if (warp == kPwMmaWarp) {
         tc::alloc(smem_u32(slot), 512);
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     k_len = kl;
                 }
             }
-            mine = (long long)((k_len + kPwTokens - 1) / kPwTokens) * p.Hkv;
+            mine = (long long)((k_len + 2 * kPwTokens - 1) / (2 * kPwTokens)) * p.Hkv;
             incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -204,7 +213,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             ticket = atomicAdd(p.ticket, 1);
         for (;;) {
             // ---- the ticket's item
-            PwItem it{-1, 0, 0, 0, 0, 0, 0, 0};
+            PwItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0};
             const long long pos = __shfl_sync(FULL, ticket, 0);
             if (ok) {
                 while (b0 < p.B && pos - before >= __shfl_sync(FULL, incl, 31)) {
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     const int rr = (int)(r - __shfl_sync(FULL, incl - mine, src));
                     it.b = b0 + src;
                     it.kvh = rr % p.Hkv;
-                    it.t0 = rr / p.Hkv * kPwTokens;
+                    it.t0 = rr / p.Hkv * (2 * kPwTokens);
                     it.cq0 = __shfl_sync(FULL, cq0, src);
                     it.q_len = __shfl_sync(FULL, q_len, src);
                     it.k_len = __shfl_sync(FULL, k_len, src);
@@ -228,6 +237,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     if (P.window > 0)
                         it.i0 = max(it.i0, it.q_len - P.window);
                     it.tiles = ((it.q_len - it.i0) + TPC - 1) / TPC;
+                    const int t1 = it.t0 + kPwTokens;
+                    it.first1 = t1 < it.k_len
+                                    ? max(0, t1 - (it.k_len - it.q_len) - it.i0) / TPC
+                                    : it.tiles;
                 }
             }
             // the next ticket, on its way while this item is copied
@@ -244,10 +257,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             __syncwarp();
             if (it.b < 0)
                 break;
-            // ---- K tile: lanes 0..7 resolve one 16-token box each; where blocks
+            // ---- K tiles: lanes 0..7 resolve one 16-token box each; where blocks
             // hold whole 64-token runs one copy per run and half, else per box
-            {
-                const int t = it.t0 + lane * kBox;
+            for (int kt = 0; kt < 2 && ok; kt++) {
+                if (kt == 1 && it.first1 >= it.tiles)
+                    break;
+                const int t = it.t0 + kt * kPwTokens + lane * kBox;
                 int row = -1;
                 if (lane < kPwTokens / kBox && t < it.k_len) {
                     const int blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
@@ -271,6 +286,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 }
                 nk++;
             }
+            if (!ok)
+                break;
             // ---- query tiles
             for (int j = 0; j < it.tiles && ok; j++) {
                 const int s = gq % kPwQStages;
@@ -299,43 +316,55 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 mbar_wait(&q_full[g % kPwQStages], (g / kPwQStages) & 1);
         }
         __syncwarp();
-    } else if (warp == kPwMmaWarp) {
+    } else if (warp >= kPwMmaWarp) {
         // ----------------------------------------------------------------- MMA
         bool ok = true;
         // A = K (negated for a negative scale: bit 13), B = Q, both K-major
         const uint32_t idS = tc::idesc_bf16(kPwTokens, kPwRows, false) | (p.neg_scale ? 1u << 13 : 0u);
+        const int kt = warp - kPwMmaWarp;  // token tile
         if (lane == 0) {
-            int gq = 0;
+            int gq = 0, nk = 0;  // query and K tiles so far
+            int used = 0;        // query tiles that this token tile took part in
             for (int n = 0; ok; n++) {
                 if (!(ok = mbar_wait(&item_ready[n % kPwItems], (n / kPwItems) & 1)))
                     break;
                 const PwItem it = items[n % kPwItems];
                 if (it.b < 0)
                     break;
-                const int ks = n % kPwKStages;
-                if (!(ok = mbar_wait(&k_full[ks], (n / kPwKStages) & 1)))
-                    break;
+                const int kts = it.first1 < it.tiles ? 2 : 1;
+                const int first = kt == 0 ? 0 : it.first1;
+                const int ks = (nk + kt) % kPwKStages;
                 const uint32_t ka = smem_u32(sK + (size_t)ks * kTile);
+                if (first < it.tiles && !(ok = mbar_wait(&k_full[ks], ((nk + kt) / kPwKStages) & 1)))
+                    break;
                 for (int j = 0; j < it.tiles; j++, gq++) {
-                    const int s = gq % kPwQStages, buf = gq % kPwSBufs;
+                    const int s = gq % kPwQStages;
                     if (!(ok = mbar_wait(&q_full[s], (gq / kPwQStages) & 1)))
                         break;
-                    if (!(ok = mbar_wait(&s_empty[buf], ((gq / kPwSBufs) & 1) ^ 1)))
-                        break;
-                    tc::fence_after();
-                    const uint32_t qb = smem_u32(sQ + (size_t)s * kTile);
+                    if (j >= first) {
+                        const int buf = 2 * kt + (used & 1);
+                        if (!(ok = mbar_wait(&s_empty[buf], ((used >> 1) & 1) ^ 1)))
+                            break;
+                        used++;
+                        tc::fence_after();
+                        const uint32_t qb = smem_u32(sQ + (size_t)s * kTile);
 #pragma unroll
-                    for (int kq = 0; kq < D / 16; kq++) {
-                        const uint32_t off = (uint32_t)(kq >> 2) * kHalf + (uint32_t)(kq & 3) * 32;
-                        tc::mma_ss(tmem + 128u * buf, tc::smem_desc(ka + off, 16, 1024),
-                                   tc::smem_desc(qb + off, 16, 1024), idS, kq > 0);
+                        for (int kq = 0; kq < D / 16; kq++) {
+                            const uint32_t off = (uint32_t)(kq >> 2) * kHalf + (uint32_t)(kq & 3) * 32;
+                            tc::mma_ss(tmem + 128u * buf, tc::smem_desc(ka + off, 16, 1024),
+                                       tc::smem_desc(qb + off, 16, 1024), idS, kq > 0);
+                        }
+                        tc::commit(smem_u32(&s_full[buf]));
+                        tc::commit(smem_u32(&q_empty[s]));
+                        if (j == it.tiles - 1)
+                            tc::commit(smem_u32(&k_empty[ks]));
+                    } else {
+                        mbar_arrive(&q_empty[s]);  // a query tile that does not see the token tile
                     }
-                    tc::commit(smem_u32(&s_full[buf]));
-                    tc::commit(smem_u32(&q_empty[s]));
                 }
                 if (!ok)
                     break;
-                tc::commit(smem_u32(&k_empty[ks]));
+                nk += kts;
                 mbar_arrive(&item_free[n % kPwItems]);
             }
             if (!ok)
@@ -347,18 +376,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax
-        const int grp = warp >> 2;
-        const int r = threadIdx.x & 127;  // token of the item = TMEM lane
-        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        float *nlse = reinterpret_cast<float *>(smem + L.lse) + warp * 2 * kPwRows;
-        float *part = reinterpret_cast<float *>(smem + L.part);
+        const int kt = warp >> 3, half = (warp >> 2) & 1;  // token tile, half of the columns
+        constexpr int kCols = kPwRows / 2;
+        const int r = threadIdx.x & 127;  // token of the tile = TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256u * kt + kCols * half;
+        float *nlse = reinterpret_cast<float *>(smem + L.lse) + warp * 2 * kCols;
+        float *part = reinterpret_cast<float *>(smem + L.part) + kt * 2 * kPwTokens;
         const float sl = p.scale_log2;
         const float2 sl2 = make_float2(sl, sl);
         grid_dependency_wait();
         bool ok = true;
-        int gq = 0;    // query tiles before this item
-        int seen = 0;  // query tiles of this group so far
-        int parts = 0; // sums handed over so far
+        int used = 0;   // query tiles of this token tile so far
+        int parts = 0;  // sums handed over so far
         for (int n = 0; ok; n++) {
             ok = __all_sync(FULL, mbar_wait(&item_ready[n % kPwItems], (n / kPwItems) & 1));
             if (!ok)
@@ -366,115 +395,110 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             const PwItem it = items[n % kPwItems];
             if (it.b < 0)
                 break;
-            const int j0 = (gq & 1) == grp ? 0 : 1;  // this group's first tile of the item
-            const int t = it.t0 + r;
-            const int base = it.k_len - it.q_len;
-            int blk = -1;
-            if (t < it.k_len)
-                blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
-            const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G;
-            // log-sum-exps of query tile j, negated, four per lane; -inf (weight 0)
-            // past the sequence.  Loaded one of the group's tiles ahead.
-            float ahead[4];
-            auto load_lse = [&](int j) {
-                const int i_first = it.i0 + j * TPC;
+            const int first = kt == 0 ? 0 : it.first1;
+            if (first < it.tiles) {
+                const int t = it.t0 + kt * kPwTokens + r;
+                const int base = it.k_len - it.q_len;
+                int blk = -1;
+                if (half == 0 && t < it.k_len)
+                    blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
+                const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G + kCols * half;
+                // log-sum-exps of this half of query tile j, negated, two per lane; -inf
+                // (weight 0) past the sequence.  Loaded one tile ahead.
+                float ahead[2];
+                auto load_lse = [&](int j) {
+                    const int i_first = it.i0 + j * TPC;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int c = lane + 32 * i;
-                    ahead[i] = j < it.tiles && i_first + c / G < it.q_len
-                                   ? -__ldg(lse + (size_t)i_first * G + c)
-                                   : -INFINITY;
+                    for (int i = 0; i < 2; i++) {
+                        const int c = lane + 32 * i;
+                        ahead[i] = j < it.tiles && i_first + (kCols * half + c) / G < it.q_len
+                                       ? -__ldg(lse + (size_t)i_first * G + c)
+                                       : -INFINITY;
+                    }
+                };
+                load_lse(first);
+                float sum = 0.f;
+                for (int j = first; j < it.tiles; j++, used++) {
+                    const int buf = 2 * kt + (used & 1);
+                    const int i_first = it.i0 + j * TPC;
+                    float *nl = nlse + (used & 1) * kCols;
+                    nl[lane] = ahead[0];
+                    nl[lane + 32] = ahead[1];
+                    __syncwarp();
+                    load_lse(j + 1);
+                    ok = __all_sync(FULL, mbar_wait(&s_full[buf], (used >> 1) & 1));
+                    if (!ok)
+                        break;
+                    tc::fence_after();
+                    uint32_t x[2][32];
+                    const uint32_t at = tl + 128u * (used & 1);
+                    tc::ld32(at, x[0]);
+                    tc::ld32(at + 32, x[1]);
+                    tc::wait_ld();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&s_empty[buf]);  // the scores are in registers
+                    // columns c0 <= c < c1 of this half are queries that see this token
+                    const int c0 = (t - base - i_first) * G - kCols * half;
+                    const int c1 = (it.q_len - i_first) * G - kCols * half;
+                    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+                    auto add = [&](auto masked_c) {
+                        constexpr bool kMasked = decltype(masked_c)::value;
+#pragma unroll
+                        for (int i = 0; i < kCols / 4; i++) {
+                            const uint32_t *y = &x[i >> 3][4 * (i & 7)];
+                            const float4 m = *reinterpret_cast<const float4 *>(nl + 4 * i);
+                            float2 u = ffma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sl2,
+                                             make_float2(m.x, m.y));
+                            float2 v = ffma2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sl2,
+                                             make_float2(m.z, m.w));
+                            if constexpr (kMasked) {
+                                const int c = 4 * i;
+                                u.x = c >= c0 && c < c1 ? u.x : -INFINITY;
+                                u.y = c + 1 >= c0 && c + 1 < c1 ? u.y : -INFINITY;
+                                v.x = c + 2 >= c0 && c + 2 < c1 ? v.x : -INFINITY;
+                                v.y = c + 3 >= c0 && c + 3 < c1 ? v.y : -INFINITY;
+                            }
+                            a0 = fadd2(a0, make_float2(fast_exp2(u.x), fast_exp2(u.y)));
+                            a1 = fadd2(a1, make_float2(fast_exp2(v.x), fast_exp2(v.y)));
+                        }
+                    };
+                    if (__any_sync(FULL, c0 > 0 || c1 < kCols))
+                        add(std::true_type());
+                    else
+                        add(std::false_type());
+                    sum += (a0.x + a0.y) + (a1.x + a1.y);
                 }
-            };
-            load_lse(j0);
-            float sum = 0.f;
-            for (int j = j0; j < it.tiles; j += 2) {
-                const int g = gq + j, buf = g % kPwSBufs;
-                const int i_first = it.i0 + j * TPC;
-                // the tile's log-sum-exps, a copy per warp
-                float *nl = nlse + (seen & 1) * kPwRows;
-                seen++;
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    nl[lane + 32 * i] = ahead[i];
-                __syncwarp();
-                load_lse(j + 2);
-                ok = __all_sync(FULL, mbar_wait(&s_full[buf], (g / kPwSBufs) & 1));
                 if (!ok)
                     break;
-                tc::fence_after();
-                // columns c0 <= c < c1 are queries that see this token
-                const int c0 = (t - base - i_first) * G;
-                const int c1 = (it.q_len - i_first) * G;
-                const bool masked = __any_sync(FULL, c0 > 0 || c1 < kPwRows);
-                float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-#pragma unroll
-                for (int q4 = 0; q4 < 4; q4++) {
-                    uint32_t x[32];
-                    tc::ld32(tl + 128u * buf + 32 * q4, x);
-                    tc::wait_ld();
-                    if (q4 == 3) {  // all scores of the buffer are in registers
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&s_empty[buf]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float4 m = *reinterpret_cast<const float4 *>(nl + 32 * q4 + 4 * i);
-                        float2 u = ffma2(make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
-                                         sl2, make_float2(m.x, m.y));
-                        float2 v = ffma2(make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])),
-                                         sl2, make_float2(m.z, m.w));
-                        if (masked) {
-                            const int c = 32 * q4 + 4 * i;
-                            u.x = c >= c0 && c < c1 ? u.x : -INFINITY;
-                            u.y = c + 1 >= c0 && c + 1 < c1 ? u.y : -INFINITY;
-                            v.x = c + 2 >= c0 && c + 2 < c1 ? v.x : -INFINITY;
-                            v.y = c + 3 >= c0 && c + 3 < c1 ? v.y : -INFINITY;
-                        }
-                        a0 = fadd2(a0, make_float2(fast_exp2(u.x), fast_exp2(u.y)));
-                        a1 = fadd2(a1, make_float2(fast_exp2(v.x), fast_exp2(v.y)));
-                    }
-                }
-                sum += (a0.x + a0.y) + (a1.x + a1.y);
-            }
-            if (!ok)
-                break;
-            // ---- the item's sums: with one tile the group that had it writes, else
-            // the second group hands its part to the first
-            const bool both = it.tiles > 1;
-            if (both) {
-                // warp w to warp w - 4, which has the same tokens
-                const int x = (parts & 1) * 4 + (warp & 3);
+                // ---- the second half hands its sums to the first (the warp with the
+                // same tokens), which writes
+                const int x = (parts & 1) * 8 + kt * 4 + (warp & 3);
                 float *pt = part + (parts & 1) * kPwTokens + r;
-                if (grp == 1) {
-                    ok = __all_sync(FULL, mbar_wait(&part_empty[x], ((parts >> 1) & 1) ^ 1));
-                    if (!ok)
-                        break;
+                ok = __all_sync(FULL, half == 1 ? mbar_wait(&part_empty[x], ((parts >> 1) & 1) ^ 1)
+                                                : mbar_wait(&part_full[x], (parts >> 1) & 1));
+                if (!ok)
+                    break;
+                if (half == 1)
                     *pt = sum;
-                } else {
-                    ok = __all_sync(FULL, mbar_wait(&part_full[x], (parts >> 1) & 1));
-                    if (!ok)
-                        break;
+                else
                     sum += *pt;
-                }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(grp == 1 ? &part_full[x] : &part_empty[x]);
+                    mbar_arrive(half == 1 ? &part_full[x] : &part_empty[x]);
                 parts++;
-            }
-            if ((both ? grp == 0 : j0 == 0) && t < it.k_len && blk >= 0 && blk < p.NB) {
-                float *dst = P.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs;
-                if (t >= base)
-                    *dst = sum;
-                else
-                    atomicAdd(dst, sum);
+                if (half == 0 && blk >= 0 && blk < p.NB) {
+                    float *dst = P.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs;
+                    if (t >= base)
+                        *dst = sum;
+                    else
+                        atomicAdd(dst, sum);
+                }
             }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&item_free[n % kPwItems]);
-            gq += it.tiles;
         }
         if (!ok && lane == 0)
             flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
@@ -515,7 +539,7 @@ cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CU
     P.weights = weights;
     P.window = window;
     // no more CTAs than items there can be
-    const long long tiles = ((long long)p.MBS * p.bs + kPwTokens - 1) / kPwTokens;
+    const long long tiles = ((long long)p.MBS * p.bs + 2 * kPwTokens - 1) / (2 * kPwTokens);
     const long long most = tiles * p.Hkv * p.B;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         // A = K (negated for a negative scale: bit 13), B = Q, both K-major
         const uint32_t idS = tc::idesc_bf16(kPwTokens, kPwRows, false) | (p.neg_scale ? 1u << 13 : 0u);
         const int kt = warp - kPwMmaWarp;  // token tile
-        if (lane == 0) {
+        // elect.sync, not lane == 0: the compiler then knows that a single thread
+        // issues, and an MMA costs the thread 45 cycles instead of 75
+        if (tc::elect_one()) {
             int gq = 0, nk = 0;  // query and K tiles so far
             int used = 0;        // query tiles that this token tile took part in
             for (int n = 0; ok; n++) {

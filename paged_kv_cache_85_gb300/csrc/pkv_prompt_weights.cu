@@ -31,6 +31,8 @@
 //   17, 18 MMA, one warp per token tile (one thread cannot issue for both
 //         without leaving the pipe idle): per query tile D / 16 steps of M = 128
 //         (tokens), N = 128 (queries) into one of two TMEM buffers
+//   19    the query tiles' log-sum-exps into a ring of four (by the softmax warps
+//         themselves they cost 500 cycles per tile)
 // Work per pair of 128 x 128 tiles and SM: 1024 cycles of 2^x (32 per cycle) and
 // as many of MMA.
 #include <cuda.h>
@@ -52,9 +54,11 @@ constexpr int kPwKStages = 3;
 constexpr int kPwQStages = 3;
 constexpr int kPwItems = 4;     // published items
 constexpr int kPwSoftWarps = 16;
-constexpr int kPwThreads = (kPwSoftWarps + 3) * 32;
+constexpr int kPwLseStages = 4;
+constexpr int kPwThreads = (kPwSoftWarps + 4) * 32;
 constexpr int kPwProducerWarp = kPwSoftWarps;
 constexpr int kPwMmaWarp = kPwSoftWarps + 1;  // and the next, for token tile B
+constexpr int kPwLseWarp = kPwSoftWarps + 3;
 
 // 256 tokens of one sequence and KV head, and the query tiles that see them
 struct PwItem {
@@ -69,7 +73,7 @@ struct PwSmem {
     size_t q, k, lse, part, bars, items, slot, total;
 };
 
-constexpr int kPwBars = 2 * kPwKStages + 2 * kPwQStages + 8 + 2 * kPwItems + 32 + 1;
+constexpr int kPwBars = 2 * kPwKStages + 2 * kPwQStages + 8 + 2 * kPwItems + 32 + 2 * kPwLseStages + 1;
 
 __host__ __device__ inline PwSmem pw_smem_layout(int D)
 {
@@ -79,8 +83,8 @@ __host__ __device__ inline PwSmem pw_smem_layout(int D)
     o += (size_t)kPwQStages * (D / 64) * kPwRows * 128;
     L.k = o;  // stages alike
     o += (size_t)kPwKStages * (D / 64) * kPwTokens * 128;
-    L.lse = o;  // [softmax warp][2][64] negated log-sum-exps of half a query tile
-    o += kPwSoftWarps * 2 * (kPwRows / 2) * sizeof(float);
+    L.lse = o;  // stages of [128] negated log-sum-exps of a query tile
+    o += kPwLseStages * kPwRows * sizeof(float);
     L.part = o;  // [token tile][2][128] the second half's sums on their way to the first
     o += 2 * 2 * kPwTokens * sizeof(float);
     L.bars = o;
@@ -125,10 +129,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     uint64_t *s_full = q_empty + kPwQStages;   // [token tile][2 buffers]
     uint64_t *s_empty = s_full + 4;            // the scores are in registers (8 warps)
     uint64_t *item_ready = s_empty + 4;
-    uint64_t *item_free = item_ready + kPwItems;  // the softmax and the MMA warps
+    uint64_t *item_free = item_ready + kPwItems;  // the softmax, MMA and lse warps
     uint64_t *part_full = item_free + kPwItems;   // [2][token tile][4] a warp's part written ...
     uint64_t *part_empty = part_full + 16;        // ... and taken over by its partner
-    uint64_t *mma_done = part_empty + 16;
+    uint64_t *lse_full = part_empty + 16;         // a query tile's log-sum-exps are there
+    uint64_t *lse_empty = lse_full + kPwLseStages;  // ... read by every softmax warp
+    uint64_t *mma_done = lse_empty + kPwLseStages;
     PwItem *items = reinterpret_cast<PwItem *>(smem + L.items);
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
     uint8_t *sQ = smem + L.q, *sK = smem + L.k;
@@ -151,7 +157,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
         for (int s = 0; s < kPwItems; s++) {
             mbar_init(&item_ready[s], 1);
-            mbar_init(&item_free[s], kPwSoftWarps + 2);
+            mbar_init(&item_free[s], kPwSoftWarps + 3);
+        }
+        for (int s = 0; s < kPwLseStages; s++) {
+            mbar_init(&lse_full[s], 1);
+            mbar_init(&lse_empty[s], kPwSoftWarps);
         }
         for (int s = 0; s < 16; s++) {
             mbar_init(&part_full[s], 1);
@@ -316,6 +326,53 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 mbar_wait(&q_full[g % kPwQStages], (g / kPwQStages) & 1);
         }
         __syncwarp();
+    } else if (warp == kPwLseWarp) {
+        // ------------------------------------------------------- log-sum-exps
+        // Query tile by query tile into a ring, negated, -inf (weight 0) past the
+        // sequence; loaded one tile ahead of its stage.
+        float *ring = reinterpret_cast<float *>(smem + L.lse);
+        grid_dependency_wait();
+        bool ok = true;
+        int gq = 0;
+        for (int n = 0; ok; n++) {
+            ok = __all_sync(FULL, mbar_wait(&item_ready[n % kPwItems], (n / kPwItems) & 1));
+            if (!ok)
+                break;
+            const PwItem it = items[n % kPwItems];
+            if (it.b < 0)
+                break;
+            const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G;
+            float ahead[4];
+            auto load = [&](int j) {
+                const int i_first = it.i0 + j * TPC;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int c = lane + 32 * i;
+                    ahead[i] = j < it.tiles && i_first + c / G < it.q_len
+                                   ? -__ldg(lse + (size_t)i_first * G + c)
+                                   : -INFINITY;
+                }
+            };
+            load(0);
+            for (int j = 0; j < it.tiles; j++, gq++) {
+                const int s = gq % kPwLseStages;
+                ok = __all_sync(FULL, mbar_wait(&lse_empty[s], ((gq / kPwLseStages) & 1) ^ 1));
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    ring[s * kPwRows + lane + 32 * i] = ahead[i];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&lse_full[s]);
+                load(j + 1);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&item_free[n % kPwItems]);
+        }
+        if (!ok && lane == 0)
+            flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
     } else if (warp >= kPwMmaWarp) {
         // ----------------------------------------------------------------- MMA
         bool ok = true;
@@ -382,12 +439,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         constexpr int kCols = kPwRows / 2;
         const int r = threadIdx.x & 127;  // token of the tile = TMEM lane
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256u * kt + kCols * half;
-        float *nlse = reinterpret_cast<float *>(smem + L.lse) + warp * 2 * kCols;
+        const float *ring = reinterpret_cast<const float *>(smem + L.lse) + kCols * half;
         float *part = reinterpret_cast<float *>(smem + L.part) + kt * 2 * kPwTokens;
         const float sl = p.scale_log2;
         const float2 sl2 = make_float2(sl, sl);
         grid_dependency_wait();
         bool ok = true;
+        int gq = 0;     // query tiles before this item
         int used = 0;   // query tiles of this token tile so far
         int parts = 0;  // sums handed over so far
         for (int n = 0; ok; n++) {
@@ -398,37 +456,30 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (it.b < 0)
                 break;
             const int first = kt == 0 ? 0 : it.first1;
+            // query tiles that do not see this token tile: their log-sum-exps are not
+            // needed, but the ring counts every warp
+            for (int j = 0; j < first && ok; j++) {
+                const int ls = (gq + j) % kPwLseStages;
+                ok = __all_sync(FULL, mbar_wait(&lse_full[ls], ((gq + j) / kPwLseStages) & 1));
+                if (ok && lane == 0)
+                    mbar_arrive(&lse_empty[ls]);
+            }
+            if (!ok)
+                break;
             if (first < it.tiles) {
                 const int t = it.t0 + kt * kPwTokens + r;
                 const int base = it.k_len - it.q_len;
                 int blk = -1;
                 if (half == 0 && t < it.k_len)
                     blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
-                const float *lse = p.lse + ((size_t)it.kvh * p.Tq + it.cq0) * G + kCols * half;
-                // log-sum-exps of this half of query tile j, negated, two per lane; -inf
-                // (weight 0) past the sequence.  Loaded one tile ahead.
-                float ahead[2];
-                auto load_lse = [&](int j) {
-                    const int i_first = it.i0 + j * TPC;
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const int c = lane + 32 * i;
-                        ahead[i] = j < it.tiles && i_first + (kCols * half + c) / G < it.q_len
-                                       ? -__ldg(lse + (size_t)i_first * G + c)
-                                       : -INFINITY;
-                    }
-                };
-                load_lse(first);
                 float sum = 0.f;
                 for (int j = first; j < it.tiles; j++, used++) {
                     const int buf = 2 * kt + (used & 1);
                     const int i_first = it.i0 + j * TPC;
-                    float *nl = nlse + (used & 1) * kCols;
-                    nl[lane] = ahead[0];
-                    nl[lane + 32] = ahead[1];
-                    __syncwarp();
-                    load_lse(j + 1);
-                    ok = __all_sync(FULL, mbar_wait(&s_full[buf], (used >> 1) & 1));
+                    const int ls = (gq + j) % kPwLseStages;
+                    const float *nl = ring + ls * kPwRows;
+                    ok = __all_sync(FULL, mbar_wait(&lse_full[ls], ((gq + j) / kPwLseStages) & 1) &&
+                                              mbar_wait(&s_full[buf], (used >> 1) & 1));
                     if (!ok)
                         break;
                     tc::fence_after();
@@ -470,6 +521,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         add(std::true_type());
                     else
                         add(std::false_type());
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&lse_empty[ls]);
                     sum += (a0.x + a0.y) + (a1.x + a1.y);
                 }
                 if (!ok)
@@ -501,6 +555,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&item_free[n % kPwItems]);
+            gq += it.tiles;
         }
         if (!ok && lane == 0)
             flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);

@@ -17,6 +17,7 @@
 #include "pkv_kernels.h"
 #include "pkv_prefill.h"
 #include "pkv_prefill_tc.cuh"
+#include "pkv_prefill_wide.cuh"
 
 namespace pkv {
 #define PKV_DECLARE_SHAPE(D, NW)                                                                  \
@@ -55,21 +56,38 @@ cudaError_t launch_prefill_d128(int G, const CUtensorMap *tmq, const CUtensorMap
                                 size_t smem, cudaStream_t stream);
 const void *prefill_kernel_d64(int G);
 const void *prefill_kernel_d128(int G);
+cudaError_t launch_prefill_wide_d64(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                    const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                    size_t smem, cudaStream_t stream);
+cudaError_t launch_prefill_wide_d128(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                     const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                     size_t smem, cudaStream_t stream);
+const void *prefill_wide_kernel_d64(int G);
+const void *prefill_wide_kernel_d128(int G);
 
-cudaError_t launch_prefill(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+// wide: the kernel with 128-key tiles
+cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
                            const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
                            cudaStream_t stream)
 {
+    if (wide)
+        return D == 128 ? launch_prefill_wide_d128(G, tmq, tmk, tmv, p, grid, smem, stream)
+                        : launch_prefill_wide_d64(G, tmq, tmk, tmv, p, grid, smem, stream);
     return D == 128 ? launch_prefill_d128(G, tmq, tmk, tmv, p, grid, smem, stream)
                     : launch_prefill_d64(G, tmq, tmk, tmv, p, grid, smem, stream);
 }
 
-const void *prefill_kernel(int D, int G)
+const void *prefill_kernel(int D, int G, bool wide)
 {
+    if (wide)
+        return D == 128 ? prefill_wide_kernel_d128(G) : prefill_wide_kernel_d64(G);
     return D == 128 ? prefill_kernel_d128(G) : prefill_kernel_d64(G);
 }
 
-size_t prefill_smem_bytes(int D) { return tc_smem_layout(D).total; }
+size_t prefill_smem_bytes(int D, bool wide)
+{
+    return wide ? wide_smem_layout(D).total : tc_smem_layout(D).total;
+}
 
 // bt: tokens per box (16, or 32 for FP8 caches with block sizes divisible by 32)
 // weights: the kernels that also record every score for the attention weights
@@ -156,7 +174,7 @@ struct DeviceState {
     int dev = 0;
     int sms = 0;
     bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
-    bool pf_smem_set[2][9] = {};     // prefill: [D == 128][G]
+    bool pf_smem_set[2][2][9] = {};  // prefill: [128-key tiles][D == 128][G]
     bool pw_smem_set[2][9] = {};     // its weights kernel: [D == 128][G]
     bool evict_smem_set = false;
 };
@@ -773,11 +791,12 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     pkv_status ps = device_state(&st);
     if (ps != PKV_OK)
         return ps;
-    const void *kfn = pkv::prefill_kernel(D, G);
-    const size_t smem = pkv::prefill_smem_bytes(D);
+    const bool wide = record;  // the calls that record take the 128-key kernel
+    const void *kfn = pkv::prefill_kernel(D, G, wide);
+    const size_t smem = pkv::prefill_smem_bytes(D, wide);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->pf_smem_set[D == 128][G];
+        bool &set = st->pf_smem_set[wide][D == 128][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem);
@@ -788,10 +807,12 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     }
     CUtensorMap tmq, tmk, tmv;
     const long long tokens = (long long)NB * bs;
-    // blocks of whole 64-token tiles: one copy per K or V tile; else K one
-    // copy per 16-token box and 64-column half, V one per box
+    // blocks of whole 64-token tiles: one copy per K or V tile (128-key kernel: K
+    // one per 64 tokens and 64-column half, V one per 64 tokens); else K one copy
+    // per 16-token box and 64-column half, V one per box
     const bool tile_copies = bs % pkv::kPrefillKeys == 0;
-    if ((ps = cached_cache_map(&tmk, k_cache, tokens, Hkv, D, tile_copies ? kMapTile : kMapBox)) != PKV_OK)
+    const int kmap = !tile_copies ? kMapBox : wide ? kMapRun : kMapTile;
+    if ((ps = cached_cache_map(&tmk, k_cache, tokens, Hkv, D, kmap)) != PKV_OK)
         return ps;
     if ((ps = cached_cache_map(&tmv, v_cache, tokens, Hkv, D, tile_copies ? kMapTile : kMapBoxHalves)) !=
         PKV_OK)
@@ -818,7 +839,6 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
     p.neg_scale = scale < 0.f;
     p.tile_copies = tile_copies ? 1 : 0;
-    CUtensorMap tmw;  // the weights kernel's view of K
     if (record) {
         p.lse = static_cast<float *>(workspace);
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
@@ -833,9 +853,6 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
             set = true;
         }
     }
-    if (record &&
-        (ps = cached_cache_map(&tmw, k_cache, tokens, Hkv, D, tile_copies ? kMapRun : kMapBox)) != PKV_OK)
-        return ps;
     // Persistent grid: one CTA per SM (each holds all of the SM's TMEM
     // columns, and asks for more than half of its shared memory so that no
     // second CTA lands beside it), each walking its share of the work items.
@@ -845,12 +862,12 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         grid = p.n_items;
     if (grid < 1)
         return PKV_OK;
-    cudaError_t e = pkv::launch_prefill(D, G, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
+    cudaError_t e = pkv::launch_prefill(D, G, wide, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
                                         smem, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_prefill launch: %s", cudaGetErrorString(e));
     if (record) {
-        e = pkv::launch_prompt_weights(D, G, &tmq, &tmw, p, weights, window, st->sms,
+        e = pkv::launch_prompt_weights(D, G, &tmq, &tmk, p, weights, window, st->sms,
                                        static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
             return fail(PKV_ERR_CUDA, "paged_prefill_weights launch: %s", cudaGetErrorString(e));

@@ -28,7 +28,7 @@ struct PrefillParams {
     int32_t *ticket = nullptr;    // nullable: work counter of the weights kernel, cleared here
 };
 
-cudaError_t launch_prefill(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
                            const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
                            cudaStream_t stream);
 cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
@@ -36,8 +36,8 @@ cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CU
                                   cudaStream_t stream);
 const void *prompt_weights_kernel_fn(int D, int G);
 size_t prompt_weights_smem_bytes(int D);
-const void *prefill_kernel(int D, int G);
-size_t prefill_smem_bytes(int D);
+const void *prefill_kernel(int D, int G, bool wide);
+size_t prefill_smem_bytes(int D, bool wide);
 constexpr int kPrefillRows = 128;  // (token, head) rows per query tile (two tiles per work item)
 constexpr int kPrefillKeys = 64;   // keys per K/V tile
 constexpr int kPrefillThreads = 11 * 32;

@@ -1,0 +1,16 @@
+// Instantiations of the paged prefill kernel with 128-key tiles (tcgen05),
+// head_dim 64, G = 1, 2, 4, 8.
+#include "pkv_prefill_wide.cuh"
+
+namespace pkv {
+
+cudaError_t launch_prefill_wide_d64(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                    const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                    size_t smem, cudaStream_t stream)
+{
+    return launch_prefill_wide_d<64>(G, tmq, tmk, tmv, p, grid, smem, stream);
+}
+
+const void *prefill_wide_kernel_d64(int G) { return prefill_wide_kernel_d<64>(G); }
+
+} // namespace pkv

@@ -56,9 +56,9 @@ constexpr int kWKStages = 2;  // K ring
 constexpr int kWVStages = 3;  // V ring: one more, a V tile is held from its copy through
                               // the conversion to the second query tile's P.V
 // q_full[2], q_empty[2], k_full, k_empty [kWKStages] each, v_full, v_empty, v_conv
-// [kWVStages] each, per query tile s_full, pv_ready, pv_done, o_free, then
-// item_ready[2], item_free[2], mma_done
-constexpr int kWBars = 4 + 2 * kWKStages + 3 * kWVStages + 8 + 4 + 1;
+// [kWVStages] each, per query tile s_full, pv_ready[2 halves], pv_done, o_free,
+// then item_ready[2], item_free[2], mma_done
+constexpr int kWBars = 4 + 2 * kWKStages + 3 * kWVStages + 10 + 4 + 1;
 
 struct WideSmem {
     size_t q, k, v, bars, items, slot, total;
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t *v_empty = v_full + kWVStages;       // both tiles' P.V of the V tile completed
     uint64_t *v_conv = v_empty + kWVStages;       // the V tile converted to f16 (8 warps)
     uint64_t *s_full = v_conv + kWVStages;        // [2] S_t written
-    uint64_t *pv_ready = s_full + 2;              // [2] P_t written over it (4 warps)
-    uint64_t *pv_done = pv_ready + 2;             // [2] P.V_t completed
+    uint64_t *pv_ready = s_full + 2;              // [half of the keys][2] P_t written (4 warps)
+    uint64_t *pv_done = pv_ready + 4;             // [2] P.V_t completed
     uint64_t *o_free = pv_done + 2;               // [2] O_t read out by its epilogue (4 warps)
     uint64_t *item_ready = o_free + 2;            // [2] item parameters published
     uint64_t *item_free = item_ready + 2;         // [2] ... no longer needed
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&q_empty[t], 1);
             mbar_init(&s_full[t], 1);
             mbar_init(&pv_ready[t], 4);
+            mbar_init(&pv_ready[2 + t], 4);
             mbar_init(&pv_done[t], 1);
             mbar_init(&o_free[t], 4);
             mbar_init(&item_ready[t], 1);
@@ -413,20 +414,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         break;
                     if (j + 1 < nk && !(ok = landed(j + 1)))
                         break;
-                    if (!(ok = mbar_wait(&pv_ready[t], gq & 1)))
-                        break;
-                    if (!(ok = turn.take()))
-                        break;
-                    tc::fence_after();
+                    // keys 64 .. 127 first: their P is written first, and their MMAs run
+                    // while the softmax is at the other half
                     const uint32_t va = smem_u32(sV + (size_t)s * kTile);
+                    auto pv = [&](int half, bool add) {
+                        tc::fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < kWKeys / 16; kk++) {
-                        const uint32_t vk = p.tile_copies ? (uint32_t)(kk >> 2) * (kPrefillKeys * 128 * HALVES) +
-                                                                (uint32_t)(kk & 3) * 2048
-                                                          : (uint32_t)kk * kBoxBytes;
-                        const uint32_t pk = dS + (kk < 4 ? 8u * kk : 96u + 8u * (kk - 4));
-                        tc::mma_ts(dO, pk, tc::smem_desc(va + vk, v_lbo, 1024), idO, (j > 0 || kk > 0) ? 1u : 0u);
-                    }
+                        for (int i = 0; i < 4; i++) {
+                            const int kk = 4 * half + i;
+                            const uint32_t vk = p.tile_copies ? (uint32_t)half * (kPrefillKeys * 128 * HALVES) +
+                                                                    (uint32_t)i * 2048
+                                                              : (uint32_t)kk * kBoxBytes;
+                            tc::mma_ts(dO, dS + 96u * half + 8u * i, tc::smem_desc(va + vk, v_lbo, 1024), idO,
+                                       (add || i > 0) ? 1u : 0u);
+                        }
+                    };
+                    if (!(ok = mbar_wait(&pv_ready[2 + t], gq & 1)) || !(ok = turn.take()))
+                        break;
+                    pv(1, j > 0);
+                    turn.pass();
+                    if (!(ok = mbar_wait(&pv_ready[t], gq & 1)) || !(ok = turn.take()))
+                        break;
+                    pv(0, true);
                     tc::commit(smem_u32(&pv_done[t]));
                     // S_t(j + 1) overwrites P_t(j)
                     ok = mbar_wait(&pv_done[t], gq & 1);
@@ -651,15 +660,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tc::st32(to, pk);
                 };
+                auto hand_over = [&](int half) {
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&pv_ready[2 * half + tq]);
+                };
                 exponentiate(tS + 96);  // keys 64..127, over score columns read above
+                hand_over(1);
                 load(0);                // keys 0..63 again
                 exponentiate(tS);
                 l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
-                tc::wait_st();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&pv_ready[tq]);
+                hand_over(0);
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
                 if (j + 1 < all && !(ok = convert_v(j + 1, boxes_next)))
                     break;

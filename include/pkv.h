@@ -376,8 +376,9 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
 /*
  * pkv_paged_prefill_weights - pkv_paged_prefill that also records.
  *
- * Arguments, limits, flags and `out` as in pkv_paged_prefill (bit for bit),
- * plus
+ * Arguments, limits, flags, precision and `out` as in pkv_paged_prefill (out
+ * within rounding: this call's attention takes key tiles of 128, so its running
+ * maxima move at other keys), plus
  *   weights    above
  *   window     0: every new token's queries are recorded; w >= 1: only those
  *              of each sequence's last w new tokens (all, where it has fewer);

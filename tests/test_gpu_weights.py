@@ -272,6 +272,75 @@ def test_prompt_weights_neighbour_nan_stays_out(pkv):
                           ref.weight_tolerance(64, big), f"sequence {b}")
 
 
+@pytest.mark.parametrize("B", [40, 300])
+def test_prompt_weights_many_sequences(pkv, B):
+    """More sequences than one warp scans at once, and than the longest-first schedule ranks."""
+    r = np.random.default_rng(B)
+    q_lens = r.integers(0, 12, size=B)
+    check_prompt(pkv, ref.Cache(q_lens + r.integers(0, 20, size=B), 16, 1, 64, seed=B), q_lens, 4, window=6, max_q=12)
+
+
+def test_prompt_weights_tiny_and_large_values(pkv):
+    """V is rounded to f16 for P.V: beyond its range it is clamped and flagged, far below it becomes subnormal."""
+    c = ref.Cache([70, 200], 16, 2, 64, seed=4)
+    v = np.where(np.isnan(ref.from_bf16(c.v)), np.nan, ref.from_bf16(c.v) * 2.0 ** -20)
+    c.v = ref.to_bf16(v.astype(np.float32))
+    d = check_prompt(pkv, c, [30, 200], 2)
+    c = ref.Cache([70, 200], 16, 2, 64, seed=4)
+    s = c.slots(1)[:5]
+    c.v.reshape(-1, 2, 64)[s] = ref.to_bf16(np.full((5, 2, 64), 65280, dtype=np.float32))  # the last that fits
+    d = Dev(c)
+    cu = torch.tensor([0, 70, 270], dtype=torch.int32, device="cuda")
+    q = bf(queries(270, 4, 64, 0))
+    run = lambda out: pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cu, cu, 200, 0.125, out, d.w, err_flag=d.err)
+    run(torch.empty_like(q))
+    assert int(d.err.item()) == 0
+    d.v.view(-1, 2, 64)[torch.from_numpy(s).cuda()] = 1e6
+    assert torch.isfinite(run(torch.empty_like(q))).all()
+    assert int(d.err.item()) == 0x10  # FLAG_V_RANGE
+
+
+@pytest.mark.parametrize("idx", [1, 2, 3])
+def test_prompt_weights_full_size_steps(pkv, idx):
+    """The 16k-token steps: out against the oracle over every row, and the weights against what every softmax
+    adds up to: each sequence and KV head receives G per recorded query in all.  Five runs give the same bits
+    where no block is shared (shared prefixes receive their additions in any order)."""
+    import oracle
+    from paged_kv_cache_85_gb300 import workload as wl
+
+    p = wl.prefill_config_workload(idx)
+    kc, vc, bad = oracle.store_kvcache(p.k_new, p.v_new, p.k_cache, p.v_cache, p.slot_mapping)
+    want = oracle.paged_prefill(p.q, kc, vc, p.block_tables, p.cu_seqlens_q, p.cu_seqlens_k, p.scale, threads=oracle.host_cores())
+    q, k, v = bf(p.q), bf(kc), bf(vc)
+    t, cq, ck = (torch.from_numpy(x).cuda() for x in (p.block_tables, p.cu_seqlens_q, p.cu_seqlens_k))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = None
+    for run in range(5):
+        w = torch.zeros(p.NB, p.Hkv, p.bs, device="cuda")
+        out = pkv.paged_prefill_weights(q, k, v, t, cq, ck, p.max_seqlen_q, p.scale, torch.empty_like(q), w, err_flag=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        if first is None:
+            first = (out, w)
+        assert torch.equal(out, first[0])
+        if idx != 3:
+            assert torch.equal(w, first[1])
+    off = np.abs(out.float().cpu().numpy() - want)
+    assert off.max() <= 1e-2 and off.mean() <= 1e-3, (off.max(), off.mean())
+    # each row's softmax sums to 1 within weight_tolerance (|score| sums below 40 for N(0, 1) inputs), and so do
+    # their sums; the fp32 weights themselves are summed in 64 bits
+    total = float(first[1].double().sum())
+    rows = float(p.Tq) * p.Hq
+    assert abs(total - rows) <= ref.weight_tolerance(p.D, 40) * rows
+    if idx != 3:
+        flat = first[1].double().sum(1).cpu().numpy().reshape(p.NB, p.bs)  # over KV heads
+        for b in range(p.B):
+            n = int(p.k_lens[b])
+            s = np.arange(n)
+            got = flat[p.block_tables[b, s // p.bs], s % p.bs].sum()
+            assert abs(got - p.q_lens[b] * p.Hq) <= ref.weight_tolerance(p.D, 40) * p.q_lens[b] * p.Hq
+
+
 # ------------------------------------------------------------------ eviction
 
 

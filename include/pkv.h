@@ -384,14 +384,18 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
  *              of each sequence's last w new tokens (all, where it has fewer);
  *              new tokens still have their weight set, to 0 where no recorded
  *              query sees them
- *   workspace  device scratch of pkv_prefill_weights_workspace_bytes(Tq, Hq)
- *              bytes, 16-byte aligned (every row's log-sum-exp)
+ *   workspace  device scratch of pkv_prefill_weights_workspace_bytes bytes for
+ *              the same sizes, 16-byte aligned: every row's log-sum-exp, and,
+ *              where max_seqlen_q, B and the heads make fewer than 152 items of
+ *              256 (new token, head) rows, partial outputs of the keys' splits
+ *              (at most some 45 MB)
  * B * Hkv * MBS * bs / 128 < 2^31.  A sequence that the attention skips
  * records nothing.  The scores of the recorded queries are made a second time
  * (their weights need each row's final sum), so recording every query adds
  * half of the attention's multiplications; a window adds little.
  */
-size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq);
+size_t pkv_prefill_weights_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
+                                           int D, int MBS, int bs);
 
 pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const void *v_cache,
                                      const int32_t *block_tables, int MBS,

@@ -120,7 +120,7 @@ def load_library():
         lib.pkv_paged_attn_decode_weights_fp8.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64,
                                                           i32, f32, f32, f32, P, P, P, sz, i32, P, P]
         lib.pkv_prefill_weights_workspace_bytes.restype = sz
-        lib.pkv_prefill_weights_workspace_bytes.argtypes = [i64, i32]
+        lib.pkv_prefill_weights_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32, i32]
         lib.pkv_paged_prefill_weights.restype = i32
         lib.pkv_paged_prefill_weights.argtypes = [P, P, P, P, i32, P, P, i32, i64, i32, i32, i32, i32,
                                                   i64, i32, f32, P, P, i32, P, sz, P, P]
@@ -389,9 +389,9 @@ def decode_weights_workspace_bytes(B, Hq, Hkv, D, MBS, bs, max_ctas=0) -> int:
     return int(load_library().pkv_decode_weights_workspace_bytes(B, Hq, Hkv, D, MBS, bs, max_ctas))
 
 
-def prefill_weights_workspace_bytes(Tq, Hq) -> int:
-    """Workspace bytes paged_prefill_weights needs."""
-    return int(load_library().pkv_prefill_weights_workspace_bytes(Tq, Hq))
+def prefill_weights_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs) -> int:
+    """Workspace bytes paged_prefill_weights needs for these sizes."""
+    return int(load_library().pkv_prefill_weights_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs))
 
 
 def evict_workspace_bytes(B, Hkv, MBS, bs, budget) -> int:
@@ -568,15 +568,16 @@ def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_se
         raise ValueError("cu_seqlens / block_tables batch sizes differ")
     _result(torch, dev, out, q)
     flag = _flag(torch, dev, err_flag)
+    MBS, max_seqlen_q = max(block_tables.shape[1], 1), int(max_seqlen_q)
     lib = _lib or load_library()
     with _on_device(dev):
         stream = _raw_stream(dev)
         ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
-            "pkv_prefill_weights_workspace_bytes", Tq, Hq), dev, stream)
+            "pkv_prefill_weights_workspace_bytes", B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs), dev, stream)
         _check(lib.pkv_paged_prefill_weights(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            max(block_tables.shape[1], 1), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
-            int(max_seqlen_q), Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), weights.data_ptr(),
+            MBS, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
+            max_seqlen_q, Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), weights.data_ptr(),
             int(window), ws_ptr, ws_bytes, flag, stream))
     return out
 

@@ -62,8 +62,8 @@ cudaError_t launch_prefill_wide_d64(int G, const CUtensorMap *tmq, const CUtenso
 cudaError_t launch_prefill_wide_d128(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
                                      const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
                                      size_t smem, cudaStream_t stream);
-const void *prefill_wide_kernel_d64(int G);
-const void *prefill_wide_kernel_d128(int G);
+const void *prefill_wide_kernel_d64(int G, bool split);
+const void *prefill_wide_kernel_d128(int G, bool split);
 
 // wide: the kernel with 128-key tiles
 cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
@@ -77,10 +77,10 @@ cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, cons
                     : launch_prefill_d64(G, tmq, tmk, tmv, p, grid, smem, stream);
 }
 
-const void *prefill_kernel(int D, int G, bool wide)
+const void *prefill_kernel(int D, int G, bool wide, bool split)
 {
     if (wide)
-        return D == 128 ? prefill_wide_kernel_d128(G) : prefill_wide_kernel_d64(G);
+        return D == 128 ? prefill_wide_kernel_d128(G, split) : prefill_wide_kernel_d64(G, split);
     return D == 128 ? prefill_kernel_d128(G) : prefill_kernel_d64(G);
 }
 
@@ -174,7 +174,7 @@ struct DeviceState {
     int dev = 0;
     int sms = 0;
     bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
-    bool pf_smem_set[2][2][9] = {};  // prefill: [128-key tiles][D == 128][G]
+    bool pf_smem_set[3][2][9] = {};  // prefill: [64-key tiles, 128, 128 split][D == 128][G]
     bool pw_smem_set[2][9] = {};     // its weights kernel: [D == 128][G]
     bool evict_smem_set = false;
 };
@@ -731,6 +731,15 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
 
 } // extern "C"
 
+// Splits over the keys of a recording prefill's items (query tile pairs of one
+// sequence and KV head), from the sizes alone.
+static int prefill_splits(int B, int max_seqlen_q, int Hq, int Hkv, int MBS, int bs)
+{
+    const long long pairs = ((long long)max_seqlen_q * (Hq / Hkv) + 2 * pkv::kPrefillRows - 1) /
+                            (2 * pkv::kPrefillRows);
+    return pkv::wide_splits(pairs * Hkv * B, (long long)MBS * bs);
+}
+
 // record: also leave every row's log-sum-exp in the workspace and add the
 // attention weights (pkv_paged_prefill_weights)
 static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v_cache,
@@ -776,7 +785,8 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (record) {
         if (!weights || !aligned16(weights))
             return fail(PKV_ERR_INVALID_ARG, "paged_prefill_weights: weights null or misaligned");
-        const size_t need = pkv_prefill_weights_workspace_bytes(Tq, Hq);
+        const size_t need =
+            pkv_prefill_weights_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs);
         if (!workspace || !aligned16(workspace) || workspace_bytes < need)
             return fail(PKV_ERR_WORKSPACE, "paged_prefill_weights: workspace needs %zu bytes "
                         "(16-byte aligned), got %zu", need, workspace ? workspace_bytes : (size_t)0);
@@ -792,11 +802,12 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (ps != PKV_OK)
         return ps;
     const bool wide = record;  // the calls that record take the 128-key kernel
-    const void *kfn = pkv::prefill_kernel(D, G, wide);
+    const int splits = record ? prefill_splits(B, max_seqlen_q, Hq, Hkv, MBS, bs) : 1;
+    const void *kfn = pkv::prefill_kernel(D, G, wide, splits > 1);
     const size_t smem = pkv::prefill_smem_bytes(D, wide);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->pf_smem_set[wide][D == 128][G];
+        bool &set = st->pf_smem_set[wide ? 1 + (splits > 1) : 0][D == 128][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem);
@@ -842,6 +853,14 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (record) {
         p.lse = static_cast<float *>(workspace);
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
+        p.splits = splits;
+        if (p.splits > 1) {
+            uint8_t *ws = static_cast<uint8_t *>(workspace) +
+                          pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
+            p.part_lse = reinterpret_cast<float *>(ws);
+            ws += pkv::align_up((size_t)p.splits * Tq * Hq * sizeof(float), 256);
+            p.part_out = reinterpret_cast<float *>(ws);
+        }
         const void *wfn = pkv::prompt_weights_kernel_fn(D, G);
         std::lock_guard<std::mutex> lk(g_mu);
         bool &set = st->pw_smem_set[D == 128][G];
@@ -858,14 +877,19 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     // second CTA lands beside it), each walking its share of the work items.
     static_assert(pkv::kPrefillThreads * 168 <= 65536, "prefill registers per thread");
     long long grid = (long long)st->sms;
-    if (grid > p.n_items)
-        grid = p.n_items;
+    if (grid > (long long)p.n_items * p.splits)
+        grid = (long long)p.n_items * p.splits;
     if (grid < 1)
         return PKV_OK;
     cudaError_t e = pkv::launch_prefill(D, G, wide, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
                                         smem, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_prefill launch: %s", cudaGetErrorString(e));
+    if (p.splits > 1) {
+        e = pkv::launch_prefill_join(D, p, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return fail(PKV_ERR_CUDA, "paged_prefill_weights join launch: %s", cudaGetErrorString(e));
+    }
     if (record) {
         e = pkv::launch_prompt_weights(D, G, &tmq, &tmk, p, weights, window, st->sms,
                                        static_cast<cudaStream_t>(stream));
@@ -887,10 +911,19 @@ pkv_status pkv_paged_prefill(const void *q, const void *k_cache, const void *v_c
                         max_seqlen_q, Hq, Hkv, D, NB, bs, scale, out, err_flag, stream);
 }
 
-size_t pkv_prefill_weights_workspace_bytes(int64_t Tq, int Hq)
+size_t pkv_prefill_weights_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
+                                           int D, int MBS, int bs)
 {
-    // every row's log-sum-exp, and the weights kernel's work counter
-    return Tq < 1 || Hq < 1 ? 0 : pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
+    if (B < 1 || Tq < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || MBS < 1 || bs < 1)
+        return 0;
+    const size_t rows = (size_t)Tq * Hq;
+    // every row's log-sum-exp and the weights kernel's work counter; where the items
+    // are split, the splits' outputs and log-sum-exps
+    size_t n = pkv::align_up(rows * sizeof(float) + sizeof(int32_t), 256);
+    const int splits = prefill_splits(B, max_seqlen_q, Hq, Hkv, MBS, bs);
+    if (splits > 1)
+        n += pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float);
+    return n;
 }
 
 pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const void *v_cache,

@@ -25,6 +25,10 @@ struct PrefillParams {
     int neg_scale;                // scale < 0: the score MMA negates Q
     int tile_copies;              // bs % 64 == 0: K/V maps copy whole 64-token tiles
     float *lse = nullptr;         // nullable: [Hkv, Tq, G] log-sum-exp of every row (log2 units)
+    // 128-key kernel, where its items are split over the keys (splits > 1)
+    int splits = 1;
+    float *part_out = nullptr;    // [splits, Tq, Hq, D] outputs of the splits
+    float *part_lse = nullptr;    // [splits, Hkv, Tq, G] their log-sum-exps, -inf: no key
     int32_t *ticket = nullptr;    // nullable: work counter of the weights kernel, cleared here
 };
 
@@ -36,8 +40,31 @@ cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CU
                                   cudaStream_t stream);
 const void *prompt_weights_kernel_fn(int D, int G);
 size_t prompt_weights_smem_bytes(int D);
-const void *prefill_kernel(int D, int G, bool wide);
+const void *prefill_kernel(int D, int G, bool wide, bool split);
 size_t prefill_smem_bytes(int D, bool wide);
+// Key tiles (of 128) per split of an item of nkt tiles; its splits are
+// ceil(nkt / chunk) <= splits.
+constexpr int kMinSplitTiles = 4;
+__host__ __device__ inline int wide_chunk(int nkt, int splits)
+{
+    const int chunk = (nkt + splits - 1) / splits;
+    return chunk < kMinSplitTiles ? kMinSplitTiles : chunk;
+}
+// Splits of a call: enough to give two items to every SM of a large GPU where
+// the query tile pairs alone do not give it one, and none shorter than
+// kMinSplitTiles tiles of the longest context.
+inline int wide_splits(long long items, long long max_ctx)
+{
+    constexpr long long kFew = 152, kWant = 304;
+    if (items < 1 || items >= kFew)
+        return 1;
+    const long long tiles = (max_ctx + 127) / 128;
+    long long s = (kWant + items - 1) / items;
+    if (s > tiles / kMinSplitTiles)
+        s = tiles / kMinSplitTiles;
+    return s < 1 ? 1 : (int)s;
+}
+cudaError_t launch_prefill_join(int D, const PrefillParams &p, cudaStream_t stream);
 constexpr int kPrefillRows = 128;  // (token, head) rows per query tile (two tiles per work item)
 constexpr int kPrefillKeys = 64;   // keys per K/V tile
 constexpr int kPrefillThreads = 11 * 32;

@@ -1,0 +1,113 @@
+// Joins the splits of the 128-key prefill kernel's items.
+//
+// Split i of a row's keys left o_i = sum 2^(s - lse_i) v (fp32, normalised) and
+// lse_i = log2 sum 2^s.  With L = log2 sum_i 2^lse_i,
+//     out = sum_i 2^(lse_i - L) o_i,
+// and L is the row's log-sum-exp for the attention weights (+inf where no split
+// could read a key: weight 0, output 0).  The splits of a row follow from its
+// sequence's lengths as in the prefill kernel.
+//
+// One warp per (row, query head).  Read once, a few MB at most (the call splits
+// only where its rows are few): bound by its latency, which is why the
+// sequences' boundaries are searched in shared memory.
+#include <cuda_bf16.h>
+
+#include "pkv_kernels.h"
+#include "pkv_prefill.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+
+constexpr int kJoinWarps = 8;
+constexpr int kJoinMaxSeqs = 152;  // more sequences are more items than are split
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillParams p)
+{
+    __shared__ int cq[kJoinMaxSeqs + 1], ck[kJoinMaxSeqs + 1];
+    constexpr int DPL = D / 32;
+    constexpr unsigned FULL = 0xffffffffu;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int i = threadIdx.x; i <= p.B; i += kJoinWarps * 32) {
+        cq[i] = p.cu_q[i];
+        ck[i] = p.cu_k[i];
+    }
+    __syncthreads();
+    const long long at = (long long)blockIdx.x * kJoinWarps + warp;
+    if (at >= p.Tq * p.Hq)
+        return;
+    const int row = (int)(at / p.Hq), hq = (int)(at % p.Hq);
+    const int G = p.Hq / p.Hkv, kvh = hq / G, g = hq - kvh * G;
+    // the sequence that holds the row: boundaries need not be sane, so every one is
+    // looked at
+    int b = -1;
+    for (int i = lane; i < p.B; i += 32)
+        if (cq[i] <= row && row < cq[i + 1])
+            b = i;
+    b = __reduce_max_sync(FULL, b);
+    if (b < 0)
+        return;
+    const int q_len = cq[b + 1] - cq[b], k_len = ck[b + 1] - ck[b];
+    // the sequences that the attention takes (prefill_seq_sane)
+    if (cq[b] < 0 || (long long)cq[b + 1] > p.Tq || k_len < q_len ||
+        (long long)k_len > (long long)p.MBS * p.bs || q_len > p.max_q)
+        return;
+    // key tiles of the row's item: a pair of query tiles of 128 / G tokens each
+    const int tpc = kPrefillRows / G, tok0 = (row - cq[b]) / (2 * tpc) * (2 * tpc);
+    const int nkt = (k_len - q_len + min(q_len, tok0 + 2 * tpc) - 1) / 128 + 1;
+    const int chunk = wide_chunk(nkt, p.splits), n = (nkt + chunk - 1) / chunk;
+
+    const size_t lse_at = ((size_t)kvh * p.Tq + row) * G + g, stride = (size_t)p.Tq * p.Hq;
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        M = fmaxf(M, p.part_lse[i * stride + lse_at]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(FULL, M, off));
+    // a NaN log-sum-exp (NaN scores) does not show in the maximum: it comes in here
+    float acc[DPL], W = 0.f;
+#pragma unroll
+    for (int c = 0; c < DPL; c++)
+        acc[c] = 0.f;
+    const float *o = p.part_out + ((size_t)row * p.Hq + hq) * D + lane * DPL;
+#pragma unroll 4
+    for (int i = 0; i < n; i++) {
+        const float lse = p.part_lse[i * stride + lse_at];
+        const float w = lse == -INFINITY ? 0.f : fast_exp2(lse - (M == -INFINITY ? 0.f : M));
+        W += w;
+        float x[DPL];
+#pragma unroll
+        for (int c = 0; c < DPL; c++)
+            x[c] = o[i * stride * D + c];
+        if (lse != -INFINITY)
+#pragma unroll
+            for (int c = 0; c < DPL; c++)
+                acc[c] += w * x[c];
+    }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    uint16_t *dst = p.out + ((size_t)row * p.Hq + hq) * D + lane * DPL;
+#pragma unroll
+    for (int c = 0; c < DPL; c += 2)
+        *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0)
+        p.lse[lse_at] = W == 0.f ? INFINITY : (M == -INFINITY ? 0.f : M) + log2f(W);
+}
+
+cudaError_t launch_prefill_join(int D, const PrefillParams &p, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((p.Tq * p.Hq + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return D == 128 ? cudaLaunchKernelEx(&cfg, prefill_join_kernel<128>, p)
+                    : cudaLaunchKernelEx(&cfg, prefill_join_kernel<64>, p);
+}
+
+} // namespace pkv

@@ -23,6 +23,11 @@
 //    written over the last quarter of the score columns, and the first half is
 //    read again and its P written over the first quarter.
 //
+//  * Few rows over long contexts (a short chunk on a long prefix) leave most SMs
+//    without an item: the host then splits every item's key tiles over up to
+//    p.splits CTAs.  Each leaves its rows' outputs (fp32) and log-sum-exps in
+//    the workspace; pkv_prefill_join.cu puts them together.
+//
 // Warps (352 threads): 0..3 softmax of query tile A, 4..7 of tile B (thread =
 // row = TMEM lane); 8 producer; 9, 10 the MMAs of tiles A and B.
 // TMEM columns: O_A [0, D), O_B [128, 128 + D), S_A [256, 384), S_B [384, 512);
@@ -60,6 +65,12 @@ constexpr int kWVStages = 3;  // V ring: one more, a V tile is held from its cop
 // then item_ready[2], item_free[2], mma_done
 constexpr int kWBars = 4 + 2 * kWKStages + 3 * kWVStages + 10 + 4 + 1;
 
+// An item's share of the key tiles: tiles j0 .. j0 + nkt[t] - 1 of query tile t.
+struct WideItem {
+    PrefillItem f;
+    int j0, split, pad0, pad1;
+};
+
 struct WideSmem {
     size_t q, k, v, bars, items, slot, total;
 };
@@ -76,8 +87,8 @@ __host__ __device__ inline WideSmem wide_smem_layout(int D)
     o += (size_t)kWVStages * (D / 64) * kWKeys * 128;
     L.bars = o;
     o += 8 * kWBars;
-    L.items = align_up(o, 16);  // two published work items of 32 bytes
-    o = L.items + 2 * 32;
+    L.items = align_up(o, 16);  // two published work items
+    o = L.items + 2 * sizeof(WideItem);
     L.slot = o;  // TMEM base, and the MMA warps' lock
     o += 16;
     L.total = align_up(o, 16) + 1024;
@@ -86,7 +97,9 @@ __host__ __device__ inline WideSmem wide_smem_layout(int D)
     return L;
 }
 
-template <int D, int G>
+// SPLIT: p.splits > 1.  Of its own, for the others' items are 4% slower with it
+// where they are short.
+template <int D, int G, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_prefill_wide_kernel(const __grid_constant__ CUtensorMap tmq,
                               const __grid_constant__ CUtensorMap tmk,
@@ -102,6 +115,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kBoxes = kWKeys / kBox;          // 16-token boxes per tile
     constexpr unsigned FULL = 0xffffffffu;
     constexpr float kLazy = 8.f;
+    const int splits = SPLIT ? p.splits : 1;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -122,7 +136,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t *mma_done = item_free + 2;           // every MMA of the CTA completed
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
     const Turn turn{slot + 1};
-    PrefillItem *items = reinterpret_cast<PrefillItem *>(smem + L.items);
+    WideItem *items = reinterpret_cast<WideItem *>(smem + L.items);
     uint8_t *sQ = smem + L.q, *sK = smem + L.k, *sV = smem + L.v;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,13 +193,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int k = 0;                // walk rounds
         for (;;) {
             // ---- the next item with work (round k: forward, then backward), or the end
-            PrefillItem it{-1, 0, 0, 0, 0, 0, {0, 0}};
+            WideItem item{{-1, 0, 0, 0, 0, 0, {0, 0}}, 0, 0, 0, 0};
+            PrefillItem &it = item.f;
             for (; ok; k++) {
-                const long long pos = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
-                if (pos >= p.n_items)
+                const long long at = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
+                if (at >= (long long)p.n_items * splits)
                     break;
-                const PrefillWork w = p.B <= 32 ? prefill_schedule<2 * TPC, 1>(p, lane, (int)pos)
-                                                : prefill_schedule<2 * TPC, kSchedChunks>(p, lane, (int)pos);
+                const int pos = SPLIT ? (int)(at / splits) : (int)at;
+                const PrefillWork w = p.B <= 32 ? prefill_schedule<2 * TPC, 1>(p, lane, pos)
+                                                : prefill_schedule<2 * TPC, kSchedChunks>(p, lane, pos);
                 int cq0 = w.cq0, cq1 = w.cq1, ck0 = w.ck0, ck1 = w.ck1;
                 if (w.b >= 0 && cq0 == kNotLoaded) {
                     cq0 = __ldg(p.cu_q + w.b);
@@ -198,7 +214,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     flag_error(p.err_flag, 0x4 /* PKV_FLAG_BAD_CONTEXT_LEN */);
                 const int tok0 = w.tile * 2 * TPC;
                 if (sane && tok0 < cq1 - cq0) {
-                    it.b = w.b;
                     it.kvh = w.kvh;
                     it.tok0 = tok0;
                     it.cq0 = cq0;
@@ -209,6 +224,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     it.nkt[1] = tok0 + TPC < it.q_len
                                     ? (base + min(it.q_len, tok0 + 2 * TPC) - 1) / kWKeys + 1
                                     : 0;
+                    if constexpr (SPLIT) {
+                        const int chunk = wide_chunk(max(it.nkt[0], it.nkt[1]), splits);
+                        item.split = (int)(at - (long long)pos * splits);
+                        item.j0 = item.split * chunk;
+                        for (int t = 0; t < 2; t++)
+                            it.nkt[t] = min(max(it.nkt[t] - item.j0, 0), chunk);
+                        if (max(it.nkt[0], it.nkt[1]) == 0)
+                            continue;  // the item has fewer splits
+                    }
+                    it.b = w.b;
                     k++;
                     break;
                 }
@@ -226,14 +251,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok)
                 it.b = -1;
             if (lane == 0) {
-                items[sl] = it;
+                items[sl] = item;
                 mbar_arrive(&item_ready[sl]);
             }
             __syncwarp();
             if (it.b < 0)
                 break;
             // ---- Q tiles, each once its tile's last S of the previous item completed
-            for (int t = 0; t < (it.nkt[1] > 0 ? 2 : 1) && ok; t++) {
+            for (int t = 0; t < 2 && ok; t++) {
+                if (it.nkt[t] == 0)
+                    continue;
                 if (n >= 1 && !(ok = __all_sync(FULL, mbar_wait(&q_empty[t], (n - 1) & 1))))
                     break;
                 if (lane == 0) {
@@ -251,9 +278,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- K and V tiles through the two rings: whichever can go.  Lanes 0-7
             // resolve one 16-token box each, a tile ahead of its copy.
             const int nkt = max(it.nkt[0], it.nkt[1]);
+            const int j0 = SPLIT ? item.j0 : 0;
             const int32_t *table = p.block_tables + (size_t)it.b * p.MBS;
             auto entry = [&](int j) -> int {
-                const int key0 = j * kWKeys + lane * kBox;
+                const int key0 = (j0 + j) * kWKeys + lane * kBox;
                 return (lane < kBoxes && j < nkt && key0 < it.k_len) ? __ldg(table + key0 / p.bs) : -1;
             };
             int next_k = entry(0), next_v = next_k;
@@ -264,7 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int s = g % (is_k ? kWKStages : kWVStages);
                 const int blk = is_k ? next_k : next_v;
                 (is_k ? next_k : next_v) = entry(j + 1);
-                const int key0 = j * kWKeys + lane * kBox;
+                const int key0 = (j0 + j) * kWKeys + lane * kBox;
                 int row = -1;
                 if (lane < kBoxes && key0 < it.k_len) {
                     if (blk >= 0 && blk < p.NB)
@@ -368,7 +396,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int n = 0; ok; n++) {
                 if (!(ok = mbar_wait(&item_ready[n & 1], (n >> 1) & 1)))
                     break;
-                const PrefillItem it = items[n & 1];
+                const PrefillItem it = items[n & 1].f;
                 if (it.b < 0)
                     break;
                 const int nk = it.nkt[t];
@@ -486,10 +514,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ok = __all_sync(FULL, mbar_wait(&item_ready[n & 1], (n >> 1) & 1));
             if (!ok)
                 break;
-            const PrefillItem it = items[n & 1];
+            const WideItem item = items[n & 1];
+            const PrefillItem &it = item.f;
             if (it.b < 0)
                 break;
             const int nkt = it.nkt[tq], all = max(it.nkt[0], it.nkt[1]);
+            const int j0 = SPLIT ? item.j0 : 0;
             const int tok = it.tok0 + tq * TPC + r / G, g = r % G;
             const bool valid = tok < it.q_len;
             const int pos = (it.k_len - it.q_len) + tok;
@@ -500,7 +530,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // boxes of a tile that the producer loads (block ids in [0, NB)); lanes 0-7
             // read the entries a tile ahead
             auto table_entry = [&](int j) -> int {
-                const int key0 = j * kWKeys + lane * kBox;
+                const int key0 = (j0 + j) * kWKeys + lane * kBox;
                 return (lane < kBoxes && j < all && key0 < k_len) ? __ldg(table + key0 / p.bs) : -1;
             };
             auto loaded = [&](int blk) { return __ballot_sync(FULL, blk >= 0 && blk < p.NB) & 0xffu; };
@@ -508,7 +538,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // k_len or of unloaded boxes zeroed (their weight is 0, and 0 * NaN would be
             // NaN).  Both groups take part in every V tile of the item, in order.
             auto convert_v = [&](int j, uint32_t boxes) -> bool {
-                const int gv = g0 + j, s = gv % kWVStages, kb = j * kWKeys + 64 * tq;
+                const int gv = g0 + j, s = gv % kWVStages, kb = (j0 + j) * kWKeys + 64 * tq;
                 if (!__all_sync(FULL, mbar_wait(&v_full[s], (gv / kWVStages) & 1)))
                     return false;
                 uint4 *vt = reinterpret_cast<uint4 *>(sV + (size_t)s * kTile + tq * (kTile / 2));
@@ -567,7 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (j == nkt - 1)
                         mbar_arrive(&q_empty[tq]);
                 }
-                const int key_base = j * kWKeys;
+                const int key_base = (j0 + j) * kWKeys;
                 // masked keys: past this row's position (the diagonal tiles) or in an
                 // unloaded box; most tiles have none in the whole warp
                 const bool any_masked = __any_sync(FULL, boxes != 0xffu || key_base + kWKeys - 1 > pos);
@@ -691,6 +721,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // values at or below 65280 convert exactly, so only a clamp gives 0x7bff
             if ((vmax & 0x7fffu) >= 0x7bffu || ((vmax >> 16) & 0x7fffu) >= 0x7bffu)
                 flag_error(p.err_flag, kFlagVRange);
+            // a split that only the other query tile has keys in
+            if (SPLIT && nkt == 0 && valid)
+                p.part_lse[(size_t)item.split * p.Tq * p.Hq +
+                           ((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] = -INFINITY;
             if (nkt > 0) {
                 const int gl = gq + nkt - 1;
                 ok = __all_sync(FULL, mbar_wait(&pv_done[tq], gl & 1));
@@ -698,27 +732,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 tc::fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                // for the attention weights; +inf (weight 0) for a row that could
-                // read no key
-                if (p.lse && valid)
-                    p.lse[((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] =
-                        l == 0.f ? INFINITY : m + log2f(l);
-                uint16_t *dst = p.out + ((size_t)(it.cq0 + tok) * p.Hq + it.kvh * G + g) * D;
+                const size_t row = (size_t)it.cq0 + tok;
+                const size_t lse_at = ((size_t)it.kvh * p.Tq + row) * G + g;
+                if constexpr (SPLIT) {
+                    // this split's output in fp32, and its log-sum-exp (-inf: no key)
+                    if (valid)
+                        p.part_lse[(size_t)item.split * p.Tq * p.Hq + lse_at] =
+                            l == 0.f ? -INFINITY : m + log2f(l);
+                    float4 *dst = reinterpret_cast<float4 *>(
+                        p.part_out + (((size_t)item.split * p.Tq + row) * p.Hq + it.kvh * G + g) * D);
 #pragma unroll 1
-                for (int cc = 0; cc < D / 32; cc++) {
-                    uint32_t ro[32];
-                    tc::ld32(tO + 32 * cc, ro);
-                    tc::wait_ld();
-                    if (valid) {
-                        uint32_t pk[16];
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t ro[32];
+                        tc::ld32(tO + 32 * cc, ro);
+                        tc::wait_ld();
+                        if (valid) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            pk[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv,
-                                                __uint_as_float(ro[2 * i + 1]) * inv);
-                        uint4 *d4 = reinterpret_cast<uint4 *>(dst + 32 * cc);
+                            for (int i = 0; i < 8; i++)
+                                dst[8 * cc + i] = make_float4(__uint_as_float(ro[4 * i]) * inv,
+                                                              __uint_as_float(ro[4 * i + 1]) * inv,
+                                                              __uint_as_float(ro[4 * i + 2]) * inv,
+                                                              __uint_as_float(ro[4 * i + 3]) * inv);
+                        }
+                    }
+                } else {
+                    // for the attention weights; +inf (weight 0) for a row that could
+                    // read no key
+                    if (valid)
+                        p.lse[lse_at] = l == 0.f ? INFINITY : m + log2f(l);
+                    uint16_t *dst = p.out + (row * p.Hq + it.kvh * G + g) * D;
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t ro[32];
+                        tc::ld32(tO + 32 * cc, ro);
+                        tc::wait_ld();
+                        if (valid) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                            for (int i = 0; i < 16; i++)
+                                pk[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv,
+                                                    __uint_as_float(ro[2 * i + 1]) * inv);
+                            uint4 *d4 = reinterpret_cast<uint4 *>(dst + 32 * cc);
+#pragma unroll
+                            for (int i = 0; i < 4; i++)
+                                d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        }
                     }
                 }
                 tc::fence_before();
@@ -759,21 +817,37 @@ inline cudaError_t launch_prefill_wide_d(int G, const CUtensorMap *tmq, const CU
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (G) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 1>, *tmq, *tmk, *tmv, p);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 2>, *tmq, *tmk, *tmv, p);
-    case 4: return cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 4>, *tmq, *tmk, *tmv, p);
-    case 8: return cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 8>, *tmq, *tmk, *tmv, p);
+    case 1:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 1, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 1, false>, *tmq, *tmk, *tmv, p);
+    case 2:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 2, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 2, false>, *tmq, *tmk, *tmv, p);
+    case 4:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 4, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 4, false>, *tmq, *tmk, *tmv, p);
+    case 8:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 8, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_wide_kernel<D, 8, false>, *tmq, *tmk, *tmv, p);
     default: return cudaErrorInvalidValue;
     }
 }
 
-template <int D> inline const void *prefill_wide_kernel_d(int G)
+template <int D> inline const void *prefill_wide_kernel_d(int G, bool split)
 {
     switch (G) {
-    case 1: return reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 1>);
-    case 2: return reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 2>);
-    case 4: return reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 4>);
-    case 8: return reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 8>);
+    case 1:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 1, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 1, false>);
+    case 2:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 2, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 2, false>);
+    case 4:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 4, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 4, false>);
+    case 8:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 8, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_wide_kernel<D, 8, false>);
     default: return nullptr;
     }
 }

@@ -11,6 +11,9 @@ cudaError_t launch_prefill_wide_d128(int G, const CUtensorMap *tmq, const CUtens
     return launch_prefill_wide_d<128>(G, tmq, tmk, tmv, p, grid, smem, stream);
 }
 
-const void *prefill_wide_kernel_d128(int G) { return prefill_wide_kernel_d<128>(G); }
+const void *prefill_wide_kernel_d128(int G, bool split)
+{
+    return prefill_wide_kernel_d<128>(G, split);
+}
 
 } // namespace pkv

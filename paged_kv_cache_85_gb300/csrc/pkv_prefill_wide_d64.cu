@@ -11,6 +11,9 @@ cudaError_t launch_prefill_wide_d64(int G, const CUtensorMap *tmq, const CUtenso
     return launch_prefill_wide_d<64>(G, tmq, tmk, tmv, p, grid, smem, stream);
 }
 
-const void *prefill_wide_kernel_d64(int G) { return prefill_wide_kernel_d<64>(G); }
+const void *prefill_wide_kernel_d64(int G, bool split)
+{
+    return prefill_wide_kernel_d<64>(G, split);
+}
 
 } // namespace pkv

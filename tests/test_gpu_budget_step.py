@@ -289,7 +289,7 @@ def test_workspace_given_by_the_caller(pkv):
     calls = [
         (pkv.decode_weights_workspace_bytes(3, 4, 2, 64, MBS, 16),
          lambda w, ws: pkv.paged_attn_decode_weights(q, k, v, t, n, 0.1, torch.empty_like(q), w, workspace=ws)),
-        (pkv.prefill_weights_workspace_bytes(3, 4),
+        (pkv.prefill_weights_workspace_bytes(3, 3, 1, 4, 2, 64, MBS, 16),
          lambda w, ws: pkv.paged_prefill_weights(q, k, v, t, cu, ck, 1, 0.1, torch.empty_like(q), w, workspace=ws)),
         (pkv.evict_workspace_bytes(3, 2, MBS, 16, 50),
          lambda w, ws: pkv.evict_kvcache(k.clone(), v.clone(), w, t, n, 50, 10, torch.empty_like(n), workspace=ws)),

@@ -272,6 +272,24 @@ def test_prompt_weights_neighbour_nan_stays_out(pkv):
                           ref.weight_tolerance(64, big), f"sequence {b}")
 
 
+@pytest.mark.parametrize("D,G,Hkv", [(64, 1, 1), (128, 4, 2), (64, 8, 1)])
+@pytest.mark.parametrize("q_lens,contexts", [([1], [5000]), ([1, 3, 5], [3000, 700, 4100]), ([0, 40, 2, 130], [600, 40, 2049, 3000]),
+                                             ([33], [512]), ([300, 1], [2500, 1])])
+def test_prompt_weights_few_rows_over_long_contexts(pkv, D, G, Hkv, q_lens, contexts):
+    """Fewer items than SMs: the keys of an item are split over CTAs and the pieces joined."""
+    for bs, window in ((256, 0), (16, 2)):
+        c = ref.Cache(contexts, bs, Hkv, D, seed=sum(q_lens) + bs, mbs_extra=2)
+        check_prompt(pkv, c, q_lens, G, window, seed=G, pad_rows=2)
+
+
+def test_prompt_weights_split_with_unreadable_pieces(pkv):
+    """A split none of whose blocks can be read, and a sequence without any, join to the rest and to zeros."""
+    c = ref.Cache([4096, 2048], 64, 2, 64, seed=5)
+    c.tables[0, 8:40] = -1
+    c.tables[1, :] = c.NB
+    check_prompt(pkv, c, [3, 2], 2, expect=FLAG_BAD_BLOCK)
+
+
 @pytest.mark.parametrize("B", [40, 300])
 def test_prompt_weights_many_sequences(pkv, B):
     """More sequences than one warp scans at once, and than the longest-first schedule ranks."""

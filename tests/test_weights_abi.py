@@ -19,12 +19,12 @@ def lib(cuda_lib_path):
         getattr(lib, name).restype = sz
         getattr(lib, name).argtypes = [i32] * n
     lib.pkv_prefill_weights_workspace_bytes.restype = sz
-    lib.pkv_prefill_weights_workspace_bytes.argtypes = [i64, i32]
+    lib.pkv_prefill_weights_workspace_bytes.argtypes = [i32, i64] + [i32] * 6
     return lib
 
 
-def prefill(lib, Tq=10, Hq=4, Hkv=2, D=64, NB=8, bs=16, B=2, max_q=5, window=0, weights=X, ws=X, ws_bytes=1 << 30, scale=0.1):
-    return lib.pkv_paged_prefill_weights(X, X, X, X, 4, X, X, B, i64(Tq), max_q, Hq, Hkv, D, i64(NB), bs, f32(scale), X,
+def prefill(lib, Tq=10, Hq=4, Hkv=2, D=64, NB=8, bs=16, B=2, MBS=4, max_q=5, window=0, weights=X, ws=X, ws_bytes=1 << 30, scale=0.1):
+    return lib.pkv_paged_prefill_weights(X, X, X, X, MBS, X, X, B, i64(Tq), max_q, Hq, Hkv, D, i64(NB), bs, f32(scale), X,
                                          weights, window, ws, sz(ws_bytes), None, None)
 
 
@@ -41,8 +41,14 @@ def test_workspace_sizes(lib):
     assert lib.pkv_decode_weights_workspace_bytes(4, 4, 2, 64, 19, 16, 0) == want
     assert lib.pkv_decode_weights_workspace_bytes(0, 4, 2, 64, 19, 16, 0) == 0
     assert lib.pkv_decode_weights_workspace_bytes(4, 6, 4, 64, 19, 16, 0) == 0
-    assert lib.pkv_prefill_weights_workspace_bytes(100, 4) == up(1600)
-    assert lib.pkv_prefill_weights_workspace_bytes(0, 4) == 0
+    f = lib.pkv_prefill_weights_workspace_bytes
+    # log-sum-exps and a counter; 1 pair of query tiles x 2 KV heads x 3 sequences are 6 items
+    assert f(3, 100, 40, 4, 2, 64, 4, 16) == up(100 * 4 * 4 + 4)  # contexts too short to split
+    # 8192 tokens are 64 tiles, 16 splits of 4: a log-sum-exp and 64 outputs per split and row
+    assert f(3, 100, 40, 4, 2, 64, 512, 16) == up(1604) + up(16 * 400 * 4) + 16 * 400 * 64 * 4
+    assert f(3, 100, 40, 4, 2, 64, 1 << 16, 16) == up(1604) + up(51 * 400 * 4) + 51 * 400 * 64 * 4  # 304 items in all
+    assert f(76, 1 << 20, 20, 4, 2, 64, 512, 16) == up((1 << 22) * 4 + 4)  # 152 items: none split
+    assert f(0, 100, 4, 4, 2, 64, 4, 16) == 0 and f(3, 0, 4, 4, 2, 64, 4, 16) == 0 and f(3, 10, 4, 5, 2, 64, 4, 16) == 0
     # per (sequence, KV head) the range that moves, and where the kept tokens come from
     assert lib.pkv_evict_workspace_bytes(3, 2, 4, 16, 20) == up(3 * 2 * 8) + 3 * 2 * 20 * 4
     # a budget above what the tables can name needs no more than that
@@ -57,6 +63,7 @@ def test_workspace_sizes(lib):
     (dict(weights=P((1 << 20) + 8)), INVALID, b"weights"),
     (dict(ws=None), WORKSPACE, b"workspace"),
     (dict(ws_bytes=159), WORKSPACE, b"workspace"),
+    (dict(MBS=4096, ws_bytes=256), WORKSPACE, b"workspace"),
     (dict(ws=P((1 << 20) + 4)), WORKSPACE, b"workspace"),
     (dict(Hq=3), INVALID, b"multiple"),
     (dict(Hq=6, Hkv=2), UNSUPPORTED, b"Hq/Hkv"),

@@ -175,7 +175,7 @@ struct DeviceState {
     int sms = 0;
     bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
     bool pf_smem_set[3][2][9] = {};  // prefill: [64-key tiles, 128, 128 split][D == 128][G]
-    bool pw_smem_set[2][9] = {};     // its weights kernel: [D == 128][G]
+    bool pw_smem_set[2][2][9] = {};  // its weights kernel: [may split][D == 128][G]
     bool evict_smem_set = false;
 };
 DeviceState g_dev[kMaxDevices];
@@ -854,16 +854,23 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         p.lse = static_cast<float *>(workspace);
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
         p.splits = splits;
+        uint8_t *ws = static_cast<uint8_t *>(workspace) +
+                      pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
+        const bool may_split = pkv::pw_may_split(B, Tq, max_seqlen_q, G, Hkv);
+        if (may_split) {
+            p.pw_count = reinterpret_cast<int32_t *>(ws);
+            ws += pkv::align_up(pkv::kPwCountBytes, 256);
+            p.pw_part = reinterpret_cast<float *>(ws);
+            ws += pkv::kPwPartBytes;
+        }
         if (p.splits > 1) {
-            uint8_t *ws = static_cast<uint8_t *>(workspace) +
-                          pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
             p.part_lse = reinterpret_cast<float *>(ws);
             ws += pkv::align_up((size_t)p.splits * Tq * Hq * sizeof(float), 256);
             p.part_out = reinterpret_cast<float *>(ws);
         }
-        const void *wfn = pkv::prompt_weights_kernel_fn(D, G);
+        const void *wfn = pkv::prompt_weights_kernel_fn(D, G, may_split);
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->pw_smem_set[D == 128][G];
+        bool &set = st->pw_smem_set[may_split][D == 128][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(wfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)pkv::prompt_weights_smem_bytes(D));
@@ -917,9 +924,12 @@ size_t pkv_prefill_weights_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, 
     if (B < 1 || Tq < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || MBS < 1 || bs < 1)
         return 0;
     const size_t rows = (size_t)Tq * Hq;
-    // every row's log-sum-exp and the weights kernel's work counter; where the items
-    // are split, the splits' outputs and log-sum-exps
+    // every row's log-sum-exp and the weights kernel's work counter; what its splits
+    // need where there may be few units; where the attention's items are split, the
+    // splits' outputs and log-sum-exps
     size_t n = pkv::align_up(rows * sizeof(float) + sizeof(int32_t), 256);
+    if (pkv::pw_may_split(B, Tq, max_seqlen_q, Hq / Hkv, Hkv))
+        n += pkv::align_up(pkv::kPwCountBytes, 256) + pkv::kPwPartBytes;
     const int splits = prefill_splits(B, max_seqlen_q, Hq, Hkv, MBS, bs);
     if (splits > 1)
         n += pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float);

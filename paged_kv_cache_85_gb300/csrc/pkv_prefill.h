@@ -30,15 +30,36 @@ struct PrefillParams {
     float *part_out = nullptr;    // [splits, Tq, Hq, D] outputs of the splits
     float *part_lse = nullptr;    // [splits, Hkv, Tq, G] their log-sum-exps, -inf: no key
     int32_t *ticket = nullptr;    // nullable: work counter of the weights kernel, cleared here
+    // nullable, for the weights kernel's splits: arrivals per unit and warp (cleared
+    // here) and partial sums [kPwFewUnits][kPwMaxSplits][256]
+    int32_t *pw_count = nullptr;
+    float *pw_part = nullptr;
 };
 
 cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
                            const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
                            cudaStream_t stream);
+constexpr int kPwFewUnits = 152;  // fewer units (256 tokens, one KV head) than this are split
+constexpr int kPwMaxSplits = 16;
+constexpr int kPwMinSplit = 4;  // query tiles of 128 rows per split at least
+// Splits of a unit at most, for so many recorded tokens.
+__host__ __device__ inline int pw_max_splits(int tokens, int G)
+{
+    const long long tiles = ((long long)tokens * G + 127) / 128;
+    const long long s = tiles / kPwMinSplit;
+    return s < 1 ? 1 : s > kPwMaxSplits ? kPwMaxSplits : (int)s;
+}
+// Whether a call may have so few units (its new tokens alone make Tq Hkv / 256).
+inline bool pw_may_split(int B, long long Tq, int max_q, int G, int Hkv)
+{
+    return (long long)B * Hkv < kPwFewUnits && Tq * Hkv < 256LL * kPwFewUnits && pw_max_splits(max_q, G) > 1;
+}
+constexpr size_t kPwCountBytes = (size_t)kPwFewUnits * 8 * sizeof(int32_t);
+constexpr size_t kPwPartBytes = (size_t)kPwFewUnits * kPwMaxSplits * 256 * sizeof(float);
 cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
                                   const PrefillParams &p, float *weights, int window, int sms,
                                   cudaStream_t stream);
-const void *prompt_weights_kernel_fn(int D, int G);
+const void *prompt_weights_kernel_fn(int D, int G, bool split);
 size_t prompt_weights_smem_bytes(int D);
 const void *prefill_kernel(int D, int G, bool wide, bool split);
 size_t prefill_smem_bytes(int D, bool wide);

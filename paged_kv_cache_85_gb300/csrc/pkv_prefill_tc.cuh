@@ -345,8 +345,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             prefetch_tensormap(&tmv);
         }
         grid_dependency_wait();  // K/V may have just been written by store_kvcache
-        if (p.ticket && c == 0 && lane == 0)
-            *p.ticket = 0;
         int gk = 0, gv = 0;      // K and V tiles issued so far (all items)
         int q_loads[2] = {0, 0}; // Q tiles A and B loaded so far
         bool ok = true;
@@ -926,11 +924,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 tc::fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                // for the attention weights of the step; +inf (weight 0) for a
-                // row that could read no key
-                if (p.lse && valid)
-                    p.lse[((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] =
-                        l == 0.f ? INFINITY : m + log2f(l);
                 uint16_t *dst = p.out + ((size_t)(it.cq0 + tok) * p.Hq + it.kvh * G + g) * D;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; cc++) {

@@ -184,8 +184,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             prefetch_tensormap(&tmv);
         }
         grid_dependency_wait();  // K/V may have just been written by store_kvcache
-        if (p.ticket && c == 0 && lane == 0)
-            *p.ticket = 0;
+        if (p.ticket && c == 0) {  // the weights kernel's counters
+            if (lane == 0)
+                *p.ticket = 0;
+            for (int i = lane; p.pw_count && i < kPwFewUnits * 8; i += 32)
+                p.pw_count[i] = 0;
+        }
         int gk = 0, gv = 0;       // K and V tiles issued so far (all items)
         int q_loads[2] = {0, 0};  // Q tiles A and B loaded so far
         bool ok = true;

@@ -18,6 +18,10 @@
 // token, head) rows that see any of them pass by in tiles of 128.  Two token
 // tiles per query tile halve the query rows read from L2, which bound the
 // kernel with one (32 KB per 128 x 128 scores, 9 TB/s: 143 us of the 16k step).
+// Where there are fewer units of 256 tokens than SMs, their query tiles are
+// split over several items; each leaves its tokens' partial sums in the
+// workspace, and the last one to arrive adds them up in the order of the splits
+// (the same result whoever is last).
 // A persistent CTA per SM takes items by ticket (sequences in order, early
 // tokens first, which are the long items of a causal chunk); the sum does not
 // depend on who takes what.  Warps:
@@ -67,6 +71,9 @@ struct PwItem {
     int i0;             // first recorded new token that sees a token of the item
     int tiles;          // query tiles from i0 on
     int first1;         // the first of them that sees token tile B (tiles: none does)
+    // where units (256 tokens of a sequence and KV head) are split over the queries:
+    // this item is split `split` of `splits` of unit `unit`
+    int unit, split, splits;
 };
 
 struct PwSmem {
@@ -107,7 +114,9 @@ struct PwParams {
     int window;        // 0: every new token records
 };
 
-template <int D, int G>
+// SPLIT: units may be split over the queries (p.pw_count is there).  Of its own:
+// with it the others are some 10 us of the 16k step slower (registers).
+template <int D, int G, bool SPLIT>
 __global__ void __launch_bounds__(kPwThreads, 1)
     prompt_weights_kernel(const __grid_constant__ CUtensorMap tmq,
                           const __grid_constant__ CUtensorMap tmk, const PwParams P)
@@ -217,15 +226,30 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     incl += y;
             }
         };
+        // splits per unit: enough items for every SM twice, where there are few units
+        int splits = 1;
+        if constexpr (SPLIT) {
+            long long units = 0;
+            int most = 0;  // recorded new tokens of a sequence at most
+            for (b0 = 0; b0 < p.B; b0 += 32) {
+                look();
+                units += __shfl_sync(FULL, incl, 31);
+                most = max(most, __reduce_max_sync(FULL, P.window > 0 ? min(q_len, P.window) : q_len));
+            }
+            b0 = 0;
+            if (units > 0 && units < kPwFewUnits)
+                splits = min(pw_max_splits(most, G), (int)((2 * kPwFewUnits + units - 1) / units));
+        }
         look();
         int ticket = 0;
         if (lane == 0)
             ticket = atomicAdd(p.ticket, 1);
         for (;;) {
             // ---- the ticket's item
-            PwItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0};
-            const long long pos = __shfl_sync(FULL, ticket, 0);
-            if (ok) {
+            PwItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1};
+            for (bool again = ok; again;) {
+                again = false;
+                const long long at = __shfl_sync(FULL, ticket, 0), pos = SPLIT ? at / splits : at;
                 while (b0 < p.B && pos - before >= __shfl_sync(FULL, incl, 31)) {
                     before += __shfl_sync(FULL, incl, 31);
                     b0 += 32;
@@ -251,6 +275,22 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     it.first1 = t1 < it.k_len
                                     ? max(0, t1 - (it.k_len - it.q_len) - it.i0) / TPC
                                     : it.tiles;
+                    if (SPLIT && splits > 1) {
+                        const int chunk = max(kPwMinSplit, (it.tiles + splits - 1) / splits);
+                        it.unit = (int)pos;
+                        it.split = (int)(at - pos * splits);
+                        it.splits = (it.tiles + chunk - 1) / chunk;
+                        const int skip = it.split * chunk;
+                        it.i0 += skip * TPC;
+                        it.tiles = min(it.tiles - skip, chunk);
+                        it.first1 = min(max(it.first1 - skip, 0), max(it.tiles, 0));
+                        if (it.tiles <= 0) {  // the unit has fewer splits: the next ticket
+                            it.b = -1;
+                            again = true;
+                            if (lane == 0)
+                                ticket = atomicAdd(p.ticket, 1);
+                        }
+                    }
                 }
             }
             // the next ticket, on its way while this item is copied
@@ -466,13 +506,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             }
             if (!ok)
                 break;
+            const int t = it.t0 + kt * kPwTokens + r;
+            const int base = it.k_len - it.q_len;
+            int blk = -1;
+            if (half == 0 && t < it.k_len)
+                blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
+            float sum = 0.f;
             if (first < it.tiles) {
-                const int t = it.t0 + kt * kPwTokens + r;
-                const int base = it.k_len - it.q_len;
-                int blk = -1;
-                if (half == 0 && t < it.k_len)
-                    blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
-                float sum = 0.f;
                 for (int j = first; j < it.tiles; j++, used++) {
                     const int buf = 2 * kt + (used & 1);
                     const int i_first = it.i0 + j * TPC;
@@ -544,7 +584,26 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 if (lane == 0)
                     mbar_arrive(half == 1 ? &part_full[x] : &part_empty[x]);
                 parts++;
-                if (half == 0 && blk >= 0 && blk < p.NB) {
+            }
+            if (half == 0) {
+                bool write = first < it.tiles;
+                if (SPLIT && it.splits > 1 && it.t0 + kt * kPwTokens < it.k_len) {
+                    float *mine = p.pw_part + ((size_t)it.unit * kPwMaxSplits) * 2 * kPwTokens + kt * kPwTokens + r;
+                    mine[(size_t)it.split * 2 * kPwTokens] = sum;
+                    __threadfence();
+                    __syncwarp();
+                    int seen = 0;
+                    if (lane == 0)
+                        seen = atomicAdd(p.pw_count + it.unit * 8 + kt * 4 + (warp & 3), 1);
+                    write = __shfl_sync(FULL, seen, 0) == it.splits - 1;
+                    if (write) {  // every other split of these 32 tokens is there
+                        __threadfence();
+                        sum = 0.f;
+                        for (int i = 0; i < it.splits; i++)
+                            sum += __ldcg(mine + (size_t)i * 2 * kPwTokens);
+                    }
+                }
+                if (write && blk >= 0 && blk < p.NB) {
                     float *dst = P.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs;
                     if (t >= base)
                         *dst = sum;
@@ -568,21 +627,23 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 static const void *prompt_weights_fn(int G)
 {
     switch (G) {
-    case 1: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 1>);
-    case 2: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 2>);
-    case 4: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 4>);
-    case 8: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 8>);
+    case 1: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 1, SPLIT>);
+    case 2: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 2, SPLIT>);
+    case 4: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 4, SPLIT>);
+    case 8: return reinterpret_cast<const void *>(&prompt_weights_kernel<D, 8, SPLIT>);
     default: return nullptr;
     }
 }
 
-const void *prompt_weights_kernel_fn(int D, int G)
+const void *prompt_weights_kernel_fn(int D, int G, bool split)
 {
-    return D == 128 ? prompt_weights_fn<128>(G) : prompt_weights_fn<64>(G);
+    if (split)
+        return D == 128 ? prompt_weights_fn<128, true>(G) : prompt_weights_fn<64, true>(G);
+    return D == 128 ? prompt_weights_fn<128, false>(G) : prompt_weights_fn<64, false>(G);
 }
 
 size_t prompt_weights_smem_bytes(int D) { return pw_smem_layout(D).total; }
@@ -597,7 +658,9 @@ cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CU
     P.window = window;
     // no more CTAs than items there can be
     const long long tiles = ((long long)p.MBS * p.bs + 2 * kPwTokens - 1) / (2 * kPwTokens);
-    const long long most = tiles * p.Hkv * p.B;
+    long long most = tiles * p.Hkv * p.B;
+    if (p.pw_count)
+        most *= pw_max_splits(window > 0 && window < p.max_q ? window : p.max_q, G);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -609,8 +672,9 @@ cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CU
     cfg.attrs = attr;
     cfg.numAttrs = 1;
 #define PKV_PW(DD, GG) \
-    if (D == DD && G == GG) \
-        return cudaLaunchKernelEx(&cfg, prompt_weights_kernel<DD, GG>, *tmq, *tmk, P);
+    if (D == DD && G == GG)                                                                          \
+        return p.pw_count ? cudaLaunchKernelEx(&cfg, prompt_weights_kernel<DD, GG, true>, *tmq, *tmk, P) \
+                          : cudaLaunchKernelEx(&cfg, prompt_weights_kernel<DD, GG, false>, *tmq, *tmk, P);
     PKV_PW(64, 1) PKV_PW(64, 2) PKV_PW(64, 4) PKV_PW(64, 8)
     PKV_PW(128, 1) PKV_PW(128, 2) PKV_PW(128, 4) PKV_PW(128, 8)
 #undef PKV_PW

@@ -290,6 +290,21 @@ def test_prompt_weights_split_with_unreadable_pieces(pkv):
     check_prompt(pkv, c, [3, 2], 2, expect=FLAG_BAD_BLOCK)
 
 
+@pytest.mark.parametrize("D,G,Hkv,window", [(64, 8, 1, 0), (128, 4, 2, 0), (64, 8, 1, 700), (64, 1, 3, 0)])
+def test_prompt_weights_few_units_split_over_queries(pkv, D, G, Hkv, window):
+    """Long prompts of few KV heads: the weights' query tiles are split over CTAs, with the same bits in every run."""
+    q_lens, contexts = [1300, 1, 700], [1300, 300, 1100]
+    c = ref.Cache(contexts, 32, Hkv, D, seed=G)
+    first = check_prompt(pkv, c, q_lens, G, window, seed=G).w.view(torch.int32)
+    for _ in range(3):
+        d = Dev(c)
+        cq = torch.tensor([0, 1300, 1301, 2001], dtype=torch.int32, device="cuda")
+        ck = torch.tensor([0, 1300, 1600, 2700], dtype=torch.int32, device="cuda")
+        q = bf(queries(2001, Hkv * G, D, G))
+        pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cq, ck, 1300, 1 / np.sqrt(D), torch.empty_like(q), d.w, window=window)
+        assert torch.equal(d.w.view(torch.int32), first)
+
+
 @pytest.mark.parametrize("B", [40, 300])
 def test_prompt_weights_many_sequences(pkv, B):
     """More sequences than one warp scans at once, and than the longest-first schedule ranks."""

@@ -42,11 +42,13 @@ def test_workspace_sizes(lib):
     assert lib.pkv_decode_weights_workspace_bytes(0, 4, 2, 64, 19, 16, 0) == 0
     assert lib.pkv_decode_weights_workspace_bytes(4, 6, 4, 64, 19, 16, 0) == 0
     f = lib.pkv_prefill_weights_workspace_bytes
-    # log-sum-exps and a counter; 1 pair of query tiles x 2 KV heads x 3 sequences are 6 items
-    assert f(3, 100, 40, 4, 2, 64, 4, 16) == up(100 * 4 * 4 + 4)  # contexts too short to split
+    # log-sum-exps and a counter (a few tokens need no partial sums of weights); 1 pair of query tiles x 2 KV heads x 3 sequences are 6 items
+    base = up(100 * 4 * 4 + 4)
+    assert f(3, 100, 40, 4, 2, 64, 4, 16) == base  # contexts too short to split
     # 8192 tokens are 64 tiles, 16 splits of 4: a log-sum-exp and 64 outputs per split and row
-    assert f(3, 100, 40, 4, 2, 64, 512, 16) == up(1604) + up(16 * 400 * 4) + 16 * 400 * 64 * 4
-    assert f(3, 100, 40, 4, 2, 64, 1 << 16, 16) == up(1604) + up(51 * 400 * 4) + 51 * 400 * 64 * 4  # 304 items in all
+    assert f(3, 100, 40, 4, 2, 64, 512, 16) == base + up(16 * 400 * 4) + 16 * 400 * 64 * 4
+    assert f(3, 100, 40, 4, 2, 64, 1 << 16, 16) == base + up(51 * 400 * 4) + 51 * 400 * 64 * 4  # 304 items in all
+    assert f(3, 100, 40, 4, 2, 64, 4, 16) == f(3, 100, 1000, 4, 2, 64, 4, 16) - up(152 * 8 * 4) - 152 * 16 * 256 * 4
     assert f(76, 1 << 20, 20, 4, 2, 64, 512, 16) == up((1 << 22) * 4 + 4)  # 152 items: none split
     assert f(0, 100, 4, 4, 2, 64, 4, 16) == 0 and f(3, 0, 4, 4, 2, 64, 4, 16) == 0 and f(3, 10, 4, 5, 2, 64, 4, 16) == 0
     # per (sequence, KV head) the range that moves, and where the kept tokens come from
@@ -64,6 +66,7 @@ def test_workspace_sizes(lib):
     (dict(ws=None), WORKSPACE, b"workspace"),
     (dict(ws_bytes=159), WORKSPACE, b"workspace"),
     (dict(MBS=4096, ws_bytes=256), WORKSPACE, b"workspace"),
+    (dict(max_q=1000, ws_bytes=256), WORKSPACE, b"workspace"),
     (dict(ws=P((1 << 20) + 4)), WORKSPACE, b"workspace"),
     (dict(Hq=3), INVALID, b"multiple"),
     (dict(Hq=6, Hkv=2), UNSUPPORTED, b"Hq/Hkv"),

@@ -337,7 +337,9 @@ pkv_status pkv_paged_attn_decode_noalloc(const void *q, const void *k_cache, con
  * p is formed in fp32 from the fp32 scores and the row's fp32 log-sum-exp.
  * Blocks shared by several sequences of a call receive every sequence's
  * addition, in no fixed order (fp32 sums may differ in the last bits from run
- * to run); without shared blocks the results are the same in every run.
+ * to run); without shared blocks the results are the same in every run.  The
+ * weights belong to the blocks: a prompt that reuses cached prefix blocks adds
+ * to what those blocks had gathered.
  * Tokens of blocks outside [0, NB) have no weight and receive none.  A query
  * row whose scores contain a NaN or +inf adds NaN to the tokens it sees.
  */
@@ -425,7 +427,7 @@ pkv_status pkv_paged_prefill_weights(const void *q, const void *k_cache, const v
  * position holds a different token for every KV head.
  *
  *   k_cache, v_cache  [NB, bs, Hkv, D] of elem_bytes = 2 (bf16) or 1 (E4M3),
- *                     D in {64, 128}; updated in place
+ *                     D in {64, 128}; distinct memory, updated in place
  *   weights           above; updated in place
  *   context_lens      int32 [B]; out_lens int32 [B], may be context_lens
  *   budget >= 1, 0 <= recent <= budget; bs a multiple of 16; B, Hkv <= 65535

@@ -985,6 +985,8 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
         return PKV_OK;
     if (!k_cache || !v_cache || !weights || !block_tables || !context_lens || !out_lens)
         return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: null pointer");
+    if (k_cache == v_cache)
+        return fail(PKV_ERR_INVALID_ARG, "evict_kvcache: k_cache and v_cache are the same memory");
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights) || !aligned16(workspace) ||
         (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
         (reinterpret_cast<uintptr_t>(context_lens) & 3u) || (reinterpret_cast<uintptr_t>(out_lens) & 3u))

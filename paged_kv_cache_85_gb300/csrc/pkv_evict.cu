@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         if (lead) {
             if (bad_len && h == 0)
                 flag_error(p.err_flag, 0x4 /* PKV_FLAG_BAD_CONTEXT_LEN */);
-            *moved = make_int2(0, 0);
+            *moved = make_int2(n, n);
         }
         return;
     }
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             if (lead) {
                 if (h == 0)
                     flag_error(p.err_flag, 0x2 /* PKV_FLAG_BAD_BLOCK */);
-                *moved = make_int2(0, 0);
+                *moved = make_int2(n, n);
             }
             return;
         }
@@ -433,11 +433,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     grid_dependency_wait();
     const int2 moved = p.ws_moved[(size_t)b * p.Hkv + h];
     if (slice == 0 && h == 0 && threadIdx.x == 0) {
-        // here, not in the selection: its CTAs all read the length, and
-        // out_lens may be context_lens.  The fence makes it visible to a next
+        // here, not in the selection: its CTAs all read the lengths, and out_lens
+        // may be (or overlap) context_lens.  The fence makes it visible to a next
         // kernel that starts as soon as this one's CTAs have left.
-        const int n = p.context_lens[b];
-        p.out_lens[b] = moved.y > 0 ? p.budget : n;
+        p.out_lens[b] = moved.y;
         __threadfence();
     }
     if (moved.x >= moved.y)

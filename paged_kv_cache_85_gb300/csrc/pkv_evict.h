@@ -29,7 +29,7 @@ struct EvictParams {
     const int32_t *context_lens;  // [B]
     int32_t *out_lens;            // [B], may be context_lens
     int32_t *ws_src;              // [B, Hkv, keep] slot that token j of the trimmed context comes from
-    int2 *ws_moved;               // [B, Hkv] (first, end): tokens j in [first, end) move
+    int2 *ws_moved;               // [B, Hkv] (first, new length): tokens first .. length - 1 move
     int32_t *err_flag;            // nullable
     int B, Hkv, MBS, bs, NB;
     int units;                    // 16-byte units of one head's row (D * element bytes / 16)

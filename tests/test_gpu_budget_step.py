@@ -325,6 +325,19 @@ def test_output_in_pinned_host_memory(pkv):
         torch.cuda.synchronize()
         got.append(out.cpu().view(torch.int16))
     assert torch.equal(*got)
+    # a prefill step: whole items, and items split over the keys
+    for lens in ([70, 1, 200], [3000, 5, 2000]):
+        c = ref.Cache(lens, 16, 2, 64, seed=3)
+        k, v, t = bf(c.k), bf(c.v), torch.from_numpy(c.tables).cuda()
+        cq = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+        ck = torch.from_numpy(np.concatenate([[0], np.cumsum(c.lens)]).astype(np.int32)).cuda()
+        got = []
+        for out in (torch.empty_like(q), torch.empty(q.shape, dtype=q.dtype).pin_memory()):
+            w = torch.from_numpy(c.w.copy()).cuda()
+            pkv.paged_prefill_weights(q, k, v, t, cq, ck, 1, 0.1, out, w)
+            torch.cuda.synchronize()
+            got.append(out.cpu().view(torch.int16))
+        assert torch.equal(*got)
 
 
 def test_arguments_are_checked(pkv):

@@ -174,6 +174,25 @@ def test_decode_weights_repeat_bit_for_bit(pkv):
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [20, 3000])
+def test_decode_weights_nan_key_stays_with_its_sequence_and_head(pkv, fp8, n):
+    """A NaN among a sequence's keys makes the weights of that sequence and KV head NaN, and no others (with the
+    context read by one worker, and split over many)."""
+    c = ref.Cache([n, 40], 16, 2, 64, fp8=fp8, seed=1)
+    qb = queries(2, 4, 64, 0)
+    _, w, add, big = ref.decode(c, ref.from_bf16(qb), 0.125)
+    s = c.slots(0)
+    c.k.reshape(-1, 2, 64)[s[n // 2], 1, 3] = 0x7F if fp8 else 0x7FC0
+    d, q = Dev(c), bf(qb)
+    d.decode(pkv, q, 0.125, torch.empty_like(q))
+    got = d.w.cpu().numpy()
+    assert np.isnan(got[s // 16, 1, s % 16]).all()
+    got[s // 16, 1, s % 16], w[s // 16, 1, s % 16] = 0, 0
+    add[s // 16, 1, s % 16] = 0
+    ref.check_weights(got, w, add, ref.weight_tolerance(64, big))
+
+
 # ------------------------------------------------------------------ prefill
 
 
@@ -374,6 +393,24 @@ def test_prompt_weights_full_size_steps(pkv, idx):
             assert abs(got - p.q_lens[b] * p.Hq) <= ref.weight_tolerance(p.D, 40) * p.q_lens[b] * p.Hq
 
 
+def test_prompt_weights_nan_key_reaches_only_its_readers(pkv):
+    """A NaN key makes the rows that see it NaN, and with them the weights of the tokens those rows see; earlier
+    rows, the other KV head and the other sequences are as without it."""
+    c = ref.Cache([300, 90], 16, 2, 64, seed=1)
+    cu = torch.tensor([0, 300, 390], dtype=torch.int32, device="cuda")
+    qb = queries(390, 4, 64, 0)
+    _, w, add, big = ref.prompt(c, ref.from_bf16(qb), cu.cpu().numpy(), 0.125)
+    s = c.slots(0)
+    c.k.reshape(-1, 2, 64)[s[200], 1, 3] = 0x7FC0
+    d, q = Dev(c), bf(qb)
+    out = pkv.paged_prefill_weights(q, d.k, d.v, d.tables, cu, cu, 300, 0.125, torch.empty_like(q), d.w, err_flag=d.err)
+    got = d.w.cpu().numpy()
+    assert torch.isfinite(out[:200]).all() and torch.isfinite(out[300:]).all() and torch.isfinite(out[:, :2]).all()
+    assert np.isnan(got[s // 16, 1, s % 16]).all()  # every token is seen by row 200 or a later one
+    got[s // 16, 1, s % 16], w[s // 16, 1, s % 16], add[s // 16, 1, s % 16] = 0, 0, 0
+    ref.check_weights(got, w, add, ref.weight_tolerance(64, big))
+
+
 # ------------------------------------------------------------------ eviction
 
 
@@ -454,3 +491,14 @@ def test_evict_bad_length_is_left_alone(pkv):
     c.lens = np.array([100, -1], dtype=np.int32)
     lens[1] = -1
     check_evict(pkv, c, 70, 8, expect=FLAG_BAD_CONTEXT_LEN, want=(k, v, w, lens))
+
+
+def test_evict_lengths_may_overlap(pkv):
+    """out_lens may be any view of the lengths' memory."""
+    c = ref.Cache([100, 20, 70, 64], 16, 2, 64, seed=3)
+    *_, lens = ref.evict(c, 60, 8)
+    d = Dev(c)
+    both = torch.empty(5, dtype=torch.int32, device="cuda")
+    both[:4] = d.lens
+    pkv.evict_kvcache(d.k, d.v, d.w, d.tables, both[:4], 60, 8, both[1:])
+    assert both[1:].tolist() == lens.tolist()

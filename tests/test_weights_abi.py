@@ -28,7 +28,10 @@ def prefill(lib, Tq=10, Hq=4, Hkv=2, D=64, NB=8, bs=16, B=2, MBS=4, max_q=5, win
                                          weights, window, ws, sz(ws_bytes), None, None)
 
 
-def evict(lib, k=X, v=X, w=X, tables=X, MBS=4, lens=X, B=2, Hkv=2, D=64, eb=2, NB=8, bs=16, budget=20, recent=5, out=X, ws=X, ws_bytes=1 << 30):
+Y = P(1 << 21)
+
+
+def evict(lib, k=X, v=Y, w=X, tables=X, MBS=4, lens=X, B=2, Hkv=2, D=64, eb=2, NB=8, bs=16, budget=20, recent=5, out=X, ws=X, ws_bytes=1 << 30):
     return lib.pkv_evict_kvcache(k, v, w, tables, MBS, lens, B, Hkv, D, eb, i64(NB), bs, budget, recent, out, ws,
                                  sz(ws_bytes), None, None)
 
@@ -103,6 +106,7 @@ def test_prefill_weights_nothing_to_do(lib, kw):
     (dict(tables=None), INVALID, b"null"), (dict(lens=None), INVALID, b"null"), (dict(out=None), INVALID, b"null"),
     (dict(k=P((1 << 20) + 8)), INVALID, b"misaligned"), (dict(w=P((1 << 20) + 4)), INVALID, b"misaligned"),
     (dict(out=P((1 << 20) + 2)), INVALID, b"misaligned"),
+    (dict(v=X), INVALID, b"same memory"),
     (dict(ws=None), WORKSPACE, b"workspace"),
     (dict(ws_bytes=64), WORKSPACE, b"workspace"),
 ])

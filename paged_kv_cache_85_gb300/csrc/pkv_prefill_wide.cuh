@@ -764,22 +764,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // read no key
                     if (valid)
                         p.lse[lse_at] = l == 0.f ? INFINITY : m + log2f(l);
-                    uint16_t *dst = p.out + (row * p.Hq + it.kvh * G + g) * D;
+                    // 64 columns (eight 16-byte pieces) of a row at a time; eight lanes
+                    // trade their rows' pieces (three butterfly steps), so that a store
+                    // instruction writes whole 128-byte lines of four rows, not 16 bytes
+                    // in each of 32 lines
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 32; cc++) {
-                        uint32_t ro[32];
-                        tc::ld32(tO + 32 * cc, ro);
+                    for (int hf = 0; hf < HALVES; hf++) {
+                        uint32_t ra[32], rb[32], v[32];
+                        tc::ld32(tO + 64 * hf, ra);
+                        tc::ld32(tO + 64 * hf + 32, rb);
                         tc::wait_ld();
-                        if (valid) {
-                            uint32_t pk[16];
 #pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                pk[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv,
-                                                    __uint_as_float(ro[2 * i + 1]) * inv);
-                            uint4 *d4 = reinterpret_cast<uint4 *>(dst + 32 * cc);
+                        for (int i = 0; i < 16; i++) {
+                            v[i] = pack_bf16x2(__uint_as_float(ra[2 * i]) * inv, __uint_as_float(ra[2 * i + 1]) * inv);
+                            v[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]) * inv,
+                                                    __uint_as_float(rb[2 * i + 1]) * inv);
+                        }
 #pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        for (int s = 1; s < 8; s *= 2) {
+                            const bool up = (lane & s) != 0;
+#pragma unroll
+                            for (int k = 0; k < 8; k++) {
+                                if (k & s)
+                                    continue;
+#pragma unroll
+                                for (int w = 0; w < 4; w++) {  // piece k of the upper lane for k + s of the lower
+                                    const uint32_t give = up ? v[4 * k + w] : v[4 * (k + s) + w];
+                                    const uint32_t got = __shfl_xor_sync(FULL, give, s);
+                                    v[4 * k + w] = up ? got : v[4 * k + w];
+                                    v[4 * (k + s) + w] = up ? v[4 * (k + s) + w] : got;
+                                }
+                            }
+                        }
+                        // this lane now has piece lane % 8 of the rows 8 (lane / 8) + k
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const int rr = 32 * (warp & 3) + (lane & 24) + k;
+                            const int tk = it.tok0 + tq * TPC + rr / G;
+                            if (tk < it.q_len)
+                                *reinterpret_cast<uint4 *>(
+                                    p.out + (((size_t)it.cq0 + tk) * p.Hq + it.kvh * G + rr % G) * D + 64 * hf +
+                                    8 * (lane & 7)) =
+                                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                         }
                     }
                 }

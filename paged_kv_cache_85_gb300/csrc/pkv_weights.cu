@@ -135,8 +135,11 @@ __global__ void __launch_bounds__(kAddThreads, G == 8 ? 4 : 8)
             s[g] = sn[g];
         read(box + kStep);
         const int h = box / S.per_head;
-        const int nvalid = m.w & (kBoxNewest - 1);
-        const bool valid = m.y >= 0 && i < nvalid;
+        // a decode kernel that gave up waiting leaves descriptors unwritten: what
+        // stands there then is checked before it is an address
+        const int nvalid = min(m.w & (kBoxNewest - 1), BT);
+        const bool valid = (unsigned)m.y < (unsigned)p.NB && (unsigned)m.x < (unsigned)p.B &&
+                           (unsigned)m.z <= (unsigned)(p.bs - BT) && m.z % BT == 0 && i < nvalid;
         // the streams of these boxes, one after the other (mostly one, and the
         // same as before)
         float lse[G];

@@ -733,11 +733,11 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
 
 // Splits over the keys of a recording prefill's items (query tile pairs of one
 // sequence and KV head), from the sizes alone.
-static int prefill_splits(int B, int max_seqlen_q, int Hq, int Hkv, int MBS, int bs)
+static pkv::WideSplit prefill_split(int B, int max_seqlen_q, int Hq, int Hkv, int MBS, int bs)
 {
     const long long pairs = ((long long)max_seqlen_q * (Hq / Hkv) + 2 * pkv::kPrefillRows - 1) /
                             (2 * pkv::kPrefillRows);
-    return pkv::wide_splits(pairs * Hkv * B, (long long)MBS * bs);
+    return pkv::wide_split(pairs * Hkv * B, (long long)MBS * bs, max_seqlen_q, B);
 }
 
 // record: also leave every row's log-sum-exp in the workspace and add the
@@ -802,7 +802,9 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (ps != PKV_OK)
         return ps;
     const bool wide = record;  // the calls that record take the 128-key kernel
-    const int splits = record ? prefill_splits(B, max_seqlen_q, Hq, Hkv, MBS, bs) : 1;
+    const pkv::WideSplit split =
+        record ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1};
+    const int splits = split.splits;
     const void *kfn = pkv::prefill_kernel(D, G, wide, splits > 1);
     const size_t smem = pkv::prefill_smem_bytes(D, wide);
     {
@@ -854,6 +856,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         p.lse = static_cast<float *>(workspace);
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
         p.splits = splits;
+        p.whole = split.whole;
         uint8_t *ws = static_cast<uint8_t *>(workspace) +
                       pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
         const bool may_split = pkv::pw_may_split(B, Tq, max_seqlen_q, G, Hkv);
@@ -884,7 +887,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     // second CTA lands beside it), each walking its share of the work items.
     static_assert(pkv::kPrefillThreads * 168 <= 65536, "prefill registers per thread");
     long long grid = (long long)st->sms;
-    if (grid > (long long)p.n_items * p.splits)
+    if (grid > (long long)p.n_items * p.splits)  // (with whole items there are more than SMs)
         grid = (long long)p.n_items * p.splits;
     if (grid < 1)
         return PKV_OK;
@@ -930,7 +933,7 @@ size_t pkv_prefill_weights_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, 
     size_t n = pkv::align_up(rows * sizeof(float) + sizeof(int32_t), 256);
     if (pkv::pw_may_split(B, Tq, max_seqlen_q, Hq / Hkv, Hkv))
         n += pkv::align_up(pkv::kPwCountBytes, 256) + pkv::kPwPartBytes;
-    const int splits = prefill_splits(B, max_seqlen_q, Hq, Hkv, MBS, bs);
+    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs).splits;
     if (splits > 1)
         n += pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float);
     return n;

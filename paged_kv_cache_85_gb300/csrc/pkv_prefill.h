@@ -27,8 +27,10 @@ struct PrefillParams {
     float *lse = nullptr;         // nullable: [Hkv, Tq, G] log-sum-exp of every row (log2 units)
     // 128-key kernel, where its items are split over the keys (splits > 1)
     int splits = 1;
+    int whole = 0;                // the first (longest) items, which are not split
     float *part_out = nullptr;    // [splits, Tq, Hq, D] outputs of the splits
-    float *part_lse = nullptr;    // [splits, Hkv, Tq, G] their log-sum-exps, -inf: no key
+    float *part_lse = nullptr;    // [splits, Hkv, Tq, G] their log-sum-exps, -inf: no key; of
+                                  // a whole item's rows the first is +inf
     int32_t *ticket = nullptr;    // nullable: work counter of the weights kernel, cleared here
     // nullable, for the weights kernel's splits: arrivals per unit and warp (cleared
     // here) and partial sums [kPwFewUnits][kPwMaxSplits][256]
@@ -71,19 +73,51 @@ __host__ __device__ inline int wide_chunk(int nkt, int splits)
     const int chunk = (nkt + splits - 1) / splits;
     return chunk < kMinSplitTiles ? kMinSplitTiles : chunk;
 }
-// Splits of a call: enough to give two items to every SM of a large GPU where
-// the query tile pairs alone do not give it one, and none shorter than
-// kMinSplitTiles tiles of the longest context.
-inline int wide_splits(long long items, long long max_ctx)
+// How a call's items are split, from its sizes: items from `whole` on into up to
+// `splits` pieces.
+//  * Where there are fewer items than SMs, all of them, into enough pieces for two
+//    per SM, none shorter than kMinSplitTiles tiles of the longest context.
+//  * Where there are a few rounds of long items, those of the last, incomplete
+//    round: 256 items (2048 new tokens of 32 heads on a context of 28672) are two
+//    rounds of 152 SMs, in the second of which 48 have nothing to do.  Worth it
+//    where the shorter last round saves more than the pieces' ends (some 8000
+//    cycles each), their outputs' way through memory (262 KB written and read of a
+//    piece, at 3500 bytes a cycle) and the join cost; a key tile is 3200 cycles.
+//    Whole call: those 256 items 820 -> 792 us; 168 items (1300 new tokens on 28672)
+//    798 -> 545; 192 (three of 512 on 8192) 269 -> 215; 512 (4096 on 16384) 1002 -> 935.
+struct WideSplit {
+    int whole, splits;
+};
+constexpr long long kWideSms = 152;
+constexpr int kJoinMaxSeqs = 152;  // sequences that the join kernel can look through
+inline WideSplit wide_split(long long items, long long max_ctx, int max_q, int B)
 {
-    constexpr long long kFew = 152, kWant = 304;
-    if (items < 1 || items >= kFew)
-        return 1;
     const long long tiles = (max_ctx + 127) / 128;
-    long long s = (kWant + items - 1) / items;
-    if (s > tiles / kMinSplitTiles)
-        s = tiles / kMinSplitTiles;
-    return s < 1 ? 1 : (int)s;
+    if (items < 1 || B > kJoinMaxSeqs)
+        return {0, 1};
+    if (items < kWideSms) {
+        long long s = (2 * kWideSms + items - 1) / items;
+        if (s > tiles / kMinSplitTiles)
+            s = tiles / kMinSplitTiles;
+        return {0, s < 1 ? 1 : (int)s};
+    }
+    const long long rounds = items / kWideSms, left = items % kWideSms;
+    if (rounds > 4 || left == 0)  // (the pieces' buffers hold all rows, 400 MB with four)
+        return {0, 1};
+    // the last round has the shortest items, the start of the longest sequence's new
+    // tokens at least (where they vary more, the longest-first order fills the SMs)
+    const long long item = (max_ctx - max_q) / 128 * 3200;
+    WideSplit best = {0, 1};
+    long long least = item + 8000 - (rounds * item) / 20;  // a twentieth of the call at least
+    for (int s = 2; s <= 4; s++) {
+        const long long pieces = (left * s + kWideSms - 1) / kWideSms;
+        const long long cost = pieces * (item / s + 8000) + left * s * 75 + 20000;
+        if (cost < least) {
+            least = cost;
+            best = {(int)(rounds * kWideSms), s};
+        }
+    }
+    return best;
 }
 cudaError_t launch_prefill_join(int D, const PrefillParams &p, cudaStream_t stream);
 constexpr int kPrefillRows = 128;  // (token, head) rows per query tile (two tiles per work item)

@@ -26,7 +26,9 @@
 //  * Few rows over long contexts (a short chunk on a long prefix) leave most SMs
 //    without an item: the host then splits every item's key tiles over up to
 //    p.splits CTAs.  Each leaves its rows' outputs (fp32) and log-sum-exps in
-//    the workspace; pkv_prefill_join.cu puts them together.
+//    the workspace; pkv_prefill_join.cu puts them together.  So are the items of
+//    an incomplete last round, where there are few rounds of long ones
+//    (wide_split).
 //
 // Warps (352 threads): 0..3 softmax of query tile A, 4..7 of tile B (thread =
 // row = TMEM lane); 8 producer; 9, 10 the MMAs of tiles A and B.
@@ -115,7 +117,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kBoxes = kWKeys / kBox;          // 16-token boxes per tile
     constexpr unsigned FULL = 0xffffffffu;
     constexpr float kLazy = 8.f;
-    const int splits = SPLIT ? p.splits : 1;
+    const int splits = SPLIT ? p.splits : 1, whole = SPLIT ? p.whole : 0;
+    const long long units = SPLIT ? whole + (long long)(p.n_items - whole) * splits : p.n_items;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -201,9 +204,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             PrefillItem &it = item.f;
             for (; ok; k++) {
                 const long long at = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
-                if (at >= (long long)p.n_items * splits)
+                if (at >= units)
                     break;
-                const int pos = SPLIT ? (int)(at / splits) : (int)at;
+                const int pos = SPLIT && at >= whole ? whole + (int)((at - whole) / splits) : (int)at;
                 const PrefillWork w = p.B <= 32 ? prefill_schedule<2 * TPC, 1>(p, lane, pos)
                                                 : prefill_schedule<2 * TPC, kSchedChunks>(p, lane, pos);
                 int cq0 = w.cq0, cq1 = w.cq1, ck0 = w.ck0, ck1 = w.ck1;
@@ -228,9 +231,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     it.nkt[1] = tok0 + TPC < it.q_len
                                     ? (base + min(it.q_len, tok0 + 2 * TPC) - 1) / kWKeys + 1
                                     : 0;
-                    if constexpr (SPLIT) {
+                    if constexpr (SPLIT)
+                        item.split = -1;
+                    if (SPLIT && at >= whole) {
                         const int chunk = wide_chunk(max(it.nkt[0], it.nkt[1]), splits);
-                        item.split = (int)(at - (long long)pos * splits);
+                        item.split = (int)((at - whole) - (long long)(pos - whole) * splits);
                         item.j0 = item.split * chunk;
                         for (int t = 0; t < 2; t++)
                             it.nkt[t] = min(max(it.nkt[t] - item.j0, 0), chunk);
@@ -726,7 +731,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if ((vmax & 0x7fffu) >= 0x7bffu || ((vmax >> 16) & 0x7fffu) >= 0x7bffu)
                 flag_error(p.err_flag, kFlagVRange);
             // a split that only the other query tile has keys in
-            if (SPLIT && nkt == 0 && valid)
+            const bool piece = SPLIT && item.split >= 0;
+            if (piece && nkt == 0 && valid)
                 p.part_lse[(size_t)item.split * p.Tq * p.Hq +
                            ((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] = -INFINITY;
             if (nkt > 0) {
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const size_t row = (size_t)it.cq0 + tok;
                 const size_t lse_at = ((size_t)it.kvh * p.Tq + row) * G + g;
-                if constexpr (SPLIT) {
+                if (piece) {
                     // this split's output in fp32, and its log-sum-exp (-inf: no key)
                     if (valid)
                         p.part_lse[(size_t)item.split * p.Tq * p.Hq + lse_at] =
@@ -762,8 +768,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 } else {
                     // for the attention weights; +inf (weight 0) for a row that could
                     // read no key
-                    if (valid)
+                    if (valid) {
                         p.lse[lse_at] = l == 0.f ? INFINITY : m + log2f(l);
+                        if (SPLIT)
+                            p.part_lse[lse_at] = INFINITY;  // nothing to join
+                    }
                     // 64 columns (eight 16-byte pieces) of a row at a time; eight lanes
                     // trade their rows' pieces (three butterfly steps), so that a store
                     // instruction writes whole 128-byte lines of four rows, not 16 bytes

@@ -301,6 +301,19 @@ def test_prompt_weights_few_rows_over_long_contexts(pkv, D, G, Hkv, q_lens, cont
         check_prompt(pkv, c, q_lens, G, window, seed=G, pad_rows=2)
 
 
+@pytest.mark.parametrize("D,G,Hkv,q_lens,contexts", [
+    (64, 8, 4, [640, 1, 513], [4200, 1, 700]),    # 240 items at most, 148 with work
+    (128, 4, 8, [1300], [2500]),                  # 168
+    (64, 2, 8, [1300, 1290], [1900, 6200]),       # 176: the second sequence's are the longer ones
+    (128, 8, 10, [512], [3500]),                  # 160
+])
+def test_prompt_weights_last_round_split(pkv, D, G, Hkv, q_lens, contexts):
+    """A few more items than SMs: those of the last round are split over the keys, the others are not."""
+    c = ref.Cache(contexts, 64, Hkv, D, seed=G, mbs_extra=1)
+    c.tables = np.concatenate([c.tables, np.full((len(contexts), 70), -1, c.tables.dtype)], axis=1)
+    check_prompt(pkv, c, q_lens, G, 16, seed=G, pad_rows=5)
+
+
 def test_prompt_weights_split_with_unreadable_pieces(pkv):
     """A split none of whose blocks can be read, and a sequence without any, join to the rest and to zeros."""
     c = ref.Cache([4096, 2048], 64, 2, 64, seed=5)

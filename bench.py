@@ -58,7 +58,7 @@ FP8_METRIC = "paged decode attention, FP8 (E4M3) KV cache: KV GB/s & % of HBM pe
 PREFILL_WORKLOAD = "qwen3_prefill_16k"  # the 16384-token Qwen3-0.6B-shaped prefill step
 CPU_BUDGET_S = 8.0  # seconds of oracle work per cpu_baseline run (one core, then all cores)
 PREFILL_SOURCES = ["pkv_prefill_tc.cuh", "pkv_prefill.h", "pkv_tc.cuh", "pkv_kernels.h", "pkv_ptx.cuh"]
-DECODE_SOURCES = ["pkv_decode.cuh", "pkv_merge.cu", "pkv_kernels.h", "pkv_ptx.cuh"]
+DECODE_SOURCES = ["pkv_decode.cuh", "pkv_merge.cu", "pkv_merge.cuh", "pkv_kernels.h", "pkv_ptx.cuh"]
 
 
 def parse_args(argv=None):

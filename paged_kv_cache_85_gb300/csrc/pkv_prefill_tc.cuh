@@ -579,11 +579,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int g0 = 0;    // K/V tiles of the previous items
         int gq = 0;    // S/P tiles of this Q tile over the previous items
         int used = 0;  // items in which this Q tile had work (its epilogues)
-        // one elected lane waits, issues the MMAs and commits (elect.sync, not lane
-        // == 0: the compiler then knows that a single thread issues, and an MMA
-        // costs the thread 45 cycles instead of 75)
-        const bool leader = tc::elect_one();
-        if (leader) {
+        // lane 0 alone waits, issues the MMAs and commits
+        if (lane == 0) {
             for (int n = 0; ok; n++) {
                 if (!(ok = mbar_wait(&item_ready[n & 1], (n >> 1) & 1)))
                     break;
@@ -675,10 +672,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         __syncwarp();
-        if (!ok && leader)
+        if (!ok && lane == 0)
             flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
         // every MMA issued has completed before TMEM is released
-        if (leader)
+        if (lane == 0)
             tc::commit(smem_u32(mma_done));
         __syncwarp();
         mbar_wait(mma_done, 0);

@@ -329,17 +329,18 @@ pkv_status pkv_paged_attn_decode_noalloc(const void *q, const void *k_cache, con
  *     p[i, h, t]
  * to weights[block of t, kv head, offset of t].  For the tokens that are new
  * in the call (the last context token of a decode step, the q_len new tokens
- * of a prefill step) it is stored instead of added, so a slot's earlier
- * content never needs clearing: every token's weight starts with the step that
- * stores it.  A token stored by a step whose attention does not record has the
- * weight its slot had before; set it where that matters.
+ * of a prefill step) the slot is set to zero before anything is added, so its
+ * earlier content never needs clearing: every token's weight starts with the
+ * step that stores it.  A token stored by a step whose attention does not
+ * record has the weight its slot had before; set it where that matters.
  *
  * p is formed in fp32 from the fp32 scores and the row's fp32 log-sum-exp.
  * Blocks shared by several sequences of a call receive every sequence's
- * addition, in no fixed order (fp32 sums may differ in the last bits from run
- * to run); without shared blocks the results are the same in every run.  The
- * weights belong to the blocks: a prompt that reuses cached prefix blocks adds
- * to what those blocks had gathered.
+ * addition, also where they are new to one of them in this call (two prompts
+ * with a common prefix in one step), in no fixed order (fp32 sums may differ in
+ * the last bits from run to run); without shared blocks the results are the
+ * same in every run.  The weights belong to the blocks: a prompt that reuses
+ * cached prefix blocks adds to what those blocks had gathered.
  * Tokens of blocks outside [0, NB) have no weight and receive none.  A query
  * row whose scores contain a NaN or +inf adds NaN to the tokens it sees.
  */

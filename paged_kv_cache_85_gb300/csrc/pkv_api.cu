@@ -854,6 +854,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     p.tile_copies = tile_copies ? 1 : 0;
     if (record) {
         p.lse = static_cast<float *>(workspace);
+        p.weights = weights;
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
         p.splits = splits;
         p.whole = split.whole;
@@ -901,7 +902,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
             return fail(PKV_ERR_CUDA, "paged_prefill_weights join launch: %s", cudaGetErrorString(e));
     }
     if (record) {
-        e = pkv::launch_prompt_weights(D, G, &tmq, &tmk, p, weights, window, st->sms,
+        e = pkv::launch_prompt_weights(D, G, &tmq, &tmk, p, window, st->sms,
                                        static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
             return fail(PKV_ERR_CUDA, "paged_prefill_weights launch: %s", cudaGetErrorString(e));

@@ -25,6 +25,8 @@ struct PrefillParams {
     int neg_scale;                // scale < 0: the score MMA negates Q
     int tile_copies;              // bs % 64 == 0: K/V maps copy whole 64-token tiles
     float *lse = nullptr;         // nullable: [Hkv, Tq, G] log-sum-exp of every row (log2 units)
+    float *weights = nullptr;     // [NB, Hkv, bs], where lse is: cleared for the new tokens by the
+                                  // attention, added to by the weights kernel
     // 128-key kernel, where its items are split over the keys (splits > 1)
     int splits = 1;
     int whole = 0;                // the first (longest) items, which are not split
@@ -59,8 +61,7 @@ inline bool pw_may_split(int B, long long Tq, int max_q, int G, int Hkv)
 constexpr size_t kPwCountBytes = (size_t)kPwFewUnits * 8 * sizeof(int32_t);
 constexpr size_t kPwPartBytes = (size_t)kPwFewUnits * kPwMaxSplits * 256 * sizeof(float);
 cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
-                                  const PrefillParams &p, float *weights, int window, int sms,
-                                  cudaStream_t stream);
+                                  const PrefillParams &p, int window, int sms, cudaStream_t stream);
 const void *prompt_weights_kernel_fn(int D, int G, bool split);
 size_t prompt_weights_smem_bytes(int D);
 const void *prefill_kernel(int D, int G, bool wide, bool split);

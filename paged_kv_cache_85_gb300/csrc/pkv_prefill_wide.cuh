@@ -1,5 +1,6 @@
 // Paged prefill attention with 128-key tiles, for the call that also records
-// attention weights (it leaves every row's log-sum-exp for pkv_prompt_weights.cu).
+// attention weights (it leaves every row's log-sum-exp for pkv_prompt_weights.cu
+// and clears the weights of the new tokens).
 //
 // What it computes, its work items, their order, its precision (scores in bf16,
 // P.V in f16, fp32 sums) and its flags are those of pkv_prefill_tc.cuh; the
@@ -367,6 +368,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok)
                 break;  // the other warps time out on their barriers and stop
+            // ---- the item's new tokens start from weight 0: the weights kernel, which
+            // waits for this one, only adds (to blocks that other sequences may share)
+            if (!SPLIT || item.split <= 0) {
+                const int t0 = it.k_len - it.q_len + it.tok0, nt = min(2 * TPC, it.q_len - it.tok0);
+                for (int i = lane; i < nt; i += 32) {
+                    const int t = t0 + i, blk = __ldg(table + t / p.bs);
+                    if (blk >= 0 && blk < p.NB)
+                        p.weights[((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs] = 0.f;
+                }
+            }
         }
         if (lane == 0) {
             if (!ok)

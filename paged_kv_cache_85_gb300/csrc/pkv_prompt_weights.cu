@@ -7,8 +7,10 @@
 //     w[t] = sum over recorded new tokens i that see t, and over the G heads
 //            of the group, of 2^(s[i, g, t] - lse[i, g]),
 // which needs the final lse of every row, so the scores are made again here.
-// It is added to weights[block, kv head, offset], or stored there for the
-// step's new tokens, whose slots may hold what an earlier owner left.
+// It is added to weights[block, kv head, offset].  The slots of the step's new
+// tokens, which may hold what an earlier owner left, were cleared by the prefill
+// kernel: a block that is new to one sequence of the step may be another one's
+// prefix, so that all additions to it have to come after that.
 //
 // The scores are made transposed, S^T = K Q^T with the cached tokens as the
 // MMA's rows, so that a thread owns one token (a TMEM lane) and the sum over
@@ -114,7 +116,6 @@ __host__ __device__ inline PwSmem pw_smem_layout(int D)
 
 struct PwParams {
     PrefillParams f;   // the prefill call's (q, lengths, tables, lse, scale)
-    float *weights;
     int window;        // 0: every new token records
 };
 
@@ -607,13 +608,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                             sum += __ldcg(mine + (size_t)i * 2 * kPwTokens);
                     }
                 }
-                if (write && blk >= 0 && blk < p.NB) {
-                    float *dst = P.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs;
-                    if (t >= base)
-                        *dst = sum;
-                    else
-                        atomicAdd(dst, sum);
-                }
+                // an addition for new tokens too (the attention cleared their slots):
+                // another sequence of the call may have them as its prefix
+                if (write && blk >= 0 && blk < p.NB)
+                    atomicAdd(p.weights + ((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs, sum);
             }
             __syncwarp();
             if (lane == 0)
@@ -653,12 +651,10 @@ const void *prompt_weights_kernel_fn(int D, int G, bool split)
 size_t prompt_weights_smem_bytes(int D) { return pw_smem_layout(D).total; }
 
 cudaError_t launch_prompt_weights(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
-                                  const PrefillParams &p, float *weights, int window, int sms,
-                                  cudaStream_t stream)
+                                  const PrefillParams &p, int window, int sms, cudaStream_t stream)
 {
     PwParams P;
     P.f = p;
-    P.weights = weights;
     P.window = window;
     // no more CTAs than items there can be
     const long long tiles = ((long long)p.MBS * p.bs + 2 * kPwTokens - 1) / (2 * kPwTokens);

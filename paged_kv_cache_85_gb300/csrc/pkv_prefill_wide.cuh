@@ -272,6 +272,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (it.b < 0)
                 break;
+            // ---- the item's new tokens start from weight 0: the weights kernel, which
+            // waits for this one, only adds (to blocks that other sequences may share).
+            // Here, where the producer would wait for the last item's Q: 16k step 411 ->
+            // 415 us; after the item's last copy 420, by the softmax threads 422.
+            if (!SPLIT || item.split <= 0) {
+                const int t0 = it.k_len - it.q_len + it.tok0, nt = min(2 * TPC, it.q_len - it.tok0);
+                for (int i = lane; i < nt; i += 32) {
+                    const int t = t0 + i, blk = __ldg(p.block_tables + (size_t)it.b * p.MBS + t / p.bs);
+                    if (blk >= 0 && blk < p.NB)
+                        p.weights[((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs] = 0.f;
+                }
+            }
             // ---- Q tiles, each once its tile's last S of the previous item completed
             for (int t = 0; t < 2 && ok; t++) {
                 if (it.nkt[t] == 0)
@@ -368,16 +380,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok)
                 break;  // the other warps time out on their barriers and stop
-            // ---- the item's new tokens start from weight 0: the weights kernel, which
-            // waits for this one, only adds (to blocks that other sequences may share)
-            if (!SPLIT || item.split <= 0) {
-                const int t0 = it.k_len - it.q_len + it.tok0, nt = min(2 * TPC, it.q_len - it.tok0);
-                for (int i = lane; i < nt; i += 32) {
-                    const int t = t0 + i, blk = __ldg(table + t / p.bs);
-                    if (blk >= 0 && blk < p.NB)
-                        p.weights[((size_t)blk * p.Hkv + it.kvh) * p.bs + t % p.bs] = 0.f;
-                }
-            }
         }
         if (lane == 0) {
             if (!ok)

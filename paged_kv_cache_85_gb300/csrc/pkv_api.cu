@@ -591,6 +591,7 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     p.v_scale = f8 ? v_scale : 1.f;
     if (record) {
         uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.weights = weights;
         p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_at);
         p.ws_box = reinterpret_cast<int4 *>(ws + plan.box_at);
         p.ws_score = reinterpret_cast<float *>(ws + plan.score_at);
@@ -608,7 +609,7 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
         if ((ps = device_state(&st)) != PKV_OK)
             return ps;
         const long long boxes = (long long)B * Hkv * (((long long)MBS * bs + plan.bt - 1) / plan.bt);
-        e = pkv::launch_merge_and_add(D, plan.G, plan.bt, f8, p, weights, boxes, st->sms, s);
+        e = pkv::launch_merge_and_add(D, plan.G, plan.bt, f8, p, boxes, st->sms, s);
     }
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "merge launch: %s", cudaGetErrorString(e));

@@ -269,9 +269,13 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
             m.blk = blk;
             if constexpr (WT) {
                 m.box = pos;
-                // for the weights kernel; a stream's last box ends in the step's new token
-                p.ws_box[pos] = make_int4(b, loaded ? blk : -1, tok0 % p.bs,
-                                          m.nvalid | (j == nb - 1 ? kBoxNewest : 0));
+                // for the weights kernel
+                p.ws_box[pos] = make_int4(b, loaded ? blk : -1, tok0 % p.bs, m.nvalid);
+                // A stream's last box ends in the step's new token, whose weight starts
+                // from 0: the weights kernel, which waits for this one, only adds (other
+                // sequences of the step may share the block).
+                if (j == nb - 1 && loaded)
+                    p.weights[((size_t)blk * p.Hkv + h) * p.bs + tok0 % p.bs + m.nvalid - 1] = 0.f;
             }
             // advance both cursors
             next_box(pb, p.B, cb, ch, cj);

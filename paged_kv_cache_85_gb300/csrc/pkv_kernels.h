@@ -45,10 +45,11 @@ struct DecodeParams {
     float v_scale;                // FP8 caches: dequant scale of V (1 for bf16)
     // The calls that record attention weights; null elsewhere.
     float *ws_lse = nullptr;      // [B, Hq] log-sum-exp (log2 units) of rows that one worker read whole
-    int4 *ws_box = nullptr;       // per box: sequence, block (-1: not read), offset, valid tokens | kBoxNewest
+    int4 *ws_box = nullptr;       // per box: sequence, block (-1: not read), offset, valid tokens
     float *ws_score = nullptr;    // per box: [G][box tokens] scores (log2 units; FP8: [box tokens][G])
+    float *weights = nullptr;     // [NB, Hkv, bs]: cleared for the step's new tokens by the decode
+                                  // kernel, added to by the merge
 };
-constexpr int kBoxNewest = 1 << 16;  // the box's last valid token is the step's new token
 
 // Host launchers (defined next to their kernels).
 cudaError_t launch_store(const void *k, const void *v, void *k_cache, void *v_cache,
@@ -60,6 +61,6 @@ cudaError_t launch_store_fp8(const void *k, const void *v, void *k_cache, void *
                              cudaStream_t stream);
 cudaError_t launch_merge(int D, int G, const DecodeParams &p, cudaStream_t stream);
 cudaError_t launch_merge_and_add(int D, int G, int bt, bool token_major, const DecodeParams &p,
-                                 float *weights, long long max_boxes, int sms, cudaStream_t stream);
+                                 long long max_boxes, int sms, cudaStream_t stream);
 
 } // namespace pkv

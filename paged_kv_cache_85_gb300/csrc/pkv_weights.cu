@@ -6,8 +6,10 @@
 // units) of its tokens for the G query heads of the group.  A token's weight
 // in this step is the sum of its G softmax values,
 //     w = sum_g 2^(s[g][t] - lse[g]),
-// added to weights[block, kv head, offset], or stored there for the step's
-// newest token, whose slot may hold what an earlier owner of the block left.
+// added to weights[block, kv head, offset].  The slot of the step's newest token,
+// which may hold what an earlier owner of the block left, was cleared by the
+// decode kernel: sequences may share the block it lies in, so that all additions
+// have to come after that.
 // lse[g] is the row's log-sum-exp: left by the worker that read the whole
 // stream, or M + log2(sum_i 2^(m_i - M) l_i) over the pieces (m_i, l_i) of a
 // split one, which each warp forms for the streams it meets, so that the
@@ -89,7 +91,7 @@ __device__ __forceinline__ void stream_lse(const DecodeParams &p, const Slices &
 // TM: the scores are token-major ([BT][G], FP8 caches), else [G][BT].
 template <int D, int G, int BT, bool TM>
 __global__ void __launch_bounds__(kAddThreads, G == 8 ? 4 : 8)
-    merge_and_add_kernel(const DecodeParams p, float *__restrict__ weights, int add_ctas)
+    merge_and_add_kernel(const DecodeParams p, int add_ctas)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int kQuads = BT / 4;  // threads per box
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kAddThreads, G == 8 ? 4 : 8)
         const int h = box / S.per_head;
         // a decode kernel that gave up waiting leaves descriptors unwritten: what
         // stands there then is checked before it is an address
-        const int nvalid = min(m.w & (kBoxNewest - 1), BT);
+        const int nvalid = min(m.w, BT);
         const bool valid = (unsigned)m.y < (unsigned)p.NB && (unsigned)m.x < (unsigned)p.B &&
                            (unsigned)m.z <= (unsigned)(p.bs - BT) && m.z % BT == 0 && i < nvalid;
         // the streams of these boxes, one after the other (mostly one, and the
@@ -185,24 +187,20 @@ __global__ void __launch_bounds__(kAddThreads, G == 8 ? 4 : 8)
                 w.w += fast_exp2(s[g].w - lse[g]);
             }
         }
-        float *dst = weights + ((size_t)m.y * p.Hkv + h) * p.bs + m.z + i;
-        const bool newest = (m.w & kBoxNewest) != 0;
-        if (i + 4 <= nvalid - (newest ? 1 : 0)) {
+        float *dst = p.weights + ((size_t)m.y * p.Hkv + h) * p.bs + m.z + i;
+        if (i + 4 <= nvalid) {
             atomicAdd(reinterpret_cast<float4 *>(dst), w);
-        } else {  // the context's last tokens: none past it, and the newest one is set
+        } else {  // none past the context's last token
             const float x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                if (newest && i + k == nvalid - 1)
-                    dst[k] = x[k];
-                else if (i + k < nvalid)
+            for (int k = 0; k < 3; k++)
+                if (i + k < nvalid)
                     atomicAdd(dst + k, x[k]);
-            }
         }
     }
 }
 
-cudaError_t launch_merge_and_add(int D, int G, int bt, bool token_major, const DecodeParams &p, float *weights,
+cudaError_t launch_merge_and_add(int D, int G, int bt, bool token_major, const DecodeParams &p,
                                  long long max_boxes, int sms, cudaStream_t stream)
 {
     const long long rows = (long long)p.B * p.Hq;
@@ -223,7 +221,7 @@ cudaError_t launch_merge_and_add(int D, int G, int bt, bool token_major, const D
     cfg.numAttrs = 1;
 #define PKV_ADD(DD, GG, BB, TM)                                  \
     if (D == DD && G == GG && bt == BB && token_major == TM) \
-        return cudaLaunchKernelEx(&cfg, merge_and_add_kernel<DD, GG, BB, TM>, p, weights, (int)add);
+        return cudaLaunchKernelEx(&cfg, merge_and_add_kernel<DD, GG, BB, TM>, p, (int)add);
 #define PKV_ADD2(DD, GG) \
     PKV_ADD(DD, GG, kBox, false) PKV_ADD(DD, GG, kBox, true) PKV_ADD(DD, GG, 2 * kBox, true)
     PKV_ADD2(64, 1) PKV_ADD2(64, 2) PKV_ADD2(64, 4) PKV_ADD2(64, 8)

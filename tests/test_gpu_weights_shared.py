@@ -105,3 +105,32 @@ def test_long_common_prefix_in_one_step(pkv, first, window):
     new = [(b, int(c.lens[b]) - q_lens[b]) for b in range(4)]
     fill(c, 6, stale=new)
     check_prompt(pkv, c, q_lens, 8, window, new)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("backwards", [False, True])
+@pytest.mark.parametrize("D,G,bs,lens", [(64, 2, 16, [50, 50, 130, 40, 51]), (128, 4, 32, [3001, 3001, 3400, 97, 3002]), (64, 8, 48, [48, 48, 49, 1, 97])])
+def test_decode_of_a_sequence_whose_newest_token_another_one_sees(pkv, fp8, backwards, D, G, bs, lens):
+    """A step that holds a sequence twice, and sequences that go on from its newest token: each adds to the shared
+    blocks, the newest token's included, over stale NaN weights."""
+    c = ref.Cache(lens, bs, 2, D, fp8=fp8, seed=2)
+    n = -(-lens[0] // bs)
+    for b in (1, 2, 4):
+        c.tables[b, :n] = c.tables[0, :n]
+    if backwards:
+        c.tables, c.lens = c.tables[::-1].copy(), c.lens[::-1].copy()
+    new = [(b, int(c.lens[b]) - 1) for b in range(5)]
+    fill(c, 8, stale=new)
+    scale = D ** -0.5
+    qb = ref.to_bf16(1.5 * np.random.default_rng(5).standard_normal((5, 2 * G, D), dtype=np.float32))
+    _, _, add, big = ref.decode(c, ref.from_bf16(qb), scale)
+    want = expected(c, add, new)
+    q, k, v, t, ctx = dev(qb), dev(c.k), dev(c.v), dev(c.tables), dev(c.lens)
+    scales = (c.k_scale, c.v_scale) if fp8 else ()
+    call = pkv.paged_attn_decode_weights_fp8 if fp8 else pkv.paged_attn_decode_weights
+    plain = pkv.paged_attn_decode_fp8 if fp8 else pkv.paged_attn_decode
+    for _ in range(3):
+        w = dev(c.w.copy())
+        out = call(q, k, v, t, ctx, scale, *scales, torch.empty_like(q), w)
+        assert torch.equal(out, plain(q, k, v, t, ctx, scale, *scales, torch.empty_like(q)))
+        ref.check_weights(w.cpu().numpy(), want, add, ref.weight_tolerance(D, big), "shared blocks")

@@ -160,17 +160,79 @@ __device__ __forceinline__ int box_block(const DecodeParams &p, int b, int j)
     return __ldg(p.block_tables + (size_t)b * p.MBS + (j * BT) / p.bs);
 }
 
-// Producer warp: lane w < NW runs worker w of this CTA.  Each lane
-// walks its own slice with two cursors: the issue cursor, and a look-ahead
-// cursor kLookahead boxes further on whose block ids are loaded into a small
-// register queue, so a copy never waits on a block-table read.  Per stage
-// every lane writes its worker's box descriptor and issues its own TMA
-// copies; lane 0 arms the stage's mbarrier with the summed byte count.
+// How the concatenated streams are cut: with at least one worker per KV head,
+// each head's region gets W / Hkv workers and is cut on its own, so worker w and
+// worker w + W / Hkv read the same (sequence, box) of two heads at the same time;
+// otherwise one region spans all heads.
+struct Slicing {
+    int R, Tr, Wr, P;  // regions; per region: boxes, workers; boxes per worker
+};
+
+__device__ __forceinline__ Slicing slicing(const DecodeParams &p, const int *pb, int W)
+{
+    Slicing S;
+    S.R = W >= p.Hkv ? p.Hkv : 1;
+    S.Tr = pb[p.B] * (p.Hkv / S.R);
+    S.Wr = W / S.R;
+    S.P = S.Tr > 0 ? (S.Tr + S.Wr - 1) / S.Wr : 1;
+    return S;
+}
+
+// A producer lane's walk over its worker's slice: the issue cursor (box pos of
+// the streams), and a look-ahead cursor kLookahead boxes further on whose block
+// ids are loaded into a small register queue, so a copy never waits on a
+// block-table read.
+struct ProducerWalk {
+    int start, end;
+    int cb, ch, cj;       // the first box: sequence, KV head, box of the stream
+    int lb, lh, lj, lpos; // look-ahead
+    int qb[kLookahead];   // qb[(pos - start) % kLookahead]: block id of box pos
+};
+
+// Lane w < NW runs worker w of this CTA: worker gw owns slice gw % Wr of region
+// gw / Wr (regions past R idle).
+template <int NW>
+__device__ __forceinline__ void walk_start(const DecodeParams &p, const int *pb, const Slicing &S, int lane,
+                                           ProducerWalk &w)
+{
+    const int gw = blockIdx.x * NW + lane;
+    const int r = gw / S.Wr;
+    w.start = w.end = 0;
+    if (lane < NW && r < S.R) {
+        const long long lo = (long long)(gw - r * S.Wr) * S.P;
+        w.start = r * S.Tr + (int)(lo < S.Tr ? lo : S.Tr);
+        w.end = r * S.Tr + (int)(lo + S.P < S.Tr ? lo + S.P : S.Tr);
+    }
+    w.cb = w.ch = w.cj = 0;
+    if (w.start < w.end)
+        locate_box(w.start, pb, p.B, w.cb, w.ch, w.cj);
+}
+
+template <int BT>
+__device__ __forceinline__ void walk_ahead(const DecodeParams &p, const int *pb, ProducerWalk &w)
+{
+    w.lb = w.cb;
+    w.lh = w.ch;
+    w.lj = w.cj;
+    w.lpos = w.start;
+#pragma unroll
+    for (int i = 0; i < kLookahead; i++) {
+        w.qb[i] = -1;
+        if (w.lpos < w.end) {
+            w.qb[i] = box_block<BT>(p, w.lb, w.lj);
+            next_box(pb, p.B, w.lb, w.lh, w.lj);
+        }
+        ++w.lpos;
+    }
+}
+
+// Producer warp.  Per stage every lane writes its worker's box descriptor and
+// issues its own TMA copies; lane 0 arms the stage's mbarrier with the summed
+// byte count.
 template <int D, int G, int NW, bool F8, int BT, bool WT>
 __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CUtensorMap *tmv,
                                                 const DecodeParams &p, uint8_t *smem,
-                                                const DecodeSmem &L, int lane, int R, int Tr,
-                                                int Wr, int P)
+                                                const DecodeSmem &L, int lane, ProducerWalk &w)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int kBoxBytes = BT * D * (F8 ? 1 : 2);
@@ -188,39 +250,13 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
     if constexpr (WT && !F8)
         once = l2_evict_first();
 
-    if (lane == 0) {
-        prefetch_tensormap(tmk);
-        prefetch_tensormap(tmv);
-    }
-    // Worker gw owns slice gw % Wr of region gw / Wr (regions past R idle).
     const bool worker = lane < NW;
-    const int gw = blockIdx.x * NW + lane;
-    const int r = gw / Wr;
-    int start = 0, end = 0;
-    if (worker && r < R) {
-        const long long lo = (long long)(gw - r * Wr) * P;
-        start = r * Tr + (int)(lo < Tr ? lo : Tr);
-        end = r * Tr + (int)(lo + P < Tr ? lo + P : Tr);
-    }
+    const int start = w.start, end = w.end;
     int pos = start;
-    int cb = 0, ch = 0, cj = 0;  // issue cursor
-    if (start < end)
-        locate_box(start, pb, p.B, cb, ch, cj);
-    int lb = cb, lh = ch, lj = cj, lpos = start;  // look-ahead cursor
-    int qb[kLookahead];  // qb[(pos - start) % kLookahead]: block id of box pos, loaded ahead
-#pragma unroll
-    for (int i = 0; i < kLookahead; i++) {
-        qb[i] = -1;
-        if (lpos < end) {
-            qb[i] = box_block<BT>(p, lb, lj);
-            next_box(pb, p.B, lb, lh, lj);
-        }
-        ++lpos;
-    }
+    int cb = w.cb, ch = w.ch, cj = w.cj;                    // issue cursor
+    int lb = w.lb, lh = w.lh, lj = w.lj, lpos = w.lpos;     // look-ahead cursor
+    auto &qb = w.qb;
     bool first_done = false;
-
-    // K/V may have just been written by store_kvcache on this stream.
-    grid_dependency_wait();
 
     int stage = 0;
     uint32_t phase = 0;
@@ -901,29 +937,25 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
     }
 }
 
+__device__ __forceinline__ int clamp_len(int n, int maxctx) { return n < 0 || n > maxctx ? (n < 0 ? 0 : maxctx) : n; }
+
 // Per-sequence clamped lengths and the exclusive prefix sum of their box
 // counts (boxes of BT tokens per KV head before sequence b), b = 0..B.
+// settled: the lengths are no longer being written.
 template <int BT>
-__device__ __forceinline__ void build_prefix(const DecodeParams &p, int *pb, int *len, int *wsum)
+__device__ __forceinline__ void build_prefix(const DecodeParams &p, int *pb, int *len, int *wsum, bool settled)
 {
     const int tid = threadIdx.x, nt = blockDim.x;
     const int lane = tid & 31, warp = tid >> 5;
     const int maxctx = p.MBS * p.bs;
     const int per = (p.B + nt - 1) / nt;
     const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
-    bool bad = false;
     int local = 0;
     for (int b = lo; b < hi; b++) {
-        int n = __ldg(p.context_lens + b);
-        if (n < 0 || n > maxctx) {
-            bad = true;
-            n = n < 0 ? 0 : maxctx;
-        }
+        const int n = clamp_len(settled ? ld_gpu(p.context_lens + b) : __ldg(p.context_lens + b), maxctx);
         len[b] = n;
         local += (n + BT - 1) / BT;
     }
-    if (bad && blockIdx.x == 0)
-        flag_error(p.err_flag, 0x4 /* PKV_FLAG_BAD_CONTEXT_LEN */);
     int incl = local;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -954,6 +986,28 @@ __device__ __forceinline__ void build_prefix(const DecodeParams &p, int *pb, int
     __syncthreads();
 }
 
+// Whether one of this thread's share of the lengths reads otherwise than
+// build_prefix found it; reports those out of range.  Four loads in flight.
+__device__ __forceinline__ bool lengths_changed(const DecodeParams &p, const int *len)
+{
+    const int maxctx = p.MBS * p.bs;
+    bool changed = false, bad = false;
+    for (int b0 = threadIdx.x; b0 < p.B; b0 += 4 * blockDim.x) {
+        int n[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            n[i] = ld_gpu(p.context_lens + min(b0 + i * (int)blockDim.x, p.B - 1));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            bad |= n[i] < 0 || n[i] > maxctx;
+            changed |= clamp_len(n[i], maxctx) != len[min(b0 + i * (int)blockDim.x, p.B - 1)];
+        }
+    }
+    if (bad && blockIdx.x == 0)
+        flag_error(p.err_flag, 0x4 /* PKV_FLAG_BAD_CONTEXT_LEN */);
+    return changed;
+}
+
 // BT: tokens per box (16; 32 for FP8 caches whose block size is a multiple
 // of 32, which halves the per-box work of the producer and the consumers).
 template <int D, int G, int NW, bool F8, int BT, bool WT>
@@ -982,33 +1036,60 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
     }
     int *pb = reinterpret_cast<int *>(smem + L.pb);
     int *len = reinterpret_cast<int *>(smem + L.len);
-    build_prefix<BT>(p, pb, len, reinterpret_cast<int *>(smem + L.scan));  // ends with __syncthreads()
+    if (threadIdx.x == NW * 32) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
 
-    // Slicing: with at least one worker per KV head, each head's region of
-    // the concatenated streams gets W / Hkv workers and is cut on its own, so
-    // worker w and worker w + W / Hkv read the same (sequence, box) of two
-    // heads at the same time; otherwise one region spans all heads.
-    const int W = (int)gridDim.x * NW;       // workers
-    const int R = W >= p.Hkv ? p.Hkv : 1;    // regions
-    const int Tr = pb[p.B] * (p.Hkv / R);    // boxes per region
-    const int Wr = W / R;                    // workers per region
-    const int P = Tr > 0 ? (Tr + Wr - 1) / Wr : 1;
+    const int W = (int)gridDim.x * NW;  // workers
+
+    // The slices follow from the lengths, which an earlier kernel of the stream may
+    // still be writing (evict_kvcache, or one of the caller's).  They are worked out
+    // from what stands there now, while that kernel ends; once it has, the lengths
+    // are read again, beside the first block ids, and the slices made again where
+    // one differs.  (Waiting first: a tiny step 6.0 -> 7.7 us, 512 sequences 217.1 ->
+    // 218.6; so 6.4 and 217.1.)
+    int *scan = reinterpret_cast<int *>(smem + L.scan);
+    ProducerWalk walk;
+    auto plan = [&](bool settled) {
+        build_prefix<BT>(p, pb, len, scan, settled);  // ends with __syncthreads()
+        if (warp == NW)
+            walk_start<NW>(p, pb, slicing(p, pb, W), lane, walk);
+        // what earlier kernels wrote (these lengths, K/V rows of store_kvcache) and
+        // still read (the workspace) is behind this
+        grid_dependency_wait();
+        if (warp == NW)
+            walk_ahead<BT>(p, pb, walk);
+    };
+    // The same in two forms, for what the compiler makes of them: straight, the block
+    // ids of the bf16 kernel wait for the vote (tiny 6.4 -> 6.8 us); as a loop, the FP8
+    // consumers spill (512 sequences 134.6 -> 135.5).
+    if constexpr (F8) {
+        plan(false);
+        if (__syncthreads_or(lengths_changed(p, len)))
+            plan(true);
+    } else {
+        for (int pass = 0;; pass++) {
+            plan(pass > 0);
+            if (pass == 1 || !__syncthreads_or(lengths_changed(p, len)))
+                break;
+        }
+    }
 
     if (warp == NW) {
-        decode_producer<D, G, NW, F8, BT, WT>(&tmk, &tmv, p, smem, L, lane, R, Tr, Wr, P);
+        decode_producer<D, G, NW, F8, BT, WT>(&tmk, &tmv, p, smem, L, lane, walk);
     } else {
         if (blockIdx.x == 0) {
-            // Publish the box layout for the merge kernel (after the previous
-            // step's kernels, which may still read the workspace).
-            grid_dependency_wait();
+            // the box layout for the merge kernel
             for (int i = threadIdx.x; i <= p.B; i += NW * 32)
                 p.ws_hdr[kWsHeaderInts + i] = pb[i];
             if (threadIdx.x == 0) {
-                p.ws_hdr[0] = Tr;
-                p.ws_hdr[1] = P;
-                p.ws_hdr[2] = Wr;
+                const Slicing S = slicing(p, pb, W);
+                p.ws_hdr[0] = S.Tr;
+                p.ws_hdr[1] = S.P;
+                p.ws_hdr[2] = S.Wr;
                 p.ws_hdr[3] = p.B;
-                p.ws_hdr[4] = R;
+                p.ws_hdr[4] = S.R;
             }
         }
         if constexpr (F8)

@@ -435,13 +435,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int slice = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     grid_dependency_wait();
     const int2 moved = p.ws_moved[(size_t)b * p.Hkv + h];
-    if (slice == 0 && h == 0 && threadIdx.x == 0) {
-        // here, not in the selection: its CTAs all read the lengths, and out_lens
-        // may be (or overlap) context_lens.  The fence makes it visible to a next
-        // kernel that starts as soon as this one's CTAs have left.
+    // here, not in the selection: its CTAs all read the lengths, and out_lens may be
+    // (or overlap) context_lens
+    if (slice == 0 && h == 0 && threadIdx.x == 0)
         p.out_lens[b] = moved.y;
-        __threadfence();
-    }
     if (moved.x >= moved.y)
         return;
     const int32_t *src = p.ws_src + ((size_t)b * p.Hkv + h) * p.keep;

@@ -25,11 +25,12 @@ __global__ void __launch_bounds__(kStoreThreads)
     grid_launch_dependents();
     const int64_t i = blockIdx.x;
     const int64_t slot = __ldg(slot_mapping + i);
-    if (slot == -1)
-        return;
     if (slot < 0 || slot >= n_slots) {
-        if (threadIdx.x == 0)
+        if (slot != -1 && threadIdx.x == 0)
             flag_error(err_flag, 0x1 /* PKV_FLAG_BAD_SLOT */);
+        // a step of nothing but padding must not end before the kernel ahead of it:
+        // the next one waits for this one only
+        grid_dependency_wait();
         return;
     }
     const uint4 *ks = k + i * row16;
@@ -80,11 +81,12 @@ __global__ void __launch_bounds__(kStoreThreads)
     grid_launch_dependents();
     const int64_t i = blockIdx.x;
     const int64_t slot = __ldg(slot_mapping + i);
-    if (slot == -1)
-        return;
     if (slot < 0 || slot >= n_slots) {
-        if (threadIdx.x == 0)
+        if (slot != -1 && threadIdx.x == 0)
             flag_error(err_flag, 0x1 /* PKV_FLAG_BAD_SLOT */);
+        // a step of nothing but padding must not end before the kernel ahead of it:
+        // the next one waits for this one only
+        grid_dependency_wait();
         return;
     }
     const uint4 *ks = k + i * row8;

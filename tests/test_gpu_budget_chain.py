@@ -102,3 +102,41 @@ def test_decode_right_after_lengths_written_on_the_gpu(pkv, fp8):
         assert torch.equal(out.view(torch.int16), want[i % 6].view(torch.int16))
     # lengths are judged as they are when the step's turn comes: none was out of range then
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("slot", [-1, 10 ** 6])
+def test_a_store_of_nothing_between_two_calls(pkv, fp8, slot):
+    """Calls that share a kept workspace, with a store between them that has only padding (or slots out of range): the
+    second call starts once the first has ended, not once the store has."""
+    rng = np.random.default_rng(2)
+    c = ref.Cache(rng.integers(300, 900, size=12), 16, 2, 64, seed=3)
+    B, G = 12, 8
+    k, v, t, ctx = dev(c.k), dev(c.v), dev(c.tables), dev(c.lens)
+    ql = rng.integers(100, 290, size=B)
+    cq, ck = (dev(np.concatenate([[0], np.cumsum(x)]).astype(np.int32)) for x in (ql, c.lens))
+    qp = dev(ref.to_bf16(rng.standard_normal((int(ql.sum()), 2 * G, 64), dtype=np.float32)))
+    q = dev(ref.to_bf16(rng.standard_normal((B, 2 * G, 64), dtype=np.float32)))
+    new = dev(ref.to_bf16(rng.standard_normal((B, 2, 64), dtype=np.float32)))
+    codes = torch.zeros((2, *c.k.shape), dtype=torch.uint8, device="cuda")
+    slots = torch.full((B,), slot, dtype=torch.int64, device="cuda")
+
+    def steps(wait):
+        w = dev(c.w.copy())
+        torch.cuda.synchronize()
+        for _ in range(4):
+            pkv.paged_prefill_weights(qp, k, v, t, cq, ck, int(ql.max()), 0.125, torch.empty_like(qp), w)
+            wait()
+            if fp8:
+                pkv.store_kvcache_fp8(new, new, codes[0], codes[1], slots, 1.0, 1.0)
+            else:
+                pkv.store_kvcache(new, new, k, v, slots)
+            wait()
+            pkv.paged_attn_decode_weights(q, k, v, t, ctx, 0.125, torch.empty_like(q), w)
+            wait()
+        torch.cuda.synchronize()
+        return w
+
+    want = steps(torch.cuda.synchronize)
+    for _ in range(10):
+        assert torch.equal(steps(lambda: None).view(torch.int32), want.view(torch.int32))

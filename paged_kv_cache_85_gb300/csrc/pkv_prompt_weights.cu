@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     k_len = kl;
                 }
             }
-            mine = (long long)((k_len + 2 * kPwTokens - 1) / (2 * kPwTokens)) * p.Hkv;
+            mine = (((long long)k_len + 2 * kPwTokens - 1) / (2 * kPwTokens)) * p.Hkv;
             incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -537,9 +537,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&s_empty[buf]);  // the scores are in registers
-                    // columns c0 <= c < c1 of this half are queries that see this token
-                    const int c0 = (t - base - i_first) * G - kCols * half;
-                    const int c1 = (it.q_len - i_first) * G - kCols * half;
+                    // columns c0 <= c < c1 of this half are queries that see this token (a
+                    // token far before them is seen by all: times G, 2^28 tokens pass 32 bits)
+                    const int c0 = max(t - base - i_first, 0) * G - kCols * half;
+                    const int c1 = min(it.q_len - i_first, TPC) * G - kCols * half;
                     float2 a0 = make_float2(0.f, 0.f), a1 = a0;
                     auto add = [&](auto masked_c) {
                         constexpr bool kMasked = decltype(masked_c)::value;

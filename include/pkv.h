@@ -390,10 +390,12 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
  *   workspace  device scratch of pkv_prefill_weights_workspace_bytes bytes for
  *              the same sizes, 16-byte aligned: every row's log-sum-exp, and,
  *              where max_seqlen_q, B and the heads make fewer than 152 items of
- *              256 (new token, head) rows, partial outputs of the keys' splits
- *              (at most some 45 MB; where they make up to 759 items of long
- *              contexts, the last of which are split, at most some 400 MB); with
- *              few new tokens and sequences, 2.5 MB of partial sums
+ *              256 (new token, head) rows, partial outputs of the keys' splits:
+ *              4 (D + 1) bytes per split and row of q, 60 MB for 151 items of
+ *              D = 128 in three splits, and more where q holds rows behind the
+ *              sequences' own (where there are up to 759 items of long contexts,
+ *              the last of which are split, at most some 400 MB); with few new
+ *              tokens and sequences, 2.5 MB of partial sums
  * B * Hkv * MBS * bs / 128 < 2^31.  A sequence that the attention skips
  * records nothing.  The scores of the recorded queries are made a second time
  * (their weights need each row's final sum), so recording every query adds

@@ -89,6 +89,9 @@ __host__ __device__ inline int wide_chunk(int nkt, int splits)
 struct WideSplit {
     int whole, splits;
 };
+// The lengths that this goes by are the tables' width and the longest chunk, which the
+// host knows.  With another number of SMs than this the pieces fill the last round less
+// well; the results are the same.
 constexpr long long kWideSms = 152;
 constexpr int kJoinMaxSeqs = 152;  // sequences that the join kernel can look through
 inline WideSplit wide_split(long long items, long long max_ctx, int max_q, int B)

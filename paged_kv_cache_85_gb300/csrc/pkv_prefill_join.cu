@@ -7,10 +7,11 @@
 // could read a key: weight 0, output 0).  The splits of a row follow from its
 // sequence's lengths as in the prefill kernel.
 //
-// One warp at a time per (row, query head).  Read once.  A few MB where few rows meet long
-// contexts: bound by its latency, which is why the sequences' boundaries are
-// searched in shared memory.  Where only the last round's items are split, up to
-// 80 MB; the other items' rows cost one load.
+// One warp at a time per (row, query head).  Read once.  Where few rows meet long
+// contexts from some KB to 60 MB (151 items in three splits): bound by its latency
+// where they are few, which is why the sequences' boundaries are searched in
+// shared memory.  Where only the last round's items are split, up to 80 MB; the
+// other items' rows cost one load.
 #include <cuda_bf16.h>
 
 #include "pkv_kernels.h"

@@ -399,6 +399,14 @@ def evict_workspace_bytes(B, Hkv, MBS, bs, budget) -> int:
     return int(load_library().pkv_evict_workspace_bytes(B, Hkv, MBS, bs, budget))
 
 
+def _c_int(value, name):
+    """``value`` as an int that fits a C int (ctypes would cut it to its lower 32 bits)."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name}={value} does not fit 32 bits")
+    return value
+
+
 def _tensors(torch, dev, *specs):
     """Check (tensor, name, dtype, dims) for each spec, all contiguous on CUDA device ``dev``."""
     for t, name, dtype, ndim in specs:
@@ -500,6 +508,7 @@ def _decode_weights(fp8, q, k_cache, v_cache, block_tables, context_lens, scale,
                     max_ctas, workspace, err_flag):
     import torch
 
+    max_ctas = _c_int(max_ctas, "max_ctas")
     dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, fp8)
     _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", torch.int32, 2),
              (context_lens, "context_lens", torch.int32, 1))
@@ -510,7 +519,7 @@ def _decode_weights(fp8, q, k_cache, v_cache, block_tables, context_lens, scale,
         raise ValueError("block_tables/context_lens batch != q batch")
     _result(torch, dev, out, q)
     flag = _flag(torch, dev, err_flag)
-    MBS, max_ctas = max(block_tables.shape[1], 1), int(max_ctas)
+    MBS = max(block_tables.shape[1], 1)
     lib = _lib or load_library()
     with _on_device(dev):
         stream = _raw_stream(dev)
@@ -556,6 +565,7 @@ def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_se
     """
     import torch
 
+    max_seqlen_q, window = _c_int(max_seqlen_q, "max_seqlen_q"), _c_int(window, "window")
     dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, False)
     i32 = torch.int32
     _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", i32, 2),
@@ -568,7 +578,7 @@ def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_se
         raise ValueError("cu_seqlens / block_tables batch sizes differ")
     _result(torch, dev, out, q)
     flag = _flag(torch, dev, err_flag)
-    MBS, max_seqlen_q = max(block_tables.shape[1], 1), int(max_seqlen_q)
+    MBS = max(block_tables.shape[1], 1)
     lib = _lib or load_library()
     with _on_device(dev):
         stream = _raw_stream(dev)
@@ -578,7 +588,7 @@ def paged_prefill_weights(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_se
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
             MBS, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
             max_seqlen_q, Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), weights.data_ptr(),
-            int(window), ws_ptr, ws_bytes, flag, stream))
+            window, ws_ptr, ws_bytes, flag, stream))
     return out
 
 
@@ -595,6 +605,7 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
     """
     import torch
 
+    budget, recent = _c_int(budget, "budget"), _c_int(recent, "recent")
     fp8 = isinstance(k_cache, torch.Tensor) and k_cache.dtype != torch.bfloat16
     dev, NB, bs, Hkv, D = _caches(torch, k_cache, v_cache, weights, fp8)
     i32 = torch.int32
@@ -604,7 +615,7 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
     if block_tables.shape[0] != B or out_lens.shape[0] != B:
         raise ValueError("block_tables/out_lens batch != context_lens batch")
     flag = _flag(torch, dev, err_flag)
-    MBS, budget = max(block_tables.shape[1], 1), int(budget)
+    MBS = max(block_tables.shape[1], 1)
     lib = _lib or load_library()
     with _on_device(dev):
         stream = _raw_stream(dev)
@@ -612,6 +623,6 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
             "pkv_evict_workspace_bytes", B, Hkv, MBS, bs, budget), dev, stream)
         _check(lib.pkv_evict_kvcache(
             k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_tables.data_ptr(), MBS,
-            context_lens.data_ptr(), B, Hkv, D, 1 if fp8 else 2, NB, bs, budget, int(recent),
+            context_lens.data_ptr(), B, Hkv, D, 1 if fp8 else 2, NB, bs, budget, recent,
             out_lens.data_ptr(), ws_ptr, ws_bytes, flag, stream))
     return out_lens

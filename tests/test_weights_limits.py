@@ -3,6 +3,8 @@ eviction, without a GPU."""
 
 import ctypes
 
+import pytest
+
 i32, i64, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
 
@@ -21,3 +23,21 @@ def test_prefill_weights_workspace_of_nearly_a_round_of_items(cuda_lib_path):
     assert f(1, 256, 256, 152, 152, 128, 4096, 16) == up(256 * 152 * 4 + 4)
     # rows of q behind the sequences' own are counted too
     assert f(1, 512, 256, 151, 151, 128, 4096, 16) > 118e6
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 10 ** 20])
+def test_numbers_beyond_a_c_int_are_refused(value):
+    """Not cut to their lower 32 bits: an eviction to a budget of 2^32 + 5 would trim to 5 tokens."""
+    import paged_kv_cache_85_gb300 as pkv
+
+    with pytest.raises(ValueError, match="budget"):
+        pkv.evict_kvcache(None, None, None, None, None, value, 0, None)
+    with pytest.raises(ValueError, match="recent"):
+        pkv.evict_kvcache(None, None, None, None, None, 10, value, None)
+    with pytest.raises(ValueError, match="window"):
+        pkv.paged_prefill_weights(None, None, None, None, None, None, 1, 0.1, None, None, window=value)
+    with pytest.raises(ValueError, match="max_seqlen_q"):
+        pkv.paged_prefill_weights(None, None, None, None, None, None, value, 0.1, None, None)
+    for call, scales in ((pkv.paged_attn_decode_weights, ()), (pkv.paged_attn_decode_weights_fp8, (1.0, 1.0))):
+        with pytest.raises(ValueError, match="max_ctas"):
+            call(None, None, None, None, None, 0.1, *scales, None, None, max_ctas=value)

@@ -355,7 +355,8 @@ pkv_status pkv_paged_attn_decode_noalloc(const void *q, const void *k_cache, con
  * for either cache type.  Beside the decode call's scratch it holds every
  * score until its row's sum is known: 4 * Hq bytes per token of the B * MBS *
  * bs the tables can name (134 MB for 512 sequences of 4096 tokens and 16
- * query heads), of which a call touches the part that its contexts fill.
+ * query heads), of which a call touches the part that its contexts fill (where
+ * scratch is short, pass tables no wider than the step needs).
  * A context of length 0 records nothing.  Two kernels on `stream`: decode, and
  * one that merges split contexts and turns the scores into weights.
  */
@@ -395,7 +396,9 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
  *              D = 128 in three splits, and more where q holds rows behind the
  *              sequences' own (where there are up to 759 items of long contexts,
  *              the last of which are split, at most some 400 MB); with few new
- *              tokens and sequences, 2.5 MB of partial sums
+ *              tokens and sequences, 2.5 MB of partial sums.  Long contexts are
+ *              those that the tables can name (MBS * bs): where scratch is short,
+ *              pass tables no wider than the step needs.
  * B * Hkv * MBS * bs / 128 < 2^31.  A sequence that the attention skips
  * records nothing.  The scores of the recorded queries are made a second time
  * (their weights need each row's final sum), so recording every query adds

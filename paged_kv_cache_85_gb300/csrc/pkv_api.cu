@@ -804,7 +804,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         return ps;
     const bool wide = record;  // the calls that record take the 128-key kernel
     const pkv::WideSplit split =
-        record ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1};
+        record ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1, 0};
     const int splits = split.splits;
     const void *kfn = pkv::prefill_kernel(D, G, wide, splits > 1);
     const size_t smem = pkv::prefill_smem_bytes(D, wide);
@@ -859,6 +859,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         p.ticket = reinterpret_cast<int32_t *>(p.lse + Tq * Hq);
         p.splits = splits;
         p.whole = split.whole;
+        p.least = split.least;
         uint8_t *ws = static_cast<uint8_t *>(workspace) +
                       pkv::align_up((size_t)Tq * Hq * sizeof(float) + sizeof(int32_t), 256);
         const bool may_split = pkv::pw_may_split(B, Tq, max_seqlen_q, G, Hkv);

@@ -30,6 +30,7 @@ struct PrefillParams {
     // 128-key kernel, where its items are split over the keys (splits > 1)
     int splits = 1;
     int whole = 0;                // the first (longest) items, which are not split
+    int least = 0;                // nor are items of fewer key tiles
     float *part_out = nullptr;    // [splits, Tq, Hq, D] outputs of the splits
     float *part_lse = nullptr;    // [splits, Hkv, Tq, G] their log-sum-exps, -inf: no key; of
                                   // a whole item's rows the first is +inf
@@ -66,16 +67,18 @@ const void *prompt_weights_kernel_fn(int D, int G, bool split);
 size_t prompt_weights_smem_bytes(int D);
 const void *prefill_kernel(int D, int G, bool wide, bool split);
 size_t prefill_smem_bytes(int D, bool wide);
-// Key tiles (of 128) per split of an item of nkt tiles; its splits are
-// ceil(nkt / chunk) <= splits.
+// Key tiles (of 128) per split of an item of nkt tiles, which is split where it has
+// `least`; its splits are ceil(nkt / chunk) <= splits, a single one if nkt <= chunk.
 constexpr int kMinSplitTiles = 4;
-__host__ __device__ inline int wide_chunk(int nkt, int splits)
+__host__ __device__ inline int wide_chunk(int nkt, int splits, int least)
 {
+    if (nkt < least)
+        return nkt;
     const int chunk = (nkt + splits - 1) / splits;
     return chunk < kMinSplitTiles ? kMinSplitTiles : chunk;
 }
-// How a call's items are split, from its sizes: items from `whole` on into up to
-// `splits` pieces.
+// How a call's items are split, from its sizes: items from `whole` on, where they
+// have `least` key tiles, into up to `splits` pieces.
 //  * Where there are fewer items than SMs, all of them, into enough pieces for two
 //    per SM, none shorter than kMinSplitTiles tiles of the longest context.
 //  * Where there are a few rounds of long items, those of the last, incomplete
@@ -86,39 +89,45 @@ __host__ __device__ inline int wide_chunk(int nkt, int splits)
 //    piece, at 3500 bytes a cycle) and the join cost; a key tile is 3200 cycles.
 //    Whole call: those 256 items 820 -> 792 us; 168 items (1300 new tokens on 28672)
 //    798 -> 545; 192 (three of 512 on 8192) 269 -> 215; 512 (4096 on 16384) 1002 -> 935.
+// The host knows the tables' width and the longest chunk, not the contexts, which may be
+// far shorter: `least` leaves items whole that the sum above does not split (four chunks
+// of 1024 tokens of 16 heads on nothing, tables of 40960: 97 us with every item of the
+// last round split, 68 so, 63 with tables as wide as the contexts).
 struct WideSplit {
-    int whole, splits;
+    int whole, splits, least;
 };
-// The lengths that this goes by are the tables' width and the longest chunk, which the
-// host knows.  With another number of SMs than this the pieces fill the last round less
-// well; the results are the same.
+// With another number of SMs than this the pieces fill the last round less well; the
+// results are the same.
 constexpr long long kWideSms = 152;
 constexpr int kJoinMaxSeqs = 152;  // sequences that the join kernel can look through
 inline WideSplit wide_split(long long items, long long max_ctx, int max_q, int B)
 {
     const long long tiles = (max_ctx + 127) / 128;
     if (items < 1 || B > kJoinMaxSeqs)
-        return {0, 1};
+        return {0, 1, 0};
     if (items < kWideSms) {
         long long s = (2 * kWideSms + items - 1) / items;
         if (s > tiles / kMinSplitTiles)
             s = tiles / kMinSplitTiles;
-        return {0, s < 1 ? 1 : (int)s};
+        return {0, s < 1 ? 1 : (int)s, 0};
     }
     const long long rounds = items / kWideSms, left = items % kWideSms;
     if (rounds > 4 || left == 0)  // (the pieces' buffers hold all rows, 400 MB with four)
-        return {0, 1};
+        return {0, 1, 0};
     // the last round has the shortest items, the start of the longest sequence's new
     // tokens at least (where they vary more, the longest-first order fills the SMs)
     const long long item = (max_ctx - max_q) / 128 * 3200;
-    WideSplit best = {0, 1};
-    long long least = item + 8000 - (rounds * item) / 20;  // a twentieth of the call at least
+    WideSplit best = {0, 1, 0};
+    long long cheapest = item + 8000 - (rounds * item) / 20;  // a twentieth of the call at least
     for (int s = 2; s <= 4; s++) {
         const long long pieces = (left * s + kWideSms - 1) / kWideSms;
         const long long cost = pieces * (item / s + 8000) + left * s * 75 + 20000;
-        if (cost < least) {
-            least = cost;
-            best = {(int)(rounds * kWideSms), s};
+        if (cost < cheapest) {
+            cheapest = cost;
+            // cost < item + 8000 - rounds item / 20, solved for the item's tiles
+            const long long gain = 20 * s - s * rounds - 20 * pieces;  // > 0, of 20 s
+            const long long ends = (pieces - 1) * 8000 + left * s * 75 + 20000;
+            best = {(int)(rounds * kWideSms), s, (int)(20 * s * ends / (gain * 3200)) + 1};
         }
     }
     return best;

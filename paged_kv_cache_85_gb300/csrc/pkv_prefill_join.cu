@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
         // key tiles of the row's item: a pair of query tiles of 128 / G tokens each
         const int tpc = kPrefillRows / G, tok0 = (row - cq[b]) / (2 * tpc) * (2 * tpc);
         const int nkt = (k_len - q_len + min(q_len, tok0 + 2 * tpc) - 1) / 128 + 1;
-        const int chunk = wide_chunk(nkt, p.splits), n = (nkt + chunk - 1) / chunk;
+        const int chunk = wide_chunk(nkt, p.splits, p.least), n = (nkt + chunk - 1) / chunk;
 
         float M = -INFINITY;
         for (int i = lane; i < n; i += 32)
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
     };
     for (long long at0 = (long long)blockIdx.x * kJoinWarps + warp; at0 < rows; at0 += 32 * warps) {
         const long long mine = at0 + lane * warps;
-        const bool split = mine < rows && !(p.whole && p.part_lse[lse_of(mine)] == INFINITY);
+        const bool split = mine < rows && p.part_lse[lse_of(mine)] != INFINITY;
         for (unsigned todo = __ballot_sync(FULL, split); todo; todo &= todo - 1)
             join(at0 + (__ffs(todo) - 1) * warps);
     }

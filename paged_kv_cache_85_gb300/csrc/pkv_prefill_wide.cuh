@@ -212,7 +212,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const long long at = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
                 if (at >= units)
                     break;
-                const int pos = SPLIT && at >= whole ? whole + (int)((at - whole) / splits) : (int)at;
+                // the split items' first pieces, then their second ones: items that turn
+                // out too short to be split fill the SMs like any others
+                int pos = (int)at, piece = -1;
+                if (SPLIT && at >= whole) {
+                    piece = ((int)at - whole) / (p.n_items - whole);
+                    pos -= piece * (p.n_items - whole);
+                }
                 const PrefillWork w = p.B <= 32 ? prefill_schedule<2 * TPC, 1>(p, lane, pos)
                                                 : prefill_schedule<2 * TPC, kSchedChunks>(p, lane, pos);
                 int cq0 = w.cq0, cq1 = w.cq1, ck0 = w.ck0, ck1 = w.ck1;
@@ -239,22 +245,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     : 0;
                     if constexpr (SPLIT)
                         item.split = -1;
-                    if (SPLIT && at >= whole) {
-                        const int chunk = wide_chunk(max(it.nkt[0], it.nkt[1]), splits);
-                        item.split = (int)((at - whole) - (long long)(pos - whole) * splits);
-                        item.j0 = item.split * chunk;
-                        for (int t = 0; t < 2; t++)
-                            it.nkt[t] = min(max(it.nkt[t] - item.j0, 0), chunk);
-                        if (max(it.nkt[0], it.nkt[1]) == 0)
+                    if (SPLIT && piece >= 0) {
+                        const int nkt = max(it.nkt[0], it.nkt[1]);
+                        const int chunk = wide_chunk(nkt, splits, p.least);
+                        item.j0 = piece * chunk;
+                        if (item.j0 >= nkt)
                             continue;  // the item has fewer splits
+                        if (nkt > chunk) {
+                            item.split = piece;
+                            for (int t = 0; t < 2; t++)
+                                it.nkt[t] = min(max(it.nkt[t] - item.j0, 0), chunk);
+                        }
                     }
                     it.b = w.b;
                     k++;
                     break;
                 }
                 // up to kSchedMaxSeqs sequences, ranks are longest first, so
-                // the first empty item ends this CTA's work
-                if (p.B <= kSchedMaxSeqs && w.b < 0) {
+                // the first empty item ends this CTA's work (but for further pieces)
+                if (!SPLIT && p.B <= kSchedMaxSeqs && w.b < 0) {
                     k = 0x3fffffff;
                     break;
                 }

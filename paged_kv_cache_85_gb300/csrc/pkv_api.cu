@@ -202,9 +202,13 @@ pkv_status device_state(DeviceState **out)
     return PKV_OK;
 }
 
+// The driver's call that encodes tensor maps, which wants a current context: a
+// thread that has made no runtime call of its own yet has none, and takes its
+// device's.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static PFN_cuCtxGetCurrent_v4000 current = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
         void *p = nullptr;
@@ -213,7 +217,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
                                              cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000, cudaEnableDefault, &q) ==
+                cudaSuccess && q == cudaDriverEntryPointSuccess)
+            current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
     });
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (current && current(&ctx) == CUDA_SUCCESS && !ctx && cudaGetDevice(&dev) == cudaSuccess)
+        cudaSetDevice(dev);  // (what is wrong with it, the encoding reports)
     return fn;
 }
 

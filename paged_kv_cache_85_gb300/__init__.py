@@ -214,10 +214,15 @@ _ws_cache: dict = {}
 
 
 def _workspace(device, stream_handle, nbytes):
+    """The plain decode calls' workspace: one per stream, grown as needed; a call that
+    is being captured has one of its own from the graph's pool (the stream's may be
+    replaced by a larger one, or used by other calls, while the graph lives)."""
     import torch
 
     if nbytes == 0:
         return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, stream_handle)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:

@@ -19,6 +19,10 @@ cached token received, and the eviction that goes by it:
     paged_prefill_weights(..., out, weights, window=0)
     evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget, recent, out_lens)
 
+Without a ``workspace`` these three keep one of 4 MiB per thread, device and
+stream for as long as the thread lives (``torch.cuda.empty_cache()`` does not
+reach it); larger ones, and those of captured calls, are allocated per call.
+
 Layouts: k, v ``[N, Hkv, D]``; caches ``[NB, bs, Hkv, D]``; q, out
 ``[B, Hq, D]`` (all bf16, contiguous, on one CUDA device); slot_mapping int64
 ``[N]`` (-1 = skip); block_tables int32 ``[B, MBS]``; context_lens int32 ``[B]``.

@@ -29,9 +29,9 @@
 //           comes from.
 // HBM-bound: 4 bytes per token and KV head read for the weights, and the rows
 // that move read and written once.  Measured with nothing trimmed before, bf16,
-// D = 128, 8 KV heads: 64 contexts up to 4096 tokens to 1024 in 87 us (select 11,
-// move 72: 392 MB of DRAM traffic, 74% of its throughput in runs of 256 bytes),
-// 8 of 32768 to 4096 in 69 (19 + 47).  Both in one kernel: 110 and 93.
+// D = 128, 8 KV heads: 64 contexts up to 4096 tokens to 1024 in 88 us (select 12,
+// move 70: 392 MB of DRAM traffic, 74% of its throughput in runs of 256 bytes),
+// 8 of 32768 to 4096 in 71 (23 + 44).  Both in one kernel: 110 and 93.
 #include <cooperative_groups.h>
 
 #include "pkv_evict.h"

@@ -31,8 +31,8 @@
 //    an incomplete last round, where there are few rounds of long ones
 //    (wide_split).
 //
-// Measured: 254 us for 8 sequences of 2048 new tokens (16 heads, 296 GFLOP: 1167
-// TFLOP/s, tensor pipe 52%), where the 64-key kernel takes 305.  Bound by the
+// Measured: 261 us for 8 sequences of 2048 new tokens (16 heads, 296 GFLOP: 1136
+// TFLOP/s, tensor pipe 52%), where the 64-key kernel takes 298.  Bound by the
 // chain above: 3200 cycles per pair of query tiles and 128 keys, of which a
 // softmax group works 2700; an item's ends are another 7400.
 //

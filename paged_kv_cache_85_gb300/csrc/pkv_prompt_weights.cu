@@ -41,8 +41,8 @@
 //         themselves they cost 500 cycles per tile)
 // Work per pair of 128 x 128 tiles and SM: 1024 cycles of 2^x (32 per cycle) and
 // as many of MMA; it takes some 2000, the softmax groups' loads, exponentials and
-// waits one after the other.  Measured: 141 us where every query of a 16k-token
-// step records (148 GFLOP: 1054 TFLOP/s; tensor pipe and 2^x 54% each), 28 us
+// waits one after the other.  Measured: 144 us where every query of a 16k-token
+// step records (148 GFLOP: 1028 TFLOP/s; tensor pipe and 2^x 54% each), 28 us
 // where the last 32 of 32 ragged prompts do (72 MB read, 2.5 TB/s: items of one
 // query tile, bound by their way through the warps).
 #include <cuda.h>

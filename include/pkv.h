@@ -455,6 +455,109 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
                              int recent, int32_t *out_lens, void *workspace, size_t workspace_bytes,
                              int32_t *err_flag, void *stream);
 
+/*
+ * FP8 caches with a scale for each block of tokens and KV head.  (No counterpart in
+ * the pages; the formulas are given in full here.)  Codes are E4M3 as in the FP8
+ * calls above, caches uint8 [NB, bs, Hkv, D]; beside them
+ *
+ *   k_scales, v_scales   device, fp32 [NB, Hkv], 16-byte aligned, under the same
+ *                        block ids: a code of block n, head h stands for
+ *                        code_value * scales[n, h].
+ *
+ * A head or block of large values then costs no other one its small ones, and no
+ * calibration is needed: the store sets the scales.  Attention takes any finite
+ * scales > 0 within [2^-40, 2^40], a NaN scale makes what it touches NaN.
+ */
+
+/*
+ * pkv_store_kvcache_scaled - quantize and scatter the step's new K/V rows, setting
+ * the scales of the blocks they go to.
+ *
+ * For a block n that slot_mapping names, a KV head h, and K or V alike, let a be the
+ * largest finite magnitude that the call stores there and want = 2^e with the least
+ * e in [-40, 40] for which a <= 448 * 2^e (e = -40 where a = 0).
+ *   - If the call stores the block's first token (offset 0), or its scale s is not
+ *     finite and > 0, the block begins: its scale becomes want, whatever it held.
+ *   - Else its scale becomes s' = max(s, want).  Where s' > s, every row of the
+ *     block and head is recoded, code' = e4m3(code_value * (s / s')), before the
+ *     call's own rows are stored (exact for powers of two, but for codes that become
+ *     subnormal).
+ * Stored codes are e4m3(x * (1 / s')): nearest even, finite values beyond 448 * s'
+ * and infinities saturate, NaN stays NaN.  All products in fp32.
+ *
+ *   k, v, slot_mapping, err_flag   as in pkv_store_kvcache
+ *   D in {64, 128}, bs a multiple of 16, Hkv <= 65535, NB*bs < 2^31
+ * The tokens of one block follow each other in slot_mapping with nothing between
+ * them (as the block manager's slots of a sequence do; in any order among
+ * themselves): where they do not, that block's rows and scales are unspecified.
+ * Valid slots are expected to be distinct.
+ */
+pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache, void *v_cache,
+                                    float *k_scales, float *v_scales, const int64_t *slot_mapping,
+                                    int64_t N, int Hkv, int D, int64_t NB, int bs, int32_t *err_flag,
+                                    void *stream);
+
+/*
+ * pkv_paged_attn_decode_scaled - pkv_paged_attn_decode_fp8 with the blocks' scales.
+ *
+ * Arguments, limits, workspace (pkv_decode_workspace_bytes), flags and arithmetic as
+ * there, each 16-token box with its block's scales; an infinite element of q makes
+ * its head's output NaN.
+ */
+pkv_status pkv_paged_attn_decode_scaled(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int MBS,
+                                        const int32_t *context_lens, int B, int Hq, int Hkv, int D,
+                                        int64_t NB, int bs, float scale, void *out, void *workspace,
+                                        size_t workspace_bytes, int max_ctas, int32_t *err_flag,
+                                        void *stream);
+
+/*
+ * pkv_paged_prefill_scaled - pkv_paged_prefill over FP8 caches with block scales.
+ *
+ * Arguments, limits and flags as in pkv_paged_prefill (PKV_FLAG_V_RANGE is not set),
+ * plus the scales and a workspace of pkv_prefill_scaled_workspace_bytes bytes for the
+ * same sizes, 16-byte aligned: partial outputs where there are few items of long
+ * contexts, as in pkv_paged_prefill_weights; often 0, and then NULL will do.
+ *
+ * Precision: scores on the tensor cores in E4M3 with fp32 accumulation, K as its
+ * codes and q in two parts, exact for elements of magnitude >= max|q| 2^-9 of their
+ * row and within max|q| 2^-17 for the rest; P . V in f16 with fp32 accumulation, V =
+ * code_value * scale rounded to f16 relative to the larger scales of its 128-token
+ * tile (absolute error <= 2^-25 of them; none where scales are powers of two within
+ * 2^13 of each other).  An infinite element of q makes its row NaN.
+ */
+size_t pkv_prefill_scaled_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
+                                          int D, int MBS, int bs);
+
+pkv_status pkv_paged_prefill_scaled(const void *q, const void *k_cache, const void *v_cache,
+                                    const float *k_scales, const float *v_scales,
+                                    const int32_t *block_tables, int MBS, const int32_t *cu_seqlens_q,
+                                    const int32_t *cu_seqlens_k, int B, int64_t Tq, int max_seqlen_q,
+                                    int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
+                                    void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                    void *stream);
+
+/*
+ * pkv_copy_blocks - block pairs[i][1] of every tensor becomes its block pairs[i][0].
+ *
+ * What a forked sequence needs before it writes into a shared, partly filled block
+ * (pkv_bm_fork), and what compaction needs (pkv_bm_compact): in one call for
+ * everything that lies under the block ids, of one layer or of many.
+ *
+ *   tensors      host array of n_tensors device pointers, each to NB blocks of
+ *   block_bytes  host array: so many contiguous bytes (caches of any type, scales,
+ *                recorded weights; block_bytes in [1, 2^31); distinct memory)
+ *   pairs        device, int32 [n_pairs, 2] source and destination, 8-byte aligned;
+ *                (-1, -1) is padding and skipped, equal ids are left alone; any other
+ *                id outside [0, NB) sets PKV_FLAG_BAD_BLOCK and its pair is skipped
+ * The destinations are expected to be distinct and no source of another pair; several
+ * destinations may share a source.  Reads the two host arrays before it returns.
+ */
+pkv_status pkv_copy_blocks(void *const *tensors, const int64_t *block_bytes, int n_tensors,
+                           const int32_t *pairs, int n_pairs, int64_t NB, int32_t *err_flag,
+                           void *stream);
+
 /* Message describing the last non-OK status returned on this host thread. */
 const char *pkv_last_error(void);
 

@@ -19,7 +19,18 @@ cached token received, and the eviction that goes by it:
     paged_prefill_weights(..., out, weights, window=0)
     evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget, recent, out_lens)
 
-Without a ``workspace`` these three keep one of 4 MiB per thread, device and
+For an FP8 cache whose scales lie per block and KV head, set by the store itself:
+
+    store_kvcache_scaled(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping)
+    paged_attn_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out)
+    paged_prefill_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens_q, cu_seqlens_k,
+                         max_seqlen_q, scale, out)
+
+and, for forked sequences and compaction, of any tensors under the block ids:
+
+    copy_blocks(tensors, pairs)
+
+Without a ``workspace`` the budget calls and the two scaled attention calls keep one of 4 MiB per thread, device and
 stream for as long as the thread lives (``torch.cuda.empty_cache()`` does not
 reach it); larger ones, and those of captured calls, are allocated per call.
 
@@ -47,6 +58,11 @@ __all__ = [
     "paged_attn_decode_weights_fp8",
     "paged_prefill_weights",
     "evict_kvcache",
+    "store_kvcache_scaled",
+    "paged_attn_decode_scaled",
+    "paged_prefill_scaled",
+    "copy_blocks",
+    "prefill_scaled_workspace_bytes",
     "decode_weights_workspace_bytes",
     "prefill_weights_workspace_bytes",
     "evict_workspace_bytes",
@@ -133,6 +149,18 @@ def load_library():
         lib.pkv_evict_kvcache.restype = i32
         lib.pkv_evict_kvcache.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64, i32, i32, i32,
                                           P, P, sz, P, P]
+        lib.pkv_store_kvcache_scaled.restype = i32
+        lib.pkv_store_kvcache_scaled.argtypes = [P, P, P, P, P, P, P, i64, i32, i32, i64, i32, P, P]
+        lib.pkv_paged_attn_decode_scaled.restype = i32
+        lib.pkv_paged_attn_decode_scaled.argtypes = [P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i64, i32,
+                                                     f32, P, P, sz, i32, P, P]
+        lib.pkv_prefill_scaled_workspace_bytes.restype = sz
+        lib.pkv_prefill_scaled_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32, i32]
+        lib.pkv_paged_prefill_scaled.restype = i32
+        lib.pkv_paged_prefill_scaled.argtypes = [P, P, P, P, P, P, i32, P, P, i32, i64, i32, i32, i32, i32,
+                                                 i64, i32, f32, P, P, sz, P, P]
+        lib.pkv_copy_blocks.restype = i32
+        lib.pkv_copy_blocks.argtypes = [ctypes.POINTER(P), ctypes.POINTER(i64), i32, P, i32, i64, P, P]
         lib.pkv_last_error.restype = ctypes.c_char_p
         lib.pkv_last_error.argtypes = []
         lib.pkv_version.restype = i32
@@ -635,3 +663,165 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
             context_lens.data_ptr(), B, Hkv, D, 1 if fp8 else 2, NB, bs, budget, recent,
             out_lens.data_ptr(), ws_ptr, ws_bytes, flag, stream))
     return out_lens
+
+
+# ---------------------------------------------------------------- FP8 caches with a scale per block and KV head
+
+
+def prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs) -> int:
+    """Workspace bytes paged_prefill_scaled needs for these sizes (often 0)."""
+    return int(load_library().pkv_prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs))
+
+
+def _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales):
+    """Check the caches and their scales; returns (device index, NB, bs, Hkv, D)."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _require_fp8_cache(t, name)
+    dev = k_cache.get_device()
+    if v_cache.get_device() != dev:
+        raise ValueError(f"v_cache is on {v_cache.device}, k_cache on {k_cache.device}")
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError(f"the caches' shapes differ: {tuple(shape)} and {tuple(v_cache.shape)}")
+    NB, bs, Hkv, D = shape
+    _tensors(torch, dev, (k_scales, "k_scales", torch.float32, 2), (v_scales, "v_scales", torch.float32, 2))
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.shape != (NB, Hkv):
+            raise ValueError(f"{name} must be [NB, Hkv] = {(NB, Hkv)} for these caches; got {tuple(t.shape)}")
+    return dev, NB, bs, Hkv, D
+
+
+def store_kvcache_scaled(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None):
+    """Quantize new bf16 K/V rows to E4M3 into caches with a scale per block and KV head.
+
+    ``k_scales`` and ``v_scales`` are fp32 ``[NB, Hkv]``, under the caches' block
+    ids.  A block whose first slot is among ``slot_mapping`` begins with the least
+    power of two that holds the new rows; an older one's scale grows where it does
+    not, and the rows that the block holds are recoded.  The tokens of one block
+    follow each other in ``slot_mapping``.  Nothing needs initialising.
+    """
+    import torch
+
+    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    bf16 = torch.bfloat16
+    _tensors(torch, dev, (k, "k", bf16, 3), (v, "v", bf16, 3), (slot_mapping, "slot_mapping", torch.int64, 1))
+    N = k.shape[0]
+    if v.shape != k.shape or tuple(k.shape[1:]) != (Hkv, D):
+        raise ValueError(f"k and v must be [N, {Hkv}, {D}] for these caches; got {tuple(k.shape)} and {tuple(v.shape)}")
+    if slot_mapping.shape[0] != N:
+        raise ValueError(f"slot_mapping has {slot_mapping.shape[0]} slots for {N} rows")
+    flag = _flag(torch, dev, err_flag)
+    lib = _lib or load_library()
+    with _on_device(dev):
+        _check(lib.pkv_store_kvcache_scaled(
+            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), slot_mapping.data_ptr(), N, Hkv, D, NB, bs, flag, _raw_stream(dev)))
+
+
+def paged_attn_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
+                             max_ctas=0, workspace=None, err_flag=None):
+    """Decode attention over FP8 caches with a scale per block and KV head; writes ``out`` and returns it."""
+    import torch
+
+    max_ctas = _c_int(max_ctas, "max_ctas")
+    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", torch.int32, 2),
+             (context_lens, "context_lens", torch.int32, 1))
+    B, Hq, D2 = q.shape
+    if D2 != D:
+        raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables/context_lens batch != q batch")
+    _result(torch, dev, out, q)
+    flag = _flag(torch, dev, err_flag)
+    MBS = max(block_tables.shape[1], 1)
+    lib = _lib or load_library()
+    with _on_device(dev):
+        stream = _raw_stream(dev)
+        ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
+            "pkv_decode_workspace_bytes", B, Hq, Hkv, D, MBS, bs, max_ctas), dev, stream)
+        _check(lib.pkv_paged_attn_decode_scaled(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), MBS, context_lens.data_ptr(), B, Hq, Hkv, D, NB, bs, float(scale),
+            out.data_ptr(), ws_ptr, ws_bytes, max_ctas, flag, stream))
+    return out
+
+
+def paged_prefill_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens_q, cu_seqlens_k,
+                         max_seqlen_q, scale, out, workspace=None, err_flag=None):
+    """``paged_prefill`` over FP8 caches with a scale per block and KV head; writes ``out`` and returns it."""
+    import torch
+
+    max_seqlen_q = _c_int(max_seqlen_q, "max_seqlen_q")
+    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    i32 = torch.int32
+    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", i32, 2),
+             (cu_seqlens_q, "cu_seqlens_q", i32, 1), (cu_seqlens_k, "cu_seqlens_k", i32, 1))
+    Tq, Hq, D2 = q.shape
+    if D2 != D:
+        raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
+    B = cu_seqlens_q.shape[0] - 1
+    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("cu_seqlens / block_tables batch sizes differ")
+    _result(torch, dev, out, q)
+    flag = _flag(torch, dev, err_flag)
+    MBS = max(block_tables.shape[1], 1)
+    lib = _lib or load_library()
+    with _on_device(dev):
+        stream = _raw_stream(dev)
+        need = _bytes("pkv_prefill_scaled_workspace_bytes", B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs)
+        ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and workspace is None else _scratch(
+            torch, workspace, need, dev, stream)
+        _check(lib.pkv_paged_prefill_scaled(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), MBS, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq, max_seqlen_q,
+            Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), ws_ptr, ws_bytes, flag, stream))
+    return out
+
+
+# ---------------------------------------------------------------- copies of blocks
+
+
+def copy_blocks(tensors, pairs, err_flag=None):
+    """For every (source, destination) of ``pairs``, block ``destination`` of every tensor becomes block ``source``.
+
+    ``tensors`` lie under one set of block ids: contiguous, ``[NB, ...]`` of any
+    types (caches, scales, recorded weights, of one layer or of many), on one
+    device.  ``pairs`` is int32 ``[n, 2]`` on it; rows of (-1, -1) are padding.
+    Destinations are distinct and no other pair's source (``BlockManager.fork``
+    and ``BlockManager.compact`` give such pairs).
+    """
+    import torch
+
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("copy_blocks: no tensors")
+    if not isinstance(tensors[0], torch.Tensor):
+        raise TypeError("tensors[0] must be a torch.Tensor")
+    dev = tensors[0].get_device()
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"tensors[{i}] must be a torch.Tensor")
+        if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"tensors[{i}] must be a contiguous CUDA tensor [NB, ...]")
+        if t.get_device() != dev or t.shape[0] != tensors[0].shape[0]:
+            raise ValueError(f"tensors[{i}] is {tuple(t.shape)} on {t.device}; the first has "
+                             f"{tensors[0].shape[0]} blocks on {tensors[0].device}")
+    _tensors(torch, dev, (pairs, "pairs", torch.int32, 2))
+    n, two = pairs.shape
+    if two != 2:
+        raise ValueError(f"pairs must be [n, 2]; got {tuple(pairs.shape)}")
+    flag = _flag(torch, dev, err_flag)
+    NB = tensors[0].shape[0]
+    tensors = [t for t in tensors if t.numel()]
+    if n == 0 or not tensors:
+        return
+    lib = _lib or load_library()
+    m = len(tensors)
+    with _on_device(dev):
+        _check(lib.pkv_copy_blocks(
+            (ctypes.c_void_p * m)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * m)(*[t.numel() // NB * t.element_size() for t in tensors]), m,
+            pairs.data_ptr(), n, NB, flag, _raw_stream(dev)))

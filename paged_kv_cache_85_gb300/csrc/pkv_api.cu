@@ -17,7 +17,9 @@
 #include "pkv_kernels.h"
 #include "pkv_prefill.h"
 #include "pkv_prefill_tc.cuh"
+#include "pkv_prefill_scaled.cuh"
 #include "pkv_prefill_wide.cuh"
+#include "pkv_scaled.h"
 
 namespace pkv {
 #define PKV_DECLARE_SHAPE(D, NW)                                                                  \
@@ -42,7 +44,11 @@ PKV_DECLARE_SHAPE(128, 8)
     cudaError_t launch_decodew8_d##D##_w##NW(int G, int bt, const CUtensorMap *tmk,               \
                                              const CUtensorMap *tmv, const DecodeParams &p,       \
                                              int grid, size_t smem, cudaStream_t stream);         \
-    const void *decodew8_kernel_d##D##_w##NW(int G, int bt);
+    const void *decodew8_kernel_d##D##_w##NW(int G, int bt);                                      \
+    cudaError_t launch_decodes8_d##D##_w##NW(int G, int bt, const CUtensorMap *tmk,               \
+                                             const CUtensorMap *tmv, const DecodeParams &p,       \
+                                             int grid, size_t smem, cudaStream_t stream);         \
+    const void *decodes8_kernel_d##D##_w##NW(int G, int bt);
 PKV_DECLARE_SHAPE8(64, 4)
 PKV_DECLARE_SHAPE8(64, 8)
 PKV_DECLARE_SHAPE8(128, 4)
@@ -64,6 +70,31 @@ cudaError_t launch_prefill_wide_d128(int G, const CUtensorMap *tmq, const CUtens
                                      size_t smem, cudaStream_t stream);
 const void *prefill_wide_kernel_d64(int G, bool split);
 const void *prefill_wide_kernel_d128(int G, bool split);
+
+cudaError_t launch_prefill_scaled_d64(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                      const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                      size_t smem, cudaStream_t stream);
+cudaError_t launch_prefill_scaled_d128(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                       const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                       size_t smem, cudaStream_t stream);
+const void *prefill_scaled_kernel_d64(int G, bool split);
+const void *prefill_scaled_kernel_d128(int G, bool split);
+
+// E4M3 caches with block scales
+cudaError_t launch_prefill_scaled(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                  const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                  size_t smem, cudaStream_t stream)
+{
+    return D == 128 ? launch_prefill_scaled_d128(G, tmq, tmk, tmv, p, grid, smem, stream)
+                    : launch_prefill_scaled_d64(G, tmq, tmk, tmv, p, grid, smem, stream);
+}
+
+const void *prefill_scaled_kernel(int D, int G, bool split)
+{
+    return D == 128 ? prefill_scaled_kernel_d128(G, split) : prefill_scaled_kernel_d64(G, split);
+}
+
+size_t prefill_scaled_smem_bytes(int D) { return scaled_smem_layout(D).total; }
 
 // wide: the kernel with 128-key tiles
 cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
@@ -90,11 +121,18 @@ size_t prefill_smem_bytes(int D, bool wide)
 }
 
 // bt: tokens per box (16, or 32 for FP8 caches with block sizes divisible by 32)
-// weights: the kernels that also record every score for the attention weights
-const void *decode_kernel(int D, int NW, int G, bool f8, int bt, bool weights)
+// kind: the kernels that also record every score for the attention weights, or those
+// of FP8 caches with a scale per block
+enum DecodeKind { kDecodePlain = 0, kDecodeWeights = 1, kDecodeScaled = 2 };
+const void *decode_kernel(int D, int NW, int G, bool f8, int bt, DecodeKind kind)
 {
     const bool pair = NW == kPairWorkers;
-    if (weights) {
+    if (kind == kDecodeScaled) {
+        if (D == 128)
+            return pair ? decodes8_kernel_d128_w4(G, bt) : decodes8_kernel_d128_w8(G, bt);
+        return pair ? decodes8_kernel_d64_w4(G, bt) : decodes8_kernel_d64_w8(G, bt);
+    }
+    if (kind == kDecodeWeights) {
         if (f8) {
             if (D == 128)
                 return pair ? decodew8_kernel_d128_w4(G, bt) : decodew8_kernel_d128_w8(G, bt);
@@ -119,6 +157,13 @@ cudaError_t launch_decode(int D, int NW, int G, bool f8, int bt, const CUtensorM
                           cudaStream_t stream)
 {
     const bool pair = NW == kPairWorkers;
+    if (p.k_scales) {
+        if (D == 128)
+            return pair ? launch_decodes8_d128_w4(G, bt, tmk, tmv, p, grid, smem, stream)
+                        : launch_decodes8_d128_w8(G, bt, tmk, tmv, p, grid, smem, stream);
+        return pair ? launch_decodes8_d64_w4(G, bt, tmk, tmv, p, grid, smem, stream)
+                    : launch_decodes8_d64_w8(G, bt, tmk, tmv, p, grid, smem, stream);
+    }
     if (p.ws_score) {
         if (f8) {
             if (D == 128)
@@ -173,8 +218,8 @@ struct DeviceState {
     bool ready = false;
     int dev = 0;
     int sms = 0;
-    bool smem_set[2][2][2][2][2][9] = {};  // [weights][fp8][32-token boxes][D == 128][NW == 8][G]
-    bool pf_smem_set[3][2][9] = {};  // prefill: [64-key tiles, 128, 128 split][D == 128][G]
+    bool smem_set[3][2][2][2][2][9] = {};  // [kind][fp8][32-token boxes][D == 128][NW == 8][G]
+    bool pf_smem_set[5][2][9] = {};  // prefill: [64-key tiles, 128, 128 split, scaled, scaled split][D == 128][G]
     bool pw_smem_set[2][2][9] = {};  // its weights kernel: [may split][D == 128][G]
     bool evict_smem_set = false;
 };
@@ -356,7 +401,9 @@ pkv_status make_cache_map8(CUtensorMap *map, const void *cache, long long tokens
 // 32-token boxes of an FP8 cache, or, for the prefill kernel, whole 64-token
 // tiles or 16-token boxes of a bf16 cache with both halves per copy; for its
 // weights kernel 64-token runs of one half.
-enum MapKind { kMapBox = 0, kMapBox8 = 1, kMapTile = 2, kMapBoxHalves = 3, kMapBox8Wide = 4, kMapRun = 5 };
+// Of an FP8 cache for its prefill kernel also 64- or 128-token runs.
+enum MapKind { kMapBox = 0, kMapBox8 = 1, kMapTile = 2, kMapBoxHalves = 3, kMapBox8Wide = 4, kMapRun = 5,
+               kMapRun8 = 6, kMapRun8Wide = 7 };
 struct MapEntry {
     const void *ptr = nullptr;
     long long tokens = 0;
@@ -378,6 +425,8 @@ pkv_status cached_cache_map(CUtensorMap *map, const void *cache, long long token
         }
     const pkv_status ps = kind == kMapBox8   ? make_cache_map8(map, cache, tokens, Hkv, D, pkv::kBox)
                           : kind == kMapBox8Wide ? make_cache_map8(map, cache, tokens, Hkv, D, 2 * pkv::kBox)
+                          : kind == kMapRun8     ? make_cache_map8(map, cache, tokens, Hkv, D, 64)
+                          : kind == kMapRun8Wide ? make_cache_map8(map, cache, tokens, Hkv, D, 128)
                           : kind == kMapTile ? make_cache_tile_map(map, cache, tokens, Hkv, D, pkv::kPrefillKeys)
                           : kind == kMapRun ? make_cache_map(map, cache, tokens, Hkv, D, pkv::kPrefillKeys)
                           : kind == kMapBoxHalves ? make_cache_tile_map(map, cache, tokens, Hkv, D, pkv::kBox)
@@ -408,7 +457,8 @@ struct DecodePlan {
 };
 
 pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas,
-                       bool with_device, DecodePlan *plan, bool f8 = false, bool weights = false)
+                       bool with_device, DecodePlan *plan, bool f8 = false,
+                       pkv::DecodeKind kind = pkv::kDecodePlain)
 {
     if (B < 1 || Hq < 1 || Hkv < 1 || MBS < 1 || bs < 1 || max_ctas < 0)
         return fail(PKV_ERR_INVALID_ARG,
@@ -491,7 +541,7 @@ pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_c
     plan->hdr_bytes = pkv::align_up((size_t)(pkv::kWsHeaderInts + B + 1) * 4, 256);
     plan->ws_bytes = plan->hdr_bytes +
                      (size_t)workers_cap * 2 * G * (size_t)(D + 4) * sizeof(float);
-    if (weights) {
+    if (kind == pkv::kDecodeWeights) {
         plan->lse_at = pkv::align_up(plan->ws_bytes, 256);
         plan->box_at = pkv::align_up(plan->lse_at + (size_t)B * Hq * sizeof(float), 256);
         plan->score_at = pkv::align_up(plan->box_at + (size_t)box_max * sizeof(int4), 256);
@@ -504,10 +554,10 @@ pkv_status plan_decode(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_c
     pkv_status ps = device_state(&st);
     if (ps != PKV_OK)
         return ps;
-    const void *kfn = pkv::decode_kernel(D, NW, G, f8, bt, weights);
+    const void *kfn = pkv::decode_kernel(D, NW, G, f8, bt, kind);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->smem_set[weights][f8][bt != pkv::kBox][D == 128][NW == pkv::kWideWorkers][G];
+        bool &set = st->smem_set[kind][f8][bt != pkv::kBox][D == 128][NW == pkv::kWideWorkers][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)kMaxDynSmem);
@@ -543,7 +593,8 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
                               int B, int Hq, int Hkv, int D, int64_t NB, int bs, float scale,
                               void *out, void *workspace, size_t workspace_bytes, int max_ctas,
                               int32_t *err_flag, void *stream, bool f8, float k_scale,
-                              float v_scale, bool record = false, float *weights = nullptr)
+                              float v_scale, bool record = false, float *weights = nullptr,
+                              const float *k_scales = nullptr, const float *v_scales = nullptr)
 {
     if (B < 0 || NB < 1)
         return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode: bad sizes B=%d NB=%lld", B, (long long)NB);
@@ -561,7 +612,10 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     if (f8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f ||
                v_scale <= 0.f))
         return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode_fp8: scales must be finite and > 0");
-    pkv_status ps = plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, true, &plan, f8, record);
+    const pkv::DecodeKind dk = record     ? pkv::kDecodeWeights
+                               : k_scales ? pkv::kDecodeScaled
+                                          : pkv::kDecodePlain;
+    pkv_status ps = plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, true, &plan, f8, dk);
     if (ps != PKV_OK)
         return ps;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out)
@@ -601,6 +655,8 @@ static pkv_status decode_impl(const void *q, const void *k_cache, const void *v_
     p.stages = plan.stages;
     p.scale_log2 = scale * 1.4426950408889634f * (f8 ? k_scale : 1.f);
     p.v_scale = f8 ? v_scale : 1.f;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
     if (record) {
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         p.weights = weights;
@@ -712,7 +768,8 @@ pkv_status pkv_paged_attn_decode_fp8(const void *q, const void *k_cache, const v
 size_t pkv_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int D, int MBS, int bs, int max_ctas)
 {
     DecodePlan plan;
-    if (B == 0 || plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, false, &plan, false, true) != PKV_OK)
+    if (B == 0 || plan_decode(B, Hq, Hkv, D, MBS, bs, max_ctas, false, &plan, false, pkv::kDecodeWeights) !=
+                      PKV_OK)
         return 0;
     return plan.ws_bytes;
 }
@@ -761,8 +818,10 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
                                int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
                                int32_t *err_flag, void *stream, bool record = false,
                                float *weights = nullptr, int window = 0, void *workspace = nullptr,
-                               size_t workspace_bytes = 0)
+                               size_t workspace_bytes = 0, const float *k_scales = nullptr,
+                               const float *v_scales = nullptr)
 {
+    const bool scaled = k_scales != nullptr;
     if (B < 0 || Tq < 0 || max_seqlen_q < 0 || NB < 1 || MBS < 1 || bs < 1 || Hq < 1 || Hkv < 1)
         return fail(PKV_ERR_INVALID_ARG, "paged_prefill: bad sizes B=%d Tq=%lld max_seqlen_q=%d "
                     "NB=%lld MBS=%d bs=%d Hq=%d Hkv=%d", B, (long long)Tq, max_seqlen_q,
@@ -804,6 +863,13 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
             return fail(PKV_ERR_WORKSPACE, "paged_prefill_weights: workspace needs %zu bytes "
                         "(16-byte aligned), got %zu", need, workspace ? workspace_bytes : (size_t)0);
     }
+    if (scaled) {
+        const size_t need =
+            pkv_prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs);
+        if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+            return fail(PKV_ERR_WORKSPACE, "paged_prefill_scaled: workspace needs %zu bytes "
+                        "(16-byte aligned), got %zu", need, workspace ? workspace_bytes : (size_t)0);
+    }
     // work items: pairs of adjacent 128-row query tiles of one sequence and KV head
     const long long pairs =
         ((long long)max_seqlen_q * G + 2 * pkv::kPrefillRows - 1) / (2 * pkv::kPrefillRows);
@@ -816,13 +882,14 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         return ps;
     const bool wide = record;  // the calls that record take the 128-key kernel
     const pkv::WideSplit split =
-        record ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1, 0};
+        record || scaled ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1, 0};
     const int splits = split.splits;
-    const void *kfn = pkv::prefill_kernel(D, G, wide, splits > 1);
-    const size_t smem = pkv::prefill_smem_bytes(D, wide);
+    const void *kfn = scaled ? pkv::prefill_scaled_kernel(D, G, splits > 1)
+                             : pkv::prefill_kernel(D, G, wide, splits > 1);
+    const size_t smem = scaled ? pkv::prefill_scaled_smem_bytes(D) : pkv::prefill_smem_bytes(D, wide);
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        bool &set = st->pf_smem_set[wide ? 1 + (splits > 1) : 0][D == 128][G];
+        bool &set = st->pf_smem_set[scaled ? 3 + (splits > 1) : wide ? 1 + (splits > 1) : 0][D == 128][G];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)smem);
@@ -837,11 +904,17 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     // one per 64 tokens and 64-column half, V one per 64 tokens); else K one copy
     // per 16-token box and 64-column half, V one per box
     const bool tile_copies = bs % pkv::kPrefillKeys == 0;
-    const int kmap = !tile_copies ? kMapBox : wide ? kMapRun : kMapTile;
+    // (codes: the longest run that divides a block, K and V alike)
+    const int copy_rows = bs % 128 == 0 ? 128 : bs % 64 == 0 ? 64 : bs % 32 == 0 ? 32 : 16;
+    const int map8 = copy_rows == 128  ? kMapRun8Wide
+                     : copy_rows == 64 ? kMapRun8
+                     : copy_rows == 32 ? kMapBox8Wide
+                                       : kMapBox8;
+    const int kmap = scaled ? map8 : !tile_copies ? kMapBox : wide ? kMapRun : kMapTile;
+    const int vmap = scaled ? map8 : tile_copies ? kMapTile : kMapBoxHalves;
     if ((ps = cached_cache_map(&tmk, k_cache, tokens, Hkv, D, kmap)) != PKV_OK)
         return ps;
-    if ((ps = cached_cache_map(&tmv, v_cache, tokens, Hkv, D, tile_copies ? kMapTile : kMapBoxHalves)) !=
-        PKV_OK)
+    if ((ps = cached_cache_map(&tmv, v_cache, tokens, Hkv, D, vmap)) != PKV_OK)
         return ps;
     if ((ps = make_q_map(&tmq, q, Tq, Hq, D, G)) != PKV_OK)
         return ps;
@@ -865,6 +938,20 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
     p.neg_scale = scale < 0.f;
     p.tile_copies = tile_copies ? 1 : 0;
+    if (scaled) {
+        p.k_scales = k_scales;
+        p.v_scales = v_scales;
+        p.copy_rows = copy_rows;
+        p.splits = splits;
+        p.whole = split.whole;
+        p.least = split.least;
+        if (splits > 1) {
+            p.part_lse = static_cast<float *>(workspace);
+            p.part_out = reinterpret_cast<float *>(
+                static_cast<uint8_t *>(workspace) +
+                pkv::align_up((size_t)splits * Tq * Hq * sizeof(float), 256));
+        }
+    }
     if (record) {
         p.lse = static_cast<float *>(workspace);
         p.weights = weights;
@@ -906,14 +993,16 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         grid = (long long)p.n_items * p.splits;
     if (grid < 1)
         return PKV_OK;
-    cudaError_t e = pkv::launch_prefill(D, G, wide, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
-                                        smem, static_cast<cudaStream_t>(stream));
+    cudaError_t e = scaled ? pkv::launch_prefill_scaled(D, G, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
+                                                        smem, static_cast<cudaStream_t>(stream))
+                           : pkv::launch_prefill(D, G, wide, &tmq, &tmk, &tmv, p, dim3((unsigned)grid),
+                                                 smem, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "paged_prefill launch: %s", cudaGetErrorString(e));
     if (p.splits > 1) {
         e = pkv::launch_prefill_join(D, p, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess)
-            return fail(PKV_ERR_CUDA, "paged_prefill_weights join launch: %s", cudaGetErrorString(e));
+            return fail(PKV_ERR_CUDA, "paged_prefill join launch: %s", cudaGetErrorString(e));
     }
     if (record) {
         e = pkv::launch_prompt_weights(D, G, &tmq, &tmk, p, window, st->sms,
@@ -1108,6 +1197,142 @@ pkv_status pkv_store_kvcache_fp8(const void *k, const void *v, void *k_cache, vo
                                           static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "store_kvcache_fp8 launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache, void *v_cache,
+                                    float *k_scales, float *v_scales, const int64_t *slot_mapping,
+                                    int64_t N, int Hkv, int D, int64_t NB, int bs, int32_t *err_flag,
+                                    void *stream)
+{
+    if (N < 0 || Hkv < 1 || NB < 1 || bs < 1)
+        return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: bad sizes N=%lld Hkv=%d NB=%lld bs=%d",
+                    (long long)N, Hkv, (long long)NB, bs);
+    if (N > 0x7fffffffLL || Hkv > 65535)
+        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N must be < 2^31 and Hkv <= 65535");
+    if (D != 64 && D != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: head_dim %d not in {64,128}", D);
+    if (bs % pkv::kBox != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: block_size %d not a multiple of 16", bs);
+    if (NB >= 0x7fffffffLL || NB * bs >= 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: NB*bs must be < 2^31");
+    if (N == 0)
+        return PKV_OK;
+    if (!k || !v || !k_cache || !v_cache || !k_scales || !v_scales || !slot_mapping)
+        return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: null pointer");
+    if (k_cache == v_cache || k_scales == v_scales)
+        return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: K and V share a cache or its scales");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(k_scales) || !aligned16(v_scales) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: pointers must be 16-byte aligned");
+    pkv::StoreScaledParams p;
+    p.x[0] = static_cast<const uint4 *>(k);
+    p.x[1] = static_cast<const uint4 *>(v);
+    p.cache[0] = static_cast<uint8_t *>(k_cache);
+    p.cache[1] = static_cast<uint8_t *>(v_cache);
+    p.scales[0] = k_scales;
+    p.scales[1] = v_scales;
+    p.slots = slot_mapping;
+    p.err_flag = err_flag;
+    p.N = N;
+    p.n_slots = (long long)NB * bs;
+    p.Hkv = Hkv;
+    p.bs = bs;
+    cudaError_t e = pkv::launch_store_scaled(D, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(PKV_ERR_CUDA, "store_kvcache_scaled launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+pkv_status pkv_paged_attn_decode_scaled(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int MBS,
+                                        const int32_t *context_lens, int B, int Hq, int Hkv, int D,
+                                        int64_t NB, int bs, float scale, void *out, void *workspace,
+                                        size_t workspace_bytes, int max_ctas, int32_t *err_flag,
+                                        void *stream)
+{
+    if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales))
+        return fail(PKV_ERR_INVALID_ARG, "paged_attn_decode_scaled: scales null or misaligned");
+    return decode_impl(q, k_cache, v_cache, block_tables, MBS, context_lens, B, Hq, Hkv, D, NB, bs,
+                       scale, out, workspace, workspace_bytes, max_ctas, err_flag, stream, true, 1.f,
+                       1.f, false, nullptr, k_scales, v_scales);
+}
+
+size_t pkv_prefill_scaled_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
+                                          int D, int MBS, int bs)
+{
+    if (B < 1 || Tq < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || MBS < 1 || bs < 1)
+        return 0;
+    const size_t rows = (size_t)Tq * Hq;
+    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs).splits;
+    return splits > 1 ? pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float)
+                      : 0;
+}
+
+pkv_status pkv_paged_prefill_scaled(const void *q, const void *k_cache, const void *v_cache,
+                                    const float *k_scales, const float *v_scales,
+                                    const int32_t *block_tables, int MBS, const int32_t *cu_seqlens_q,
+                                    const int32_t *cu_seqlens_k, int B, int64_t Tq, int max_seqlen_q,
+                                    int Hq, int Hkv, int D, int64_t NB, int bs, float scale, void *out,
+                                    void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                    void *stream)
+{
+    if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales))
+        return fail(PKV_ERR_INVALID_ARG, "paged_prefill_scaled: scales null or misaligned");
+    return prefill_impl(q, k_cache, v_cache, block_tables, MBS, cu_seqlens_q, cu_seqlens_k, B, Tq,
+                        max_seqlen_q, Hq, Hkv, D, NB, bs, scale, out, err_flag, stream, false, nullptr, 0,
+                        workspace, workspace_bytes, k_scales, v_scales);
+}
+
+pkv_status pkv_copy_blocks(void *const *tensors, const int64_t *block_bytes, int n_tensors,
+                           const int32_t *pairs, int n_pairs, int64_t NB, int32_t *err_flag,
+                           void *stream)
+{
+    if (n_tensors < 0 || n_pairs < 0 || NB < 1 || NB > 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID_ARG, "copy_blocks: bad sizes n_tensors=%d n_pairs=%d NB=%lld",
+                    n_tensors, n_pairs, (long long)NB);
+    if (n_tensors == 0 || n_pairs == 0)
+        return PKV_OK;
+    if (!tensors || !block_bytes || !pairs)
+        return fail(PKV_ERR_INVALID_ARG, "copy_blocks: null pointer");
+    if (reinterpret_cast<uintptr_t>(pairs) & 7u)
+        return fail(PKV_ERR_INVALID_ARG, "copy_blocks: pairs must be 8-byte aligned");
+    for (int i = 0; i < n_tensors; i++) {
+        if (!tensors[i])
+            return fail(PKV_ERR_INVALID_ARG, "copy_blocks: tensor %d is null", i);
+        if (block_bytes[i] < 1 || block_bytes[i] > 0x7fffffffLL)
+            return fail(PKV_ERR_INVALID_ARG, "copy_blocks: tensor %d has %lld bytes per block, not in "
+                        "[1, 2^31)", i, (long long)block_bytes[i]);
+        for (int j = 0; j < i; j++)
+            if (tensors[j] == tensors[i])
+                return fail(PKV_ERR_INVALID_ARG, "copy_blocks: tensors %d and %d are the same memory", j, i);
+    }
+    DeviceState *st = nullptr;
+    pkv_status ps = device_state(&st);
+    if (ps != PKV_OK)
+        return ps;
+    for (int i0 = 0; i0 < n_tensors; i0 += pkv::kCopyTensors) {
+        pkv::CopyParams p;
+        p.n_tensors = n_tensors - i0 < pkv::kCopyTensors ? n_tensors - i0 : pkv::kCopyTensors;
+        p.pairs = reinterpret_cast<const int2 *>(pairs);
+        p.err_flag = err_flag;
+        p.n = n_pairs;
+        p.NB = (int)NB;
+        p.chunks = 0;
+        for (int i = 0; i < p.n_tensors; i++) {
+            pkv::CopyTensor &t = p.t[i];
+            t.base = static_cast<uint8_t *>(tensors[i0 + i]);
+            t.block_bytes = block_bytes[i0 + i];
+            t.chunks = (int)((t.block_bytes + pkv::kCopyChunk - 1) / pkv::kCopyChunk);
+            const uintptr_t both = reinterpret_cast<uintptr_t>(t.base) | (uintptr_t)t.block_bytes;
+            t.vec = (both & 15u) == 0 ? 16 : (both & 3u) == 0 ? 4 : 1;
+            p.chunks += t.chunks;
+        }
+        cudaError_t e = pkv::launch_copy_blocks(p, st->sms, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return fail(PKV_ERR_CUDA, "copy_blocks launch: %s", cudaGetErrorString(e));
+    }
     return PKV_OK;
 }
 

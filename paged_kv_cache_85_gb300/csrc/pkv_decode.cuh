@@ -63,7 +63,12 @@ constexpr int kLookahead = 4;  // boxes per worker whose block ids are loaded ah
 // Per-worker box descriptor of a stage, written by the producer.
 struct __align__(16) BoxMeta {
     int b, h, tok0, nvalid;
-    int flags, blk, box, pad;  // box: position in the streams (with WT)
+    int flags, blk;
+    union {
+        int box;   // position in the streams (with WT)
+        float ks;  // scale of the block's K (with SC)
+    };
+    float vs;      // scale of the block's V (with SC)
 };
 constexpr int kBoxValid = 1;     // the worker has a box in this stage
 constexpr int kBoxLoaded = 2;    // its K/V were copied (the block id was valid)
@@ -187,7 +192,24 @@ struct ProducerWalk {
     int cb, ch, cj;       // the first box: sequence, KV head, box of the stream
     int lb, lh, lj, lpos; // look-ahead
     int qb[kLookahead];   // qb[(pos - start) % kLookahead]: block id of box pos
+    // with SC alike: the box's KV head, and the scales of its block, loaded
+    // kLookahead - kScaleAhead boxes after the block id
+    int qh[kLookahead];
+    float qk[kLookahead], qv[kLookahead];
 };
+constexpr int kScaleAhead = 2;  // boxes ahead of use that a block's scales are loaded
+
+// The scales of the block in slot i of the queue.  An earlier kernel of the stream
+// (the store) may have written them while this one was starting.
+__device__ __forceinline__ void load_scales(const DecodeParams &p, ProducerWalk &w, int i)
+{
+    w.qk[i] = w.qv[i] = 1.f;
+    if (w.qb[i] >= 0 && w.qb[i] < p.NB) {
+        const size_t at = (size_t)w.qb[i] * p.Hkv + w.qh[i];
+        w.qk[i] = ld_gpu(p.k_scales + at);
+        w.qv[i] = ld_gpu(p.v_scales + at);
+    }
+}
 
 // Lane w < NW runs worker w of this CTA: worker gw owns slice gw % Wr of region
 // gw / Wr (regions past R idle).
@@ -208,7 +230,7 @@ __device__ __forceinline__ void walk_start(const DecodeParams &p, const int *pb,
         locate_box(w.start, pb, p.B, w.cb, w.ch, w.cj);
 }
 
-template <int BT>
+template <int BT, bool SC>
 __device__ __forceinline__ void walk_ahead(const DecodeParams &p, const int *pb, ProducerWalk &w)
 {
     w.lb = w.cb;
@@ -220,16 +242,23 @@ __device__ __forceinline__ void walk_ahead(const DecodeParams &p, const int *pb,
         w.qb[i] = -1;
         if (w.lpos < w.end) {
             w.qb[i] = box_block<BT>(p, w.lb, w.lj);
+            if constexpr (SC)
+                w.qh[i] = w.lh;
             next_box(pb, p.B, w.lb, w.lh, w.lj);
         }
         ++w.lpos;
+    }
+    if constexpr (SC) {
+#pragma unroll
+        for (int i = 0; i < kScaleAhead; i++)
+            load_scales(p, w, i);
     }
 }
 
 // Producer warp.  Per stage every lane writes its worker's box descriptor and
 // issues its own TMA copies; lane 0 arms the stage's mbarrier with the summed
 // byte count.
-template <int D, int G, int NW, bool F8, int BT, bool WT>
+template <int D, int G, int NW, bool F8, int BT, bool WT, bool SC>
 __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CUtensorMap *tmv,
                                                 const DecodeParams &p, uint8_t *smem,
                                                 const DecodeSmem &L, int lane, ProducerWalk &w)
@@ -303,6 +332,10 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
             m.nvalid = min(BT, len[b] - tok0);
             m.flags = flags;
             m.blk = blk;
+            if constexpr (SC) {
+                m.ks = w.qk[u];
+                m.vs = w.qv[u];
+            }
             if constexpr (WT) {
                 m.box = pos;
                 // for the weights kernel
@@ -319,9 +352,14 @@ __device__ __forceinline__ void decode_producer(const CUtensorMap *tmk, const CU
             qb[u] = -1;
             if (lpos < end) {
                 qb[u] = box_block<BT>(p, lb, lj);
+                if constexpr (SC)
+                    w.qh[u] = lh;
                 next_box(pb, p.B, lb, lh, lj);
             }
             ++lpos;
+            // the scales of the box kScaleAhead on, whose block id came in rounds ago
+            if constexpr (SC)
+                load_scales(p, w, (u + kScaleAhead) % kLookahead);
         } else if (worker) {
             meta[stage * NW + lane].flags = 0;
         }
@@ -604,7 +642,14 @@ template <int D> __device__ __forceinline__ uint32_t box8_chunk(int t, int c)
 //     max exceeds it by more than 2^8, which bounds P by 256 (exact range of
 //     f16) and skips the rescale on most boxes.
 // k_scale is folded into the score scale and v_scale into the output.
-template <int D, int G, int NW, int BT, bool WT>
+// With SC every block has scales of its own.  A box lies in one block: its K scale
+// multiplies the box's scores, and its V scale the weights before they are rounded
+// to f16, relative to the unit vref in which O is held.  vref follows where the
+// ratio leaves [2^-7, 2^7] (with the running max's 2^8 that keeps P in f16's range,
+// and its rounding, subnormals included, below 2^-17 of the largest weight): O is
+// then rescaled.  Scales that are powers of two make every one of these products
+// exact but the last.
+template <int D, int G, int NW, int BT, bool WT, bool SC>
 __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8_t *smem,
                                                     const DecodeSmem &L, int warp, int lane)
 {
@@ -645,6 +690,7 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
     float f0 = 0.f, f0l = 0.f, f1 = 0.f, f1l = 0.f;
     float o[MT][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float vref = 1.f, vinv = 1.f;  // with SC: O's unit and its reciprocal
     bool whole = false;
 #pragma unroll
     for (int j = 0; j < MT; j++)
@@ -687,7 +733,7 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
             // sq = 2^(E - 7) for amax in [2^E, 2^(E+1)): |q / sq| < 256 <= 448
             int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
             ebits = min(max(ebits, 8), 254);
-            const float sq = __uint_as_float((uint32_t)(ebits - 7) << 23);
+            float sq = __uint_as_float((uint32_t)(ebits - 7) << 23);
             const float inv = __uint_as_float((uint32_t)(261 - ebits) << 23);
 #pragma unroll
             for (int w = 0; w < KW; w++) {
@@ -706,6 +752,8 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 qh[w] = c01 | (c23 << 16);
                 ql[w] = f32x2_to_e4m3x2(rs[0], rs[1]) | (f32x2_to_e4m3x2(rs[2], rs[3]) << 16);
             }
+            if constexpr (SC)  // an infinite element makes the head's scores NaN
+                sq = amax == INFINITY ? NAN : sq;
             const float sq0 = __shfl_sync(FULL, sq, 4 * h0);
             const float sq1 = __shfl_sync(FULL, sq, (4 * h1) & 31);
             f0 = p.scale_log2 * sq0;
@@ -718,6 +766,8 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
             for (int j = 0; j < MT; j++)
                 o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
             whole = (bm.flags & kStreamFirst) != 0;
+            if constexpr (SC)
+                vref = vinv = 1.f;
         }
         const int nvw = (bm.flags & kBoxLoaded) ? bm.nvalid : 0;
         // the stage goes back to the producer once the warp's last read of it
@@ -792,6 +842,11 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 sv[u][1] = fmaf(sl[1], f1l, sh[1] * f1);
                 sv[u][2] = fmaf(sl[2], f0l, sh[2] * f0);
                 sv[u][3] = fmaf(sl[3], f1l, sh[3] * f1);
+                if constexpr (SC) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        sv[u][i] *= bm.ks;
+                }
                 // with one sub-box, its V words are loaded before the softmax,
                 // whose reductions cover their latency; with two, each after it
                 // (registers)
@@ -830,6 +885,21 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 b0 = fmaxf(b0, __shfl_xor_sync(FULL, b0, x));
                 b1 = fmaxf(b1, __shfl_xor_sync(FULL, b1, x));
             }
+            float r = 1.f;
+            if constexpr (SC) {
+                r = bm.vs * vinv;
+                if (!(r >= 0x1p-7f && r <= 0x1p7f) && bm.vs > 0.f) {
+                    const float a = vref / bm.vs;
+                    vref = bm.vs;
+                    vinv = 1.f / vref;
+                    r = 1.f;
+#pragma unroll
+                    for (int j = 0; j < MT; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            o[j][i] *= a;
+                }
+            }
             if (__any_sync(FULL, b0 > m0 + kLazy || b1 > m1 + kLazy)) {
                 const float n0 = fmaxf(m0, b0), n1 = fmaxf(m1, b1);
                 const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
@@ -854,8 +924,8 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 const float p2 = fast_exp2(sv[u][2] - m0), p3 = fast_exp2(sv[u][3] - m1);
                 l0 += p0 + p2;
                 l1 += p1 + p3;
-                const uint32_t pb0 = movmatrix_trans(pack_f16x2(p0, p1));
-                const uint32_t pb1 = movmatrix_trans(pack_f16x2(p2, p3));
+                const uint32_t pb0 = movmatrix_trans(SC ? pack_f16x2(p0 * r, p1 * r) : pack_f16x2(p0, p1));
+                const uint32_t pb1 = movmatrix_trans(SC ? pack_f16x2(p2 * r, p3 * r) : pack_f16x2(p2, p3));
                 if (NSUB > 1) {
                     load_v(u, nv);
                     if (u == NSUB - 1 || nvw <= 16 * (u + 1))
@@ -900,7 +970,7 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                         if (g == 0)
                             p.ws_lse[hq0 + head] = row_lse(mr, lt);
                     }
-                    const float f = lt > 0.f ? p.v_scale / lt : 0.f;
+                    const float f = lt > 0.f ? (SC ? vref : p.v_scale) / lt : 0.f;
                     uint16_t *dst = p.out + (hq0 + head) * D + g * (D / 8);
 #pragma unroll
                     for (int c = 0; c < D / 64; c++) {
@@ -915,7 +985,7 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                 } else {
                     float *pg = p.ws_part +
                                 (((size_t)gw * 2 + ((bm.flags & kSlot1) ? 1 : 0)) * G + head) * (D + 4);
-                    const float vs = p.v_scale;
+                    const float vs = SC ? vref : p.v_scale;
 #pragma unroll
                     for (int c = 0; c < D / 32; c++) {
                         const int j = 2 * c;
@@ -924,7 +994,9 @@ __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8
                                         o[j + 1][2 + hh] * vs);
                     }
                     if (g == 0) {
-                        pg[D] = mr;
+                        // (a maximum of -inf tells the merge that no token was read; with
+                        // SC a piece of nothing but NaN scores is not to be taken for one)
+                        pg[D] = SC && isnan(lt) && mr == -INFINITY ? 0.f : mr;
                         pg[D + 1] = lt;
                     }
                 }
@@ -1010,12 +1082,14 @@ __device__ __forceinline__ bool lengths_changed(const DecodeParams &p, const int
 
 // BT: tokens per box (16; 32 for FP8 caches whose block size is a multiple
 // of 32, which halves the per-box work of the producer and the consumers).
-template <int D, int G, int NW, bool F8, int BT, bool WT>
+// SC: FP8 caches with a scale per block and KV head.
+template <int D, int G, int NW, bool F8, int BT, bool WT, bool SC>
 __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 2) : 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const DecodeParams p)
 {
     static_assert(BT == kBox || (F8 && BT == 2 * kBox), "32-token boxes on the FP8 path only");
+    static_assert(!SC || (F8 && !WT), "block scales: FP8 caches, without recorded weights");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const DecodeSmem L = decode_smem_layout(D, G, NW, p.stages, p.B, F8 ? 1 : 2, BT);
@@ -1059,7 +1133,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
         // still read (the workspace) is behind this
         grid_dependency_wait();
         if (warp == NW)
-            walk_ahead<BT>(p, pb, walk);
+            walk_ahead<BT, SC>(p, pb, walk);
     };
     // The same in two forms, for what the compiler makes of them: straight, the block
     // ids of the bf16 kernel wait for the vote (tiny 6.4 -> 6.8 us); as a loop, the FP8
@@ -1077,7 +1151,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
     }
 
     if (warp == NW) {
-        decode_producer<D, G, NW, F8, BT, WT>(&tmk, &tmv, p, smem, L, lane, walk);
+        decode_producer<D, G, NW, F8, BT, WT, SC>(&tmk, &tmv, p, smem, L, lane, walk);
     } else {
         if (blockIdx.x == 0) {
             // the box layout for the merge kernel
@@ -1093,13 +1167,13 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == kPairWorkers ? (F8 ? 3 : 
             }
         }
         if constexpr (F8)
-            decode_consumer_fp8<D, G, NW, BT, WT>(p, smem, L, warp, lane);
+            decode_consumer_fp8<D, G, NW, BT, WT, SC>(p, smem, L, warp, lane);
         else
             decode_consumer<D, G, NW, WT>(p, smem, L, warp, lane);
     }
 }
 
-template <int D, int NW, bool F8, int BT = kBox, bool WT = false>
+template <int D, int NW, bool F8, int BT = kBox, bool WT = false, bool SC = false>
 inline cudaError_t launch_decode_shape(int G, const CUtensorMap *tmk, const CUtensorMap *tmv,
                                        const DecodeParams &p, int grid, size_t smem,
                                        cudaStream_t stream)
@@ -1115,22 +1189,22 @@ inline cudaError_t launch_decode_shape(int G, const CUtensorMap *tmk, const CUte
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (G) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 1, NW, F8, BT, WT>, *tmk, *tmv, p);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 2, NW, F8, BT, WT>, *tmk, *tmv, p);
-    case 4: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 4, NW, F8, BT, WT>, *tmk, *tmv, p);
-    case 8: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 8, NW, F8, BT, WT>, *tmk, *tmv, p);
+    case 1: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 1, NW, F8, BT, WT, SC>, *tmk, *tmv, p);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 2, NW, F8, BT, WT, SC>, *tmk, *tmv, p);
+    case 4: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 4, NW, F8, BT, WT, SC>, *tmk, *tmv, p);
+    case 8: return cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, 8, NW, F8, BT, WT, SC>, *tmk, *tmv, p);
     default: return cudaErrorInvalidValue;
     }
 }
 
-template <int D, int NW, bool F8, int BT = kBox, bool WT = false>
+template <int D, int NW, bool F8, int BT = kBox, bool WT = false, bool SC = false>
 inline const void *decode_kernel_shape(int G)
 {
     switch (G) {
-    case 1: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 1, NW, F8, BT, WT>);
-    case 2: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 2, NW, F8, BT, WT>);
-    case 4: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 4, NW, F8, BT, WT>);
-    case 8: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 8, NW, F8, BT, WT>);
+    case 1: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 1, NW, F8, BT, WT, SC>);
+    case 2: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 2, NW, F8, BT, WT, SC>);
+    case 4: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 4, NW, F8, BT, WT, SC>);
+    case 8: return reinterpret_cast<const void *>(&paged_decode_kernel<D, 8, NW, F8, BT, WT, SC>);
     default: return nullptr;
     }
 }

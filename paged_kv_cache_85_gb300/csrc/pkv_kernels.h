@@ -49,6 +49,8 @@ struct DecodeParams {
     float *ws_score = nullptr;    // per box: [G][box tokens] scores (log2 units; FP8: [box tokens][G])
     float *weights = nullptr;     // [NB, Hkv, bs]: cleared for the step's new tokens by the decode
                                   // kernel, added to by the merge
+    // FP8 caches with a scale per block and KV head; null elsewhere.
+    const float *k_scales = nullptr, *v_scales = nullptr;  // [NB, Hkv]
 };
 
 // Host launchers (defined next to their kernels).

@@ -39,11 +39,19 @@ struct PrefillParams {
     // here) and partial sums [kPwFewUnits][kPwMaxSplits][256]
     int32_t *pw_count = nullptr;
     float *pw_part = nullptr;
+    // E4M3 caches with a scale per block and KV head; null elsewhere
+    const float *k_scales = nullptr, *v_scales = nullptr;  // [NB, Hkv]
+    int copy_rows = 0;            // tokens per copy: 128, 64, 32 or 16, which divide bs
 };
 
 cudaError_t launch_prefill(int D, int G, bool wide, const CUtensorMap *tmq, const CUtensorMap *tmk,
                            const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
                            cudaStream_t stream);
+cudaError_t launch_prefill_scaled(int D, int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                  const CUtensorMap *tmv, const PrefillParams &p, dim3 grid, size_t smem,
+                                  cudaStream_t stream);
+const void *prefill_scaled_kernel(int D, int G, bool split);
+size_t prefill_scaled_smem_bytes(int D);
 constexpr int kPwFewUnits = 152;  // fewer units (256 tokens, one KV head) than this are split
 constexpr int kPwMaxSplits = 16;
 constexpr int kPwMinSplit = 4;  // query tiles of 128 rows per split at least

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
 #pragma unroll
         for (int c = 0; c < DPL; c += 2)
             *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-        if (lane == 0)
+        if (lane == 0 && p.lse)
             p.lse[lse_at] = W == 0.f ? INFINITY : (M == -INFINITY ? 0.f : M) + log2f(W);
     };
     for (long long at0 = (long long)blockIdx.x * kJoinWarps + warp; at0 < rows; at0 += 32 * warps) {

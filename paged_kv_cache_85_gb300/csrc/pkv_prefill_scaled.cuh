@@ -1,0 +1,996 @@
+// Causal prefill attention over E4M3 caches with a scale per block and KV head.
+//
+// What it computes, its work items, their order and splits, and its schedule are those
+// of pkv_prefill_wide.cuh (128-key tiles, one score buffer per query tile, P over S in
+// two halves, the MMA warps' lock).  What the codes change:
+//
+//  * Scores run on the E4M3 path with K as the raw codes, so a K tile is half the bytes
+//    and nobody converts it.  Q becomes two E4M3 parts, q = sq (high + low), once per
+//    item and row: two multiplications at twice the rate of bf16's one, in the same
+//    shared memory.  sq and K's scale join the softmax scale of a row; where the boxes of
+//    a tile have different scales, every box's scores are multiplied by theirs first.
+//  * V's codes become f16, times their block's scale over a unit in which O is held, in
+//    buffers of their own (they are twice the codes' bytes).  With scales that are powers
+//    of two that product is exact.  The unit moves where a tile's largest scale leaves
+//    [2^-8, 2^7] of it; O is then rescaled with the running maximum.
+//  * The producer brings each box's scales beside its tile's copies: blocks two tiles
+//    ahead, scales one.
+//
+// Precision: Q's parts below; P and V in f16, fp32 sums.  A V value far below the tile's
+// largest scale is held to 2^-25 of that scale.
+//
+// Warps (352 threads): 0..3 softmax of query tile A, 4..7 of tile B (thread = row = TMEM
+// lane); 8 producer; 9, 10 the MMAs of tiles A and B.  TMEM as in pkv_prefill_wide.cuh.
+// Shared memory (D = 128): Q 64 KB, two stages each of K and V codes, 16 KB each, three
+// buffers of V as f16, 32 KB each.
+#pragma once
+
+#include "pkv_prefill_wide.cuh"
+
+namespace pkv {
+
+constexpr int kSKeys = kWKeys;  // keys per tile
+constexpr int kSKStages = 2;    // K ring: codes
+constexpr int kSRStages = 2;    // V ring: codes
+constexpr int kSVStages = 3;    // V as f16: one more than a tile's P.V of both query tiles needs
+                                // (with two, a query tile that is ahead waits for the other)
+// Tiles whose boxes' scales are kept: twice the stages, so that they may be read until
+// the warp arrives for the tile after the next, which is when the producer goes on.
+constexpr int kSScales = 4;
+static_assert(kSScales >= 2 * kSKStages && kSScales >= 2 * kSRStages, "a tile's scales outlive its stage");
+// q_full[2], q_conv[2], q_empty[2], k_full, k_empty [kSKStages] each, r_full, r_empty
+// [kSRStages] each, v_conv, v_empty [kSVStages] each, per query tile s_full,
+// pv_ready[2 halves], pv_done, o_free, then item_ready[2], item_free[2], mma_done
+constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
+
+// The scales of a tile's eight boxes.  K: equal says that all are scale[0] (boxes that
+// are not read count as any).  V: 0 for a box that is not read.
+struct __align__(16) BoxScales {
+    float scale[kSKeys / kBox];
+    int equal, pad[3];
+};
+
+struct ScaledSmem {
+    size_t q, k, r, v, scales, bars, items, slot, total;
+};
+
+__host__ __device__ inline ScaledSmem scaled_smem_layout(int D)
+{
+    ScaledSmem L;
+    size_t o = 0;
+    L.q = o;  // [tile][D/64 halves][128 rows][128 B]
+    o += (size_t)2 * (D / 64) * kTcRows * 128;
+    L.k = o;  // stages of [128 keys][D codes]
+    o += (size_t)kSKStages * kSKeys * D;
+    L.r = o;  // alike, V
+    o += (size_t)kSRStages * kSKeys * D;
+    L.v = o;  // stages of [D/64 halves][128 keys][128 B]
+    o += (size_t)kSVStages * (D / 64) * kSKeys * 128;
+    L.scales = o;  // of the last kSScales K tiles, then of V tiles
+    o += 2 * kSScales * sizeof(BoxScales);
+    L.bars = o;
+    o += 8 * kSBars;
+    L.items = align_up(o, 16);  // two published work items
+    o = L.items + 2 * sizeof(WideItem);
+    L.slot = o;  // TMEM base, and the MMA warps' lock
+    o += 16;
+    L.total = align_up(o, 16) + 1024;
+    if (L.total < kTcMinSmem)
+        L.total = kTcMinSmem;
+    return L;
+}
+
+// Eight E4M3 codes times f (a pair of f16) as eight f16.
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b, uint32_t f)
+{
+    uint4 r;
+    e4m3x4_to_f16x2x2(a, r.x, r.y);
+    e4m3x4_to_f16x2x2(b, r.z, r.w);
+    r.x = f16x2_mul(r.x, f);
+    r.y = f16x2_mul(r.y, f);
+    r.z = f16x2_mul(r.z, f);
+    r.w = f16x2_mul(r.w, f);
+    return r;
+}
+
+// SPLIT: p.splits > 1.  Of its own, for the others' items are 4% slower with it
+// where they are short.
+template <int D, int G, bool SPLIT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    paged_prefill_scaled_kernel(const __grid_constant__ CUtensorMap tmq,
+                              const __grid_constant__ CUtensorMap tmk,
+                              const __grid_constant__ CUtensorMap tmv, const PrefillParams p)
+{
+    constexpr int TPC = kTcRows / G;               // query tokens per tile
+    constexpr int HALVES = D / 64;
+    constexpr uint32_t kQHalf = kTcRows * 128;     // 16 KB
+    constexpr uint32_t kQTile = HALVES * kQHalf;
+    constexpr uint32_t kTile = kSKeys * D;         // one K (or V) tile of codes
+    constexpr uint32_t kVHalf = kSKeys * 128;      // 64 columns of a V tile as f16
+    constexpr uint32_t kVTile = HALVES * kVHalf;
+    constexpr int kBoxes = kSKeys / kBox;          // 16-token boxes per tile
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr float kLazy = 8.f;
+    const int splits = SPLIT ? p.splits : 1, whole = SPLIT ? p.whole : 0;
+    const long long units = SPLIT ? whole + (long long)(p.n_items - whole) * splits : p.n_items;
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const ScaledSmem L = scaled_smem_layout(D);
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L.bars);  // [2] Q tile t landed
+    uint64_t *q_conv = q_full + 2;                // [2] ... and became E4M3 parts (4 warps)
+    uint64_t *q_empty = q_conv + 2;               // [2] tile t's last S of the item completed
+    uint64_t *k_full = q_empty + 2;
+    uint64_t *k_empty = k_full + kSKStages;       // both tiles' S of the K tile completed (4 warps each)
+    uint64_t *r_full = k_empty + kSKStages;       // V codes landed
+    uint64_t *r_empty = r_full + kSRStages;       // ... and were read (8 warps)
+    uint64_t *v_conv = r_empty + kSRStages;       // the V tile as f16 (8 warps)
+    uint64_t *v_empty = v_conv + kSVStages;       // both tiles' P.V of the V tile completed
+    uint64_t *s_full = v_empty + kSVStages;       // [2] S_t written
+    uint64_t *pv_ready = s_full + 2;              // [half of the keys][2] P_t written (4 warps)
+    uint64_t *pv_done = pv_ready + 4;             // [2] P.V_t completed
+    uint64_t *o_free = pv_done + 2;               // [2] O_t read out by its epilogue (4 warps)
+    uint64_t *item_ready = o_free + 2;            // [2] item parameters published
+    uint64_t *item_free = item_ready + 2;         // [2] ... no longer needed
+    uint64_t *mma_done = item_free + 2;           // every MMA of the CTA completed
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
+    const Turn turn{slot + 1};
+    WideItem *items = reinterpret_cast<WideItem *>(smem + L.items);
+    uint8_t *sQ = smem + L.q, *sK = smem + L.k, *sR = smem + L.r, *sV = smem + L.v;
+    BoxScales *k_scales = reinterpret_cast<BoxScales *>(smem + L.scales), *v_scales = k_scales + kSScales;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    if (warp == kTcProducerWarp && lane == 0) {
+        for (int t = 0; t < 2; t++) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&q_conv[t], 4);
+            mbar_init(&q_empty[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&pv_ready[t], 4);
+            mbar_init(&pv_ready[2 + t], 4);
+            mbar_init(&pv_done[t], 1);
+            mbar_init(&o_free[t], 4);
+            mbar_init(&item_ready[t], 1);
+            mbar_init(&item_free[t], 10);  // two MMA warps, eight softmax warps
+        }
+        for (int s = 0; s < kSKStages; s++) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 8);
+        }
+        for (int s = 0; s < kSRStages; s++) {
+            mbar_init(&r_full[s], 1);
+            mbar_init(&r_empty[s], 8);
+        }
+        for (int s = 0; s < kSVStages; s++) {
+            mbar_init(&v_conv[s], 8);
+            mbar_init(&v_empty[s], 2);  // both MMA warps
+        }
+        mbar_init(mma_done, 2);
+        *turn.word = 0;
+        fence_mbarrier_init();
+    } else if (warp == kTcMmaWarp) {
+        tc::alloc(smem_u32(slot), kTcCols);
+        tc::relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *slot;
+    const int nC = (int)gridDim.x;
+    const int c = (int)blockIdx.x;
+
+    if (warp == kTcProducerWarp) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tensormap(&tmq);
+            prefetch_tensormap(&tmk);
+            prefetch_tensormap(&tmv);
+        }
+        grid_dependency_wait();  // K/V may have just been written by store_kvcache
+        int gk = 0, gv = 0;       // K and V tiles issued so far (all items)
+        int q_loads[2] = {0, 0};  // Q tiles A and B loaded so far
+        bool ok = true;
+        int n = 0;                // items published
+        int k = 0;                // walk rounds
+        for (;;) {
+            // ---- the next item with work (round k: forward, then backward), or the end
+            WideItem item{{-1, 0, 0, 0, 0, 0, {0, 0}}, 0, 0, 0, 0};
+            PrefillItem &it = item.f;
+            for (; ok; k++) {
+                const long long at = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
+                if (at >= units)
+                    break;
+                // the split items' first pieces, then their second ones: items that turn
+                // out too short to be split fill the SMs like any others
+                int pos = (int)at, piece = -1;
+                if (SPLIT && at >= whole) {
+                    piece = ((int)at - whole) / (p.n_items - whole);
+                    pos -= piece * (p.n_items - whole);
+                }
+                const PrefillWork w = p.B <= 32 ? prefill_schedule<2 * TPC, 1>(p, lane, pos)
+                                                : prefill_schedule<2 * TPC, kSchedChunks>(p, lane, pos);
+                int cq0 = w.cq0, cq1 = w.cq1, ck0 = w.ck0, ck1 = w.ck1;
+                if (w.b >= 0 && cq0 == kNotLoaded) {
+                    cq0 = __ldg(p.cu_q + w.b);
+                    cq1 = __ldg(p.cu_q + w.b + 1);
+                    ck0 = __ldg(p.cu_k + w.b);
+                    ck1 = __ldg(p.cu_k + w.b + 1);
+                }
+                const bool sane = w.b >= 0 && prefill_seq_sane(p, cq0, cq1, ck0, ck1);
+                if (w.b >= 0 && !sane && lane == 0)
+                    flag_error(p.err_flag, 0x4 /* PKV_FLAG_BAD_CONTEXT_LEN */);
+                const int tok0 = w.tile * 2 * TPC;
+                if (sane && tok0 < cq1 - cq0) {
+                    it.kvh = w.kvh;
+                    it.tok0 = tok0;
+                    it.cq0 = cq0;
+                    it.q_len = cq1 - cq0;
+                    it.k_len = ck1 - ck0;
+                    const int base = it.k_len - it.q_len;
+                    it.nkt[0] = (base + min(it.q_len, tok0 + TPC) - 1) / kSKeys + 1;
+                    it.nkt[1] = tok0 + TPC < it.q_len
+                                    ? (base + min(it.q_len, tok0 + 2 * TPC) - 1) / kSKeys + 1
+                                    : 0;
+                    if constexpr (SPLIT)
+                        item.split = -1;
+                    if (SPLIT && piece >= 0) {
+                        const int nkt = max(it.nkt[0], it.nkt[1]);
+                        const int chunk = wide_chunk(nkt, splits, p.least);
+                        item.j0 = piece * chunk;
+                        if (item.j0 >= nkt)
+                            continue;  // the item has fewer splits
+                        if (nkt > chunk) {
+                            item.split = piece;
+                            for (int t = 0; t < 2; t++)
+                                it.nkt[t] = min(max(it.nkt[t] - item.j0, 0), chunk);
+                        }
+                    }
+                    it.b = w.b;
+                    k++;
+                    break;
+                }
+                // up to kSchedMaxSeqs sequences, ranks are longest first, so
+                // the first empty item ends this CTA's work (but for further pieces)
+                if (!SPLIT && p.B <= kSchedMaxSeqs && w.b < 0) {
+                    k = 0x3fffffff;
+                    break;
+                }
+            }
+            // ---- publish it in slot n & 1, once the item two back is done with it
+            const int sl = n & 1;
+            if (n >= 2 && !(ok = ok && __all_sync(FULL, mbar_wait(&item_free[sl], ((n >> 1) & 1) ^ 1))))
+                break;  // the other warps time out on item_ready and stop
+            if (!ok)
+                it.b = -1;
+            if (lane == 0) {
+                items[sl] = item;
+                mbar_arrive(&item_ready[sl]);
+            }
+            __syncwarp();
+            if (it.b < 0)
+                break;
+            // ---- Q tiles, each once its tile's last S of the previous item completed
+            for (int t = 0; t < 2 && ok; t++) {
+                if (it.nkt[t] == 0)
+                    continue;
+                if (n >= 1 && !(ok = __all_sync(FULL, mbar_wait(&q_empty[t], (n - 1) & 1))))
+                    break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[t], HALVES * kQHalf);
+#pragma unroll
+                    for (int h = 0; h < HALVES; h++)
+                        tma_load_4d(sQ + t * kQTile + h * kQHalf, &tmq, 0, h, it.kvh * G,
+                                    it.cq0 + it.tok0 + t * TPC, &q_full[t]);
+                }
+                ++q_loads[t];
+            }
+            if (!ok)
+                break;
+            n++;
+            // ---- K and V tiles through the two rings: whichever can go.  Lanes 0-7
+            // resolve one 16-token box each: its block two tiles ahead of the copy, the
+            // block's scale one tile ahead.
+            const int nkt = max(it.nkt[0], it.nkt[1]);
+            const int j0 = SPLIT ? item.j0 : 0;
+            const int32_t *table = p.block_tables + (size_t)it.b * p.MBS;
+            auto entry = [&](int j) -> int {
+                const int key0 = (j0 + j) * kSKeys + lane * kBox;
+                return (lane < kBoxes && j < nkt && key0 < it.k_len) ? __ldg(table + key0 / p.bs) : -1;
+            };
+            // (written by the store, maybe while this kernel was starting)
+            auto scale_of = [&](const float *scales, int blk) {
+                return blk >= 0 && blk < p.NB ? ld_gpu(scales + (size_t)blk * p.Hkv + it.kvh) : 0.f;
+            };
+            int blk_k = entry(0), next_k = entry(1), blk_v = blk_k, next_v = next_k;
+            float sc_k = scale_of(p.k_scales, blk_k), sc_v = scale_of(p.v_scales, blk_v);
+            const int per = p.copy_rows;  // tokens per copy: so many lie in one block
+            auto issue = [&](int j, int g, bool is_k) {
+                uint64_t *fb = is_k ? k_full : r_full;
+                const int s = g % (is_k ? kSKStages : kSRStages);
+                const int blk = is_k ? blk_k : blk_v;
+                float sc = is_k ? sc_k : sc_v;
+                if (is_k) {
+                    blk_k = next_k;
+                    sc_k = scale_of(p.k_scales, blk_k);
+                    next_k = entry(j + 2);
+                } else {
+                    blk_v = next_v;
+                    sc_v = scale_of(p.v_scales, blk_v);
+                    next_v = entry(j + 2);
+                }
+                const int key0 = (j0 + j) * kSKeys + lane * kBox;
+                int row = -1;
+                if (lane < kBoxes && key0 < it.k_len) {
+                    if (blk >= 0 && blk < p.NB)
+                        row = blk * p.bs + key0 % p.bs;
+                    else
+                        flag_error(p.err_flag, 0x2 /* PKV_FLAG_BAD_BLOCK */);
+                }
+                // the boxes' scales: of K one stands in for those that are not read
+                const uint32_t read = __ballot_sync(FULL, row >= 0);
+                BoxScales &bx = (is_k ? k_scales : v_scales)[g % kSScales];
+                if (is_k) {
+                    const float first = __shfl_sync(FULL, sc, read ? __ffs(read) - 1 : 0);
+                    if (row < 0)
+                        sc = read ? first : 1.f;
+                    const bool equal = __all_sync(FULL, lane >= kBoxes || sc == (read ? first : 1.f));
+                    if (lane == 0)
+                        bx.equal = equal;
+                }
+                if (lane < kBoxes)
+                    bx.scale[lane] = sc;
+                // rows past k_len of a run come along: their scores are masked and
+                // their V rows zeroed
+                const bool copies = row >= 0 && (lane * kBox) % per == 0;
+                const uint32_t mask = __ballot_sync(FULL, copies);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&fb[s], (uint32_t)__popc(mask) * per * D);
+                __syncwarp();
+                if (copies)
+                    tma_load_3d((is_k ? sK : sR) + (size_t)s * kTile + lane * (kBox * D), is_k ? &tmk : &tmv,
+                                0, it.kvh, row, &fb[s]);
+            };
+            int jk = 0, jv = 0;
+            uint64_t t_last = sm_clock();
+            while (jk < nkt || jv < nkt) {
+                bool prog = false;
+                if (jk < nkt) {
+                    const bool free_k = tc::test_wait(smem_u32(&k_empty[gk % kSKStages]),
+                                                      ((gk / kSKStages) & 1) ^ 1);
+                    if (__shfl_sync(FULL, free_k, 0)) {
+                        issue(jk++, gk++, true);
+                        prog = true;
+                    }
+                }
+                if (jv < jk) {
+                    const bool free_v = tc::test_wait(smem_u32(&r_empty[gv % kSRStages]),
+                                                      ((gv / kSRStages) & 1) ^ 1);
+                    if (__shfl_sync(FULL, free_v, 0)) {
+                        issue(jv++, gv++, false);
+                        prog = true;
+                    }
+                }
+                if (prog) {
+                    t_last = sm_clock();
+                } else {
+                    __nanosleep(32);
+                    if (__shfl_sync(FULL, sm_clock() - t_last > kPollLimitCycles, 0)) {
+                        ok = false;
+                        break;
+                    }
+                }
+            }
+            if (!ok)
+                break;  // the other warps time out on their barriers and stop
+        }
+        if (lane == 0) {
+            if (!ok)
+                flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
+            // copies still in flight land before the CTA may exit
+            for (int t = 0; t < 2; t++)
+                if (q_loads[t] >= 1)
+                    mbar_wait(&q_full[t], (q_loads[t] - 1) & 1);
+            for (int g = max(0, gk - kSKStages); g < gk; g++)
+                mbar_wait(&k_full[g % kSKStages], (g / kSKStages) & 1);
+            for (int g = max(0, gv - kSRStages); g < gv; g++)
+                mbar_wait(&r_full[g % kSRStages], (g / kSRStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kTcMmaWarp || warp == kTcMmaWarp + 1) {
+        // ----------------------------------------------------------------- MMA
+        // One warp per query tile t.  Per key tile j: P.V_t(j), then, once it has
+        // read P_t(j), S_t(j + 1) into the same buffer.  The two warps take turns (a
+        // lock in shared memory) with such a pair: a tile's MMAs then run back to
+        // back while the other tile's softmax works.  Without it both tiles' MMAs
+        // share the pipe, both softmax groups get their scores at the same time, and
+        // the pipe idles while both work (4707 cycles per pair of tiles and 128 keys).
+        // A K, V or Q stage is released by one arrival per query tile: V by this warp,
+        // which waits for its P.V, K and Q by the softmax group as it finds S_t(j), or
+        // by this warp, for a stage its tile does not read, once that stage's tile has
+        // landed (so that the arrival counts towards that tile's phase).  Plain
+        // arrivals: each further commit costs the issuing thread about 100 cycles.
+        const int t = warp - kTcMmaWarp;
+        bool ok = true;
+        const uint32_t qt = smem_u32(sQ) + (uint32_t)t * kQTile;
+        const uint32_t idS = tc::idesc_e4m3(kTcRows, kSKeys);
+        const uint32_t idO = tc::idesc_f16(kTcRows, D, true);
+        const uint32_t dS = tmem + 256u + 128u * (uint32_t)t, dO = tmem + 128u * (uint32_t)t;
+        // K rows of D codes, swizzled at their width
+        const auto k_desc = [](uint32_t at) {
+            return D == 128 ? tc::smem_desc(at, 16, 1024) : tc::smem_desc_64b(at, 16, 512);
+        };
+        if (tc::elect_one()) {
+            int g0 = 0;    // K/V tiles of the previous items
+            int gq = 0;    // S/P tiles of this query tile so far
+            int used = 0;  // items in which this query tile had work
+            for (int n = 0; ok; n++) {
+                if (!(ok = mbar_wait(&item_ready[n & 1], (n >> 1) & 1)))
+                    break;
+                const PrefillItem it = items[n & 1].f;
+                if (it.b < 0)
+                    break;
+                const int nk = it.nkt[t];
+                const int nkt = max(it.nkt[0], it.nkt[1]);
+                if (nk > 0 && !(ok = mbar_wait(&q_conv[t], used & 1)))
+                    break;
+                tc::fence_after();
+                if (nk == 0)
+                    mbar_arrive(&q_empty[t]);  // this tile reads no Q this item
+                // S_t(j), its K tile landed and S_t's buffer free
+                auto scores = [&](int j) {
+                    const int s = (g0 + j) % kSKStages;
+                    tc::fence_after();
+                    const uint32_t ka = smem_u32(sK + (size_t)s * kTile);
+                    // Q = high + low part, both in one accumulator: the second part lies
+                    // behind the first, D = 128 in the other half, D = 64 in the same rows
+#pragma unroll
+                    for (int kq = 0; kq < 2 * (D / 32); kq++) {
+                        const uint32_t step = (uint32_t)(kq % (D / 32)) * 32;
+                        const uint32_t offq = kq < D / 32 ? step : step + (D == 128 ? kQHalf : 64u);
+                        tc::mma_ss_f8(dS, tc::smem_desc(qt + offq, 16, 1024), k_desc(ka + step), idS, kq > 0);
+                    }
+                    tc::commit(smem_u32(&s_full[t]));
+                };
+                auto landed = [&](int j) {
+                    return mbar_wait(&k_full[(g0 + j) % kSKStages], ((g0 + j) / kSKStages) & 1);
+                };
+                if (nk > 0) {
+                    // the buffer is free: this warp saw the previous item's last P.V complete
+                    if (!(ok = landed(0)) || !(ok = turn.take()))
+                        break;
+                    scores(0);
+                    turn.pass();
+                }
+                for (int j = 0; j < nk; j++) {
+                    // P.V_t(j) once P_t(j) is written and V tile j converted; and, so that
+                    // nothing is waited for that the other warp may owe while the turn is
+                    // held, K tile j + 1 landed
+                    const int s = (g0 + j) % kSVStages;
+                    if (!(ok = mbar_wait(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
+                        break;
+                    // the item's first P.V overwrites O: the tile's previous epilogue
+                    // must have read it out
+                    if (j == 0 && used >= 1 && !(ok = mbar_wait(&o_free[t], (used - 1) & 1)))
+                        break;
+                    if (j + 1 < nk && !(ok = landed(j + 1)))
+                        break;
+                    // keys 64 .. 127 first: their P is written first, and their MMAs run
+                    // while the softmax is at the other half
+                    const uint32_t va = smem_u32(sV + (size_t)s * kVTile);
+                    auto pv = [&](int half, bool add) {
+                        tc::fence_after();
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int kk = 4 * half + i;
+                            tc::mma_ts(dO, dS + 96u * half + 8u * i,
+                                       tc::smem_desc(va + 2048u * kk, kVHalf, 1024), idO,
+                                       (add || i > 0) ? 1u : 0u);
+                        }
+                    };
+                    if (!(ok = mbar_wait(&pv_ready[2 + t], gq & 1)) || !(ok = turn.take()))
+                        break;
+                    pv(1, j > 0);
+                    turn.pass();
+                    if (!(ok = mbar_wait(&pv_ready[t], gq & 1)) || !(ok = turn.take()))
+                        break;
+                    pv(0, true);
+                    tc::commit(smem_u32(&pv_done[t]));
+                    // S_t(j + 1) overwrites P_t(j)
+                    ok = mbar_wait(&pv_done[t], gq & 1);
+                    gq++;
+                    if (ok) {
+                        mbar_arrive(&v_empty[s]);
+                        if (j + 1 < nk)
+                            scores(j + 1);
+                    }
+                    turn.pass();
+                    if (!ok)
+                        break;
+                }
+                // K and V tiles that this query tile does not read
+                for (int j = nk; ok && j < nkt; j++) {
+                    const int s = (g0 + j) % kSVStages;
+                    if (!(ok = landed(j)))
+                        break;
+                    for (int w = 0; w < 4; w++)  // for its softmax warps
+                        mbar_arrive(&k_empty[(g0 + j) % kSKStages]);
+                    if (!(ok = mbar_wait(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
+                        break;
+                    mbar_arrive(&v_empty[s]);
+                }
+                if (!ok)
+                    break;
+                g0 += nkt;
+                used += nk > 0 ? 1 : 0;
+                mbar_arrive(&item_free[n & 1]);
+            }
+            if (!ok)
+                flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
+            tc::commit(smem_u32(mma_done));  // every MMA completes before TMEM is released
+        }
+        __syncwarp();
+        mbar_wait(mma_done, 0);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int tq = warp >> 2;            // query tile of this group (A = 0, B = 1)
+        const int r = threadIdx.x & 127;     // row = TMEM lane
+        const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tO = tmem + 128u * tq + tl, tS = tmem + 256u + 128u * tq + tl;
+        bool ok = true;
+        int g0 = 0, gq = 0;
+        int used = 0;  // items in which this query tile had work
+        for (int n = 0; ok; n++) {
+            ok = __all_sync(FULL, mbar_wait(&item_ready[n & 1], (n >> 1) & 1));
+            if (!ok)
+                break;
+            const WideItem item = items[n & 1];
+            const PrefillItem &it = item.f;
+            if (it.b < 0)
+                break;
+            const int nkt = it.nkt[tq], all = max(it.nkt[0], it.nkt[1]);
+            const int j0 = SPLIT ? item.j0 : 0;
+            const int tok = it.tok0 + tq * TPC + r / G, g = r % G;
+            const bool valid = tok < it.q_len;
+            const int pos = (it.k_len - it.q_len) + tok;
+            const int32_t *table = p.block_tables + (size_t)it.b * p.MBS;
+            const int k_len = it.k_len;
+            float m = -INFINITY, l = 0.f;
+            float unit = 1.f;   // of the V tiles so far: V = unit * f16
+            float o_unit = 1.f; // of O
+            // boxes of a tile that the producer loads (block ids in [0, NB)); lanes 0-7
+            // read the entries a tile ahead
+            auto table_entry = [&](int j) -> int {
+                const int key0 = (j0 + j) * kSKeys + lane * kBox;
+                return (lane < kBoxes && j < all && key0 < k_len) ? __ldg(table + key0 / p.bs) : -1;
+            };
+            auto loaded = [&](int blk) { return __ballot_sync(FULL, blk >= 0 && blk < p.NB) & 0xffu; };
+            // This group's half (64 keys) of V tile j: codes -> f16 in the other buffer,
+            // times their block's scale over `unit`, rows past k_len or of unloaded boxes
+            // zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups take part
+            // in every V tile of the item, in order, so both have the same `unit`: it
+            // moves to a tile's largest scale where that is 2^7 above it (448 * 2^7 is
+            // within f16) or 2^8 below (where f16 would begin to lose bits).
+            auto convert_v = [&](int j, uint32_t boxes) -> bool {
+                const int gv = g0 + j, s = gv % kSRStages, kb = (j0 + j) * kSKeys + 64 * tq;
+                if (!__all_sync(FULL, mbar_wait(&r_full[s], (gv / kSRStages) & 1)))
+                    return false;
+                constexpr int CPR = D / 16;              // 16-byte pieces of a row of codes
+                constexpr int NCH = 64 * CPR / 128;      // ... per thread
+                const uint4 *vr = reinterpret_cast<const uint4 *>(sR + (size_t)s * kTile + tq * (kTile / 2));
+                uint4 w[NCH];
+#pragma unroll
+                for (int u = 0; u < NCH; u++)
+                    w[u] = vr[r + 128 * u];
+                const float *sc = v_scales[gv % kSScales].scale;
+                const float4 s0 = *reinterpret_cast<const float4 *>(sc), s1 = *reinterpret_cast<const float4 *>(sc + 4);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&r_empty[s]);
+                const float most = fmaxf(fmaxf(fmaxf(s0.x, s0.y), fmaxf(s0.z, s0.w)),
+                                         fmaxf(fmaxf(s1.x, s1.y), fmaxf(s1.z, s1.w)));
+                if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f))
+                    unit = most;
+                const float inv = 1.f / unit;
+                const uint32_t mine = (boxes >> (4 * tq)) & 0xfu;
+                const bool clear = mine != 0xfu || kb + 64 > k_len;
+                // the f16 buffer's last tile has been read
+                const int b = gv % kSVStages;
+                if (!__all_sync(FULL, mbar_wait(&v_empty[b], ((gv / kSVStages) & 1) ^ 1)))
+                    return false;
+                uint8_t *vt = sV + (size_t)b * kVTile;
+#pragma unroll
+                for (int u = 0; u < NCH; u++) {
+                    const int at = r + 128 * u, row = at / CPR;
+                    // as the copy swizzled it: piece `col` of the row lies at at % CPR
+                    const int col = D == 128 ? (at % CPR) ^ (row & 7) : (at % CPR) ^ ((row >> 1) & 3);
+                    const float f = sc[4 * tq + row / kBox];
+                    const uint32_t f2 = pack_f16x2(f * inv, f * inv);
+                    uint4 a = e4m3x8_to_f16(w[u].x, w[u].y, f2), c = e4m3x8_to_f16(w[u].z, w[u].w, f2);
+                    if (clear && (kb + row >= k_len || !((mine >> (row / kBox)) & 1u)))
+                        a = c = make_uint4(0u, 0u, 0u, 0u);
+                    // sixteen values: pieces 2 (col % 4) and the next of their half's row.
+                    // Lanes of the second half write the next one first, so that eight lanes
+                    // (a row of D = 128, two of D = 64) touch all banks
+                    uint8_t *line = vt + (col >> 2) * kVHalf + (64 * tq + row) * 128;
+                    const bool swap = D == 128 && (col >> 2) != 0;
+                    const int p0 = (2 * (col & 3)) ^ (row & 7), p1 = (2 * (col & 3) + 1) ^ (row & 7);
+                    *reinterpret_cast<uint4 *>(line + 16 * (swap ? p1 : p0)) = swap ? c : a;
+                    *reinterpret_cast<uint4 *>(line + 16 * (swap ? p0 : p1)) = swap ? a : c;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&v_conv[b]);
+                return true;
+            };
+            // This row of Q as two E4M3 parts, q = sq (high + low), in its own place.  With
+            // sq = 2^(E - 7) for max|q| in [2^E, 2^(E + 1)) the sum is exact for every
+            // element of magnitude >= max|q| 2^-9 and within max|q| 2^-17 for the rest
+            // (E4M3's least step is 2^-9).  A negative softmax scale negates the parts; an
+            // infinite element makes the row NaN.
+            float sl = 0.f;  // score -> log2 units, but for K's scale
+            if (nkt > 0) {
+                if (!(ok = __all_sync(FULL, mbar_wait(&q_full[tq], used & 1))))
+                    break;
+                used++;
+                uint8_t *qr = sQ + (size_t)tq * kQTile + r * 128;
+                uint4 w[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; i++)
+                    w[i] = *reinterpret_cast<const uint4 *>(qr + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4));
+                uint32_t top = 0;  // two bf16 magnitudes
+#pragma unroll
+                for (int i = 0; i < D / 8; i++) {
+                    constexpr uint32_t ABS = 0x7fff7fffu;
+                    top = bf16x2_max(bf16x2_max(top, w[i].x & ABS), bf16x2_max(w[i].y & ABS, bf16x2_max(w[i].z & ABS, w[i].w & ABS)));
+                }
+                const int ebits = min(max((int)(max(top & 0xffffu, top >> 16) >> 7), 8), 254);
+                sl = p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23);
+                if (max(top & 0xffffu, top >> 16) == 0x7f80u)
+                    sl = NAN;
+                float inv = __uint_as_float((uint32_t)(261 - ebits) << 23);
+                if (p.neg_scale)
+                    inv = -inv;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) {  // sixteen elements
+                    const uint4 e[2] = {w[2 * i], w[2 * i + 1]};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        const uint32_t w0 = c & 1 ? e[c >> 1].z : e[c >> 1].x, w1 = c & 1 ? e[c >> 1].w : e[c >> 1].y;
+                        const float2 x0 = bf16x2_to_float2(w0), x1 = bf16x2_to_float2(w1);
+                        const float a0 = x0.x * inv, a1 = x0.y * inv, a2 = x1.x * inv, a3 = x1.y * inv;
+                        const uint32_t h01 = f32x2_to_e4m3x2(a0, a1), h23 = f32x2_to_e4m3x2(a2, a3);
+                        const float2 b01 = f16x2_to_float2(e4m3x2_to_f16x2(h01));
+                        const float2 b23 = f16x2_to_float2(e4m3x2_to_f16x2(h23));
+                        hi[c] = h01 | (h23 << 16);
+                        lo[c] = f32x2_to_e4m3x2(a0 - b01.x, a1 - b01.y) | (f32x2_to_e4m3x2(a2 - b23.x, a3 - b23.y) << 16);
+                    }
+                    const int lo_at = D == 128 ? (int)kQHalf + ((i ^ (r & 7)) << 4) : ((4 + i) ^ (r & 7)) << 4;
+                    *reinterpret_cast<uint4 *>(qr + ((i ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(qr + lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&q_conv[tq]);
+            }
+            uint32_t boxes = loaded(table_entry(0));
+            int blk_next = table_entry(1);
+            if (!(ok = convert_v(0, boxes)))
+                break;
+            for (int j = 0; j < nkt; j++) {
+                const int gt = gq + j;
+                const uint32_t boxes_next = loaded(blk_next);
+                blk_next = table_entry(j + 2);
+                ok = __all_sync(FULL, mbar_wait(&s_full[tq], gt & 1));
+                if (!ok)
+                    break;
+                tc::fence_after();
+                // the scales of the K tile's boxes (its stage's barrier orders them behind
+                // the producer's writes), then, S_t(j) being complete, the K tile, and
+                // after the item's last one Q, may go
+                const int sk = (g0 + j) % kSKStages;
+                if (!(ok = __all_sync(FULL, mbar_wait(&k_full[sk], ((g0 + j) / kSKStages) & 1))))
+                    break;
+                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
+                const bool equal = ks.equal != 0;
+                const float ks0 = ks.scale[0];
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&k_empty[sk]);
+                    if ((warp & 3) == 0 && j == nkt - 1)
+                        mbar_arrive(&q_empty[tq]);
+                }
+                // one scale in the tile: it joins the row's; else every box's scores are
+                // multiplied by theirs
+                const float cs = equal ? sl * ks0 : sl;
+                const float2 cs2 = make_float2(cs, cs);
+                const int key_base = (j0 + j) * kSKeys;
+                // masked keys: past this row's position (the diagonal tiles) or in an
+                // unloaded box; most tiles have none in the whole warp
+                const bool any_masked = __any_sync(FULL, boxes != 0xffu || key_base + kSKeys - 1 > pos);
+                const int lim = pos - key_base;  // keys i > lim are in the future
+                float x[64];
+                auto load = [&](int half) {
+                    uint32_t a[32], b[32];
+                    tc::ld32(tS + 64 * half, a);
+                    tc::ld32(tS + 64 * half + 32, b);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        x[i] = __uint_as_float(a[i]);
+                        x[32 + i] = __uint_as_float(b[i]);
+                    }
+                    if (!equal) {
+#pragma unroll
+                        for (int i = 0; i < 64; i++)
+                            x[i] *= ks.scale[4 * half + i / kBox];
+                    }
+                    if (any_masked) {
+                        const uint32_t hb = boxes >> (4 * half);
+#pragma unroll
+                        for (int i = 0; i < 64; i++)
+                            x[i] = (64 * half + i > lim || !((hb >> (i / kBox)) & 1u)) ? -INFINITY : x[i];
+                    }
+                };
+                auto top = [&]() {
+                    float t8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        t8[i] = x[i];
+#pragma unroll
+                    for (int i = 8; i < 64; i++)
+                        t8[i & 7] = fmaxf(t8[i & 7], x[i]);
+                    return fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
+                                 fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+                };
+                load(0);
+                float mraw = top();
+                load(1);
+                mraw = fmaxf(mraw, top());
+                const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
+                const bool moves = __any_sync(FULL, mx > m + kLazy);
+                if (moves || unit != o_unit) {
+                    const float mn = moves ? fmaxf(m, mx) : m;
+                    const float alpha = !moves || mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+                    const float o_alpha = unit == o_unit ? alpha : alpha * (o_unit / unit);
+                    o_unit = unit;
+                    if (j > 0) {
+                        // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1)
+                        // completed, and the next P.V waits for this group's P
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; cc++) {
+                            uint32_t ro[32];
+                            tc::ld32(tO + 32 * cc, ro);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                ro[i] = __float_as_uint(__uint_as_float(ro[i]) * o_alpha);
+                            tc::st32(tO + 32 * cc, ro);
+                        }
+                        tc::wait_st();
+                    }
+                    l *= alpha;
+                    m = mn;
+                }
+                const float nmu = m == -INFINITY ? 0.f : -m;
+                const float2 nm2 = make_float2(nmu, nmu);
+                float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
+                auto exponentiate = [&](uint32_t to) {
+                    uint32_t pk[32];
+                    if (!any_masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) {
+                            const float2 a = ffma2(make_float2(x[2 * i], x[2 * i + 1]), cs2, nm2);
+                            const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                            if (i & 1)
+                                ls1 = fadd2(ls1, e);
+                            else
+                                ls0 = fadd2(ls0, e);
+                            pk[i] = pack_f16x2(e.x, e.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) {
+                            float2 a = ffma2(make_float2(x[2 * i], x[2 * i + 1]), cs2, nm2);
+                            // exact zeros for masked keys (also when the scale is 0)
+                            a.x = x[2 * i] == -INFINITY ? -INFINITY : a.x;
+                            a.y = x[2 * i + 1] == -INFINITY ? -INFINITY : a.y;
+                            const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                            if (i & 1)
+                                ls1 = fadd2(ls1, e);
+                            else
+                                ls0 = fadd2(ls0, e);
+                            pk[i] = pack_f16x2(e.x, e.y);
+                        }
+                    }
+                    tc::st32(to, pk);
+                };
+                auto hand_over = [&](int half) {
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&pv_ready[2 * half + tq]);
+                };
+                exponentiate(tS + 96);  // keys 64..127, over score columns read above
+                hand_over(1);
+                load(0);                // keys 0..63 again
+                exponentiate(tS);
+                l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+                hand_over(0);
+                // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
+                if (j + 1 < all && !(ok = convert_v(j + 1, boxes_next)))
+                    break;
+                boxes = boxes_next;
+            }
+            if (!ok)
+                break;
+            // V tiles that only the other query tile reads
+            for (int jv = max(nkt, 1) + (nkt > 0 ? 1 : 0); ok && jv < all; jv++) {
+                const uint32_t bx = loaded(table_entry(jv));
+                ok = convert_v(jv, bx);
+            }
+            if (!ok)
+                break;
+            // a split that only the other query tile has keys in
+            const bool piece = SPLIT && item.split >= 0;
+            if (piece && nkt == 0 && valid)
+                p.part_lse[(size_t)item.split * p.Tq * p.Hq +
+                           ((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] = -INFINITY;
+            if (nkt > 0) {
+                const int gl = gq + nkt - 1;
+                ok = __all_sync(FULL, mbar_wait(&pv_done[tq], gl & 1));
+                if (!ok)
+                    break;
+                tc::fence_after();
+                const float inv = l > 0.f ? o_unit / l : 0.f;
+                const size_t row = (size_t)it.cq0 + tok;
+                const size_t lse_at = ((size_t)it.kvh * p.Tq + row) * G + g;
+                if (piece) {
+                    // this split's output in fp32, and its log-sum-exp (-inf: no key)
+                    if (valid)
+                        p.part_lse[(size_t)item.split * p.Tq * p.Hq + lse_at] =
+                            l == 0.f ? -INFINITY : m + log2f(l);
+                    float4 *dst = reinterpret_cast<float4 *>(
+                        p.part_out + (((size_t)item.split * p.Tq + row) * p.Hq + it.kvh * G + g) * D);
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t ro[32];
+                        tc::ld32(tO + 32 * cc, ro);
+                        tc::wait_ld();
+                        if (valid) {
+#pragma unroll
+                            for (int i = 0; i < 8; i++)
+                                dst[8 * cc + i] = make_float4(__uint_as_float(ro[4 * i]) * inv,
+                                                              __uint_as_float(ro[4 * i + 1]) * inv,
+                                                              __uint_as_float(ro[4 * i + 2]) * inv,
+                                                              __uint_as_float(ro[4 * i + 3]) * inv);
+                        }
+                    }
+                } else {
+                    if (SPLIT && valid)
+                        p.part_lse[lse_at] = INFINITY;  // nothing to join
+                    // 64 columns (eight 16-byte pieces) of a row at a time; eight lanes
+                    // trade their rows' pieces (three butterfly steps), so that a store
+                    // instruction writes whole 128-byte lines of four rows, not 16 bytes
+                    // in each of 32 lines
+#pragma unroll 1
+                    for (int hf = 0; hf < HALVES; hf++) {
+                        uint32_t ra[32], rb[32], v[32];
+                        tc::ld32(tO + 64 * hf, ra);
+                        tc::ld32(tO + 64 * hf + 32, rb);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            v[i] = pack_bf16x2(__uint_as_float(ra[2 * i]) * inv, __uint_as_float(ra[2 * i + 1]) * inv);
+                            v[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]) * inv,
+                                                    __uint_as_float(rb[2 * i + 1]) * inv);
+                        }
+#pragma unroll
+                        for (int s = 1; s < 8; s *= 2) {
+                            const bool up = (lane & s) != 0;
+#pragma unroll
+                            for (int k = 0; k < 8; k++) {
+                                if (k & s)
+                                    continue;
+#pragma unroll
+                                for (int w = 0; w < 4; w++) {  // piece k of the upper lane for k + s of the lower
+                                    const uint32_t give = up ? v[4 * k + w] : v[4 * (k + s) + w];
+                                    const uint32_t got = __shfl_xor_sync(FULL, give, s);
+                                    v[4 * k + w] = up ? got : v[4 * k + w];
+                                    v[4 * (k + s) + w] = up ? v[4 * (k + s) + w] : got;
+                                }
+                            }
+                        }
+                        // this lane now has piece lane % 8 of the rows 8 (lane / 8) + k
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const int rr = 32 * (warp & 3) + (lane & 24) + k;
+                            const int tk = it.tok0 + tq * TPC + rr / G;
+                            if (tk < it.q_len)
+                                *reinterpret_cast<uint4 *>(
+                                    p.out + (((size_t)it.cq0 + tk) * p.Hq + it.kvh * G + rr % G) * D + 64 * hf +
+                                    8 * (lane & 7)) =
+                                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        }
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&o_free[tq]);  // the tile's next first P.V may overwrite O
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&item_free[n & 1]);
+            g0 += all;
+            gq += nkt;
+        }
+        if (!ok && lane == 0)
+            flag_error(p.err_flag, 0x8 /* PKV_FLAG_TIMEOUT */);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kTcMmaWarp) {
+        tc::fence_after();
+        tc::dealloc(tmem, kTcCols);
+    }
+}
+
+template <int D>
+inline cudaError_t launch_prefill_scaled_d(int G, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                         const CUtensorMap *tmv, const PrefillParams &p, dim3 grid,
+                                         size_t smem, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (G) {
+    case 1:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 1, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 1, false>, *tmq, *tmk, *tmv, p);
+    case 2:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 2, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 2, false>, *tmq, *tmk, *tmv, p);
+    case 4:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 4, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 4, false>, *tmq, *tmk, *tmv, p);
+    case 8:
+        return p.splits > 1 ? cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 8, true>, *tmq, *tmk, *tmv, p)
+                            : cudaLaunchKernelEx(&cfg, paged_prefill_scaled_kernel<D, 8, false>, *tmq, *tmk, *tmv, p);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int D> inline const void *prefill_scaled_kernel_d(int G, bool split)
+{
+    switch (G) {
+    case 1:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 1, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 1, false>);
+    case 2:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 2, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 2, false>);
+    case 4:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 4, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 4, false>);
+    case 8:
+        return split ? reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 8, true>)
+                     : reinterpret_cast<const void *>(&paged_prefill_scaled_kernel<D, 8, false>);
+    default: return nullptr;
+    }
+}
+
+} // namespace pkv

@@ -11,6 +11,7 @@
 // loads/stores; the row is Hkv*D*2 bytes (2 KB for 8 KV heads x 128).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
+#include "pkv_quant.cuh"
 
 namespace pkv {
 
@@ -61,17 +62,6 @@ __global__ void __launch_bounds__(kStoreThreads)
 // kv_cache_dtype): every bf16 value is widened, multiplied by the reciprocal
 // of its tensor's scale in fp32, and encoded as OCP E4M3 (nearest even,
 // finite saturation).  One thread turns 8 values (16 B) into 8 codes (8 B).
-__device__ __forceinline__ uint2 quantize8(uint4 a, float inv)
-{
-    const float2 f0 = bf16x2_to_float2(a.x), f1 = bf16x2_to_float2(a.y);
-    const float2 f2 = bf16x2_to_float2(a.z), f3 = bf16x2_to_float2(a.w);
-    const uint32_t c0 = f32x2_to_e4m3x2(__fmul_rn(f0.x, inv), __fmul_rn(f0.y, inv));
-    const uint32_t c1 = f32x2_to_e4m3x2(__fmul_rn(f1.x, inv), __fmul_rn(f1.y, inv));
-    const uint32_t c2 = f32x2_to_e4m3x2(__fmul_rn(f2.x, inv), __fmul_rn(f2.y, inv));
-    const uint32_t c3 = f32x2_to_e4m3x2(__fmul_rn(f3.x, inv), __fmul_rn(f3.y, inv));
-    return make_uint2(c0 | (c1 << 16), c2 | (c3 << 16));
-}
-
 __global__ void __launch_bounds__(kStoreThreads)
     store_kvcache_fp8_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                              uint2 *__restrict__ k_cache, uint2 *__restrict__ v_cache,

@@ -24,6 +24,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     return d;
 }
 
+// The same with the 64-byte swizzle (mode 4): K-major rows of 64 B, 8-row atoms 512 B
+// apart.
+__device__ __forceinline__ uint64_t smem_desc_64b(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return (smem_desc(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
+}
+
 // Instruction descriptor for kind::f16 with bf16 A and B and an f32
 // accumulator: D format (bits 4-5) = f32, A/B format (7-9, 10-12) = bf16,
 // B major-ness (bit 16), N >> 3 (bits 17-22), M >> 4 (bits 24-28).
@@ -38,6 +45,23 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major)
 {
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
+}
+
+// Instruction descriptor for kind::f8f6f4 with K-major E4M3 A and B (format fields 0)
+// and an f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem desc] . B[smem desc], 8-bit elements, 32 along the contraction
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
 }
 
 // D[tmem] (+)= A[smem desc] . B[smem desc]

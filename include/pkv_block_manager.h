@@ -98,6 +98,30 @@ int pkv_bm_can_evict(const pkv_block_manager *bm, int64_t seq_id);
  */
 pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget);
 
+/*
+ * New sequence child_id with parent_id's tokens (a beam, a second sample of one
+ * prompt).  Their full blocks are shared (one more reference each).  A last block
+ * that is partly filled would be written by both, so the child gets a free block in
+ * its place: pair[0], pair[1] receive the two ids, source and destination, for
+ * pkv_copy_blocks, or -1, -1 where the last block is full.  Enqueue the copy before
+ * either sequence's next store on the same stream.  Fails with PKV_ERR_INVALID_ARG
+ * (unknown parent, existing child) or PKV_ERR_WORKSPACE (no free block, no host
+ * memory), changing nothing.
+ */
+pkv_status pkv_bm_fork(pkv_block_manager *bm, int64_t parent_id, int64_t child_id, int32_t *pair);
+
+/*
+ * Move the sequences' blocks to the lowest ids: afterwards the n blocks in use are
+ * 0 .. n - 1 (so that, for instance, the caches' tails can be given back).
+ * pairs[0 .. *n) receives the moves, source and destination, for pkv_copy_blocks: no
+ * id is both, and what moves keeps its references, its place in every table and its
+ * content hash; free blocks that moves overwrite lose theirs.  With more moves than
+ * `cap` pairs nothing changes, *n says how many there are, and PKV_ERR_WORKSPACE is
+ * returned.  Block tables and slots taken before are void; enqueue the copy before
+ * any use of new ones on the same stream.
+ */
+pkv_status pkv_bm_compact(pkv_block_manager *bm, int32_t *pairs, int64_t cap, int64_t *n);
+
 /* Free blocks in the pool. */
 int64_t pkv_bm_num_free_blocks(const pkv_block_manager *bm);
 

@@ -43,6 +43,10 @@ def _lib():
         lib.pkv_bm_can_evict.argtypes = [P, i64]
         lib.pkv_bm_evict.restype = i32
         lib.pkv_bm_evict.argtypes = [P, i64, i64]
+        lib.pkv_bm_fork.restype = i32
+        lib.pkv_bm_fork.argtypes = [P, i64, i64, P]
+        lib.pkv_bm_compact.restype = i32
+        lib.pkv_bm_compact.argtypes = [P, P, i64, ctypes.POINTER(i64)]
         lib.pkv_bm_num_free_blocks.restype = i64
         lib.pkv_bm_num_free_blocks.argtypes = [P]
         lib.pkv_bm_seq_len.restype = i64
@@ -133,6 +137,28 @@ class BlockManager:
         blocks, beside ``evict_kvcache`` with the same budget; take that call's block tables
         first.  Raises PkvError if a block is shared."""
         _check(self._lib, self._lib.pkv_bm_evict(self._h, seq_id, int(budget)))
+
+    def fork(self, parent_id: int, child_id: int) -> np.ndarray:
+        """New sequence ``child_id`` with the parent's tokens, sharing its full blocks.
+
+        Returns int32 ``[n, 2]``, the (source, destination) of the last block where it is
+        partly filled (n is 0 or 1): give it to ``copy_blocks`` with every tensor under the
+        block ids before either sequence's next store.
+        """
+        pair = np.empty((1, 2), dtype=np.int32)
+        _check(self._lib, self._lib.pkv_bm_fork(self._h, int(parent_id), int(child_id), _ptr(pair)))
+        return pair if pair[0, 0] >= 0 else pair[:0]
+
+    def compact(self) -> np.ndarray:
+        """Move the sequences' blocks to the lowest ids; returns the moves, int32 ``[n, 2]``.
+
+        Give them to ``copy_blocks`` before any use of the tables and slots as they are
+        now; those taken before are void.
+        """
+        pairs = np.empty((self.num_blocks, 2), dtype=np.int32)
+        n = ctypes.c_int64()
+        _check(self._lib, self._lib.pkv_bm_compact(self._h, _ptr(pairs), self.num_blocks, ctypes.byref(n)))
+        return pairs[: n.value].copy()
 
     @property
     def num_free_blocks(self) -> int:

@@ -3,7 +3,9 @@
 #include "pkv_block_manager.h"
 
 #include <cstring>
+#include <new>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 namespace pkv {
@@ -365,6 +367,83 @@ pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget)
     }
     s.tokens.resize((size_t)budget);
     s.trimmed = true;
+    return PKV_OK;
+}
+
+pkv_status pkv_bm_fork(pkv_block_manager *bm, int64_t parent_id, int64_t child_id, int32_t *pair)
+{
+    if (!bm || !pair)
+        return err(PKV_ERR_INVALID_ARG, "bm_fork: null argument");
+    auto it = bm->seqs.find(parent_id);
+    if (it == bm->seqs.end())
+        return err(PKV_ERR_INVALID_ARG, "bm_fork: unknown parent sequence id");
+    if (bm->seqs.count(child_id))
+        return err(PKV_ERR_INVALID_ARG, "bm_fork: child sequence id already allocated");
+    const bool partial = (int64_t)it->second.tokens.size() % bm->block_size != 0;
+    if (partial && bm->free_ids.empty())
+        return err(PKV_ERR_WORKSPACE, "bm_fork: no free block for the child's last one");
+    Sequence *child = nullptr;
+    try {
+        Sequence copy = it->second;
+        child = &bm->seqs.emplace(child_id, std::move(copy)).first->second;
+    } catch (const std::bad_alloc &) {
+        return err(PKV_ERR_WORKSPACE, "bm_fork: out of host memory");
+    }
+    pair[0] = pair[1] = -1;
+    for (size_t i = 0; i < child->table.size(); i++) {
+        if (partial && i + 1 == child->table.size()) {
+            pair[0] = child->table[i];
+            child->table[i] = pair[1] = bm->take_front();
+        } else {
+            bm->blocks[child->table[i]].ref_count++;
+        }
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_bm_compact(pkv_block_manager *bm, int32_t *pairs, int64_t cap, int64_t *n)
+{
+    if (!bm || !n || cap < 0 || (cap > 0 && !pairs))
+        return err(PKV_ERR_INVALID_ARG, "bm_compact: bad arguments");
+    const int32_t NB = (int32_t)bm->blocks.size();
+    int32_t used = 0;
+    for (const Block &b : bm->blocks)
+        used += b.ref_count > 0;
+    // as many free ids below `used` as blocks in use from it on
+    int64_t moves = 0;
+    for (int32_t id = used; id < NB; id++)
+        moves += bm->blocks[id].ref_count > 0;
+    *n = moves;
+    if (moves > cap)
+        return err(PKV_ERR_WORKSPACE, "bm_compact: more moves than the list holds");
+    std::vector<int32_t> to;
+    try {
+        to.assign((size_t)NB, -1);
+    } catch (const std::bad_alloc &) {
+        return err(PKV_ERR_WORKSPACE, "bm_compact: out of host memory");
+    }
+    int32_t dst = 0;
+    int64_t at = 0;
+    for (int32_t src = used; src < NB; src++) {
+        if (bm->blocks[src].ref_count == 0)
+            continue;
+        while (bm->blocks[dst].ref_count > 0)
+            dst++;
+        bm->forget(dst);
+        bm->free_ids.remove(dst);
+        std::swap(bm->blocks[dst], bm->blocks[src]);
+        auto it = bm->hash_to_block.find(bm->blocks[dst].hash);
+        if (bm->blocks[dst].hash != kNoHash && it != bm->hash_to_block.end() && it->second == src)
+            it->second = dst;
+        bm->free_ids.push_back(src);
+        to[src] = dst;
+        pairs[2 * at] = src;
+        pairs[2 * at + 1] = dst;
+        at++;
+    }
+    for (auto &s : bm->seqs)
+        for (int32_t &id : s.second.table)
+            id = to[id] >= 0 ? to[id] : id;
     return PKV_OK;
 }
 

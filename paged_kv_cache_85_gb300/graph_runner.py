@@ -10,12 +10,15 @@ Replaying removes the per-launch host cost, which dominates small batches.
 
 A step is store_kvcache followed by paged_attn_decode, exactly as the eager
 calls; only the launches are recorded.  The caches, block-table width (MBS)
-and softmax scale are fixed per runner.
+and softmax scale are fixed per runner.  With ``k_scales`` and ``v_scales`` the
+caches are FP8 with a scale per block and KV head, and a step is
+store_kvcache_scaled followed by paged_attn_decode_scaled.
 """
 
 from __future__ import annotations
 
-from . import decode_workspace_bytes, paged_attn_decode, store_kvcache
+from . import (decode_workspace_bytes, paged_attn_decode, paged_attn_decode_scaled, store_kvcache,
+               store_kvcache_scaled)
 
 
 def graph_batch_sizes(max_bs: int) -> list[int]:
@@ -30,11 +33,14 @@ class DecodeGraphRunner:
     """Captured decode steps over fixed caches; ``step`` replays one."""
 
     def __init__(self, k_cache, v_cache, num_q_heads: int, max_bs: int, max_blocks_per_seq: int,
-                 scale: float, batch_sizes=None, stream=None):
+                 scale: float, batch_sizes=None, stream=None, k_scales=None, v_scales=None):
         import torch
 
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales go together")
         self.torch = torch
         self.k_cache, self.v_cache = k_cache, v_cache
+        self.k_scales, self.v_scales = k_scales, v_scales
         NB, bs, Hkv, D = k_cache.shape
         dev = k_cache.device
         self.Hq, self.Hkv, self.D, self.MBS = num_q_heads, Hkv, D, max_blocks_per_seq
@@ -64,6 +70,12 @@ class DecodeGraphRunner:
         torch.cuda.synchronize(dev)
 
     def _run(self, b: int):
+        if self.k_scales is not None:
+            cache = (self.k_cache, self.v_cache, self.k_scales, self.v_scales)
+            store_kvcache_scaled(self.k_new[:b], self.v_new[:b], *cache, self.slots[:b])
+            paged_attn_decode_scaled(self.q[:b], *cache, self.tables[:b], self.lens[:b], self.scale, self.out[:b],
+                                     workspace=self.ws)
+            return
         store_kvcache(self.k_new[:b], self.v_new[:b], self.k_cache, self.v_cache, self.slots[:b])
         paged_attn_decode(self.q[:b], self.k_cache, self.v_cache, self.tables[:b], self.lens[:b],
                           self.scale, self.out[:b], workspace=self.ws)

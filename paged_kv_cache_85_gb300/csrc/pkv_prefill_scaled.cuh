@@ -43,11 +43,20 @@ static_assert(kSScales >= 2 * kSKStages && kSScales >= 2 * kSRStages, "a tile's 
 // pv_ready[2 halves], pv_done, o_free, then item_ready[2], item_free[2], mma_done
 constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
 
-// The scales of a tile's eight boxes.  K: equal says that all are scale[0] (boxes that
-// are not read count as any).  V: 0 for a box that is not read.
+// The scales of a tile's eight boxes, and which of them are read (a bit each).
+// K: equal says that all scales are scale[0] (boxes that are not read count as any).
+// V: scale over unit as a pair of f16 in `factor`; O is held in `unit`.
 struct __align__(16) BoxScales {
-    float scale[kSKeys / kBox];
-    int equal, pad[3];
+    union {
+        float scale[kSKeys / kBox];
+        uint32_t factor[kSKeys / kBox];
+    };
+    int read;
+    union {
+        int equal;
+        float unit;
+    };
+    int pad[2];
 };
 
 struct ScaledSmem {
@@ -119,7 +128,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const ScaledSmem L = scaled_smem_layout(D);
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L.bars);  // [2] Q tile t landed
     uint64_t *q_conv = q_full + 2;                // [2] ... and became E4M3 parts (4 warps)
-    uint64_t *q_empty = q_conv + 2;               // [2] tile t's last S of the item completed
+    uint64_t *q_empty = q_conv + 2;               // [2] tile t's last S of the item completed (4 warps)
     uint64_t *k_full = q_empty + 2;
     uint64_t *k_empty = k_full + kSKStages;       // both tiles' S of the K tile completed (4 warps each)
     uint64_t *r_full = k_empty + kSKStages;       // V codes landed
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int t = 0; t < 2; t++) {
             mbar_init(&q_full[t], 1);
             mbar_init(&q_conv[t], 4);
-            mbar_init(&q_empty[t], 1);
+            mbar_init(&q_empty[t], 4);
             mbar_init(&s_full[t], 1);
             mbar_init(&pv_ready[t], 4);
             mbar_init(&pv_ready[2 + t], 4);
@@ -304,6 +313,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             int blk_k = entry(0), next_k = entry(1), blk_v = blk_k, next_v = next_k;
             float sc_k = scale_of(p.k_scales, blk_k), sc_v = scale_of(p.v_scales, blk_v);
+            // V tiles' unit: moves to a tile's largest scale where that is 2^7 above it
+            // (448 * 2^7 is within f16) or 2^8 below (where f16 begins to lose bits)
+            float unit = 1.f, per_unit = 1.f;
             const int per = p.copy_rows;  // tokens per copy: so many lie in one block
             auto issue = [&](int j, int g, bool is_k) {
                 uint64_t *fb = is_k ? k_full : r_full;
@@ -335,11 +347,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (row < 0)
                         sc = read ? first : 1.f;
                     const bool equal = __all_sync(FULL, lane >= kBoxes || sc == (read ? first : 1.f));
+                    if (lane < kBoxes)
+                        bx.scale[lane] = sc;
                     if (lane == 0)
                         bx.equal = equal;
+                } else {
+                    const float most = __uint_as_float(__reduce_max_sync(
+                        FULL, row >= 0 && sc > 0.f && sc < INFINITY ? __float_as_uint(sc) : 0u));
+                    if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f)) {
+                        unit = most;
+                        per_unit = 1.f / most;
+                    }
+                    if (lane < kBoxes)
+                        bx.factor[lane] = pack_f16x2(sc * per_unit, sc * per_unit);
+                    if (lane == 0)
+                        bx.unit = unit;
                 }
-                if (lane < kBoxes)
-                    bx.scale[lane] = sc;
+                if (lane == 0)
+                    bx.read = (int)read;
                 // rows past k_len of a run come along: their scores are masked and
                 // their V rows zeroed
                 const bool copies = row >= 0 && (lane * kBox) % per == 0;
@@ -436,8 +461,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (nk > 0 && !(ok = mbar_wait(&q_conv[t], used & 1)))
                     break;
                 tc::fence_after();
-                if (nk == 0)
-                    mbar_arrive(&q_empty[t]);  // this tile reads no Q this item
+                for (int w = 0; nk == 0 && w < 4; w++)  // this tile reads no Q this item
+                    mbar_arrive(&q_empty[t]);
                 // S_t(j), its K tile landed and S_t's buffer free
                 auto scores = [&](int j) {
                     const int s = (g0 + j) % kSKStages;
@@ -542,6 +567,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         int g0 = 0, gq = 0;
         int used = 0;  // items in which this query tile had work
+        // Conversion of this group's half of a V tile: a thread turns 16 codes of rows
+        // conv_row + kConvStep u.  Eight lanes take four pieces each of two rows, for
+        // D = 128 of different halves: that way their reads and either of their writes
+        // touch all banks.
+        constexpr int kConvPieces = 64 * (D / 16) / 128, kConvStep = 64 / kConvPieces;
+        const int conv_row = 64 * tq + (D == 128 ? 2 * (r >> 4) + ((r >> 2) & 1) : r >> 2);
+        const int conv_col = D == 128 ? (r & 3) + 4 * (((r >> 2) ^ (r >> 3)) & 1) : r & 3;
+        const int conv_from = conv_row * D + 16 * (D == 128 ? conv_col ^ (conv_row & 7)
+                                                            : conv_col ^ ((conv_row >> 1) & 3));
+        const int conv_line = (conv_col >> 2) * (int)kVHalf + conv_row * 128;
+        const int conv_to0 = conv_line + 16 * ((2 * (conv_col & 3)) ^ (conv_row & 7));
+        const int conv_to1 = conv_line + 16 * ((2 * (conv_col & 3) + 1) ^ (conv_row & 7));
         for (int n = 0; ok; n++) {
             ok = __all_sync(FULL, mbar_wait(&item_ready[n & 1], (n >> 1) & 1));
             if (!ok)
@@ -555,75 +592,67 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int tok = it.tok0 + tq * TPC + r / G, g = r % G;
             const bool valid = tok < it.q_len;
             const int pos = (it.k_len - it.q_len) + tok;
-            const int32_t *table = p.block_tables + (size_t)it.b * p.MBS;
             const int k_len = it.k_len;
             float m = -INFINITY, l = 0.f;
             float unit = 1.f;   // of the V tiles so far: V = unit * f16
             float o_unit = 1.f; // of O
-            // boxes of a tile that the producer loads (block ids in [0, NB)); lanes 0-7
-            // read the entries a tile ahead
-            auto table_entry = [&](int j) -> int {
-                const int key0 = (j0 + j) * kSKeys + lane * kBox;
-                return (lane < kBoxes && j < all && key0 < k_len) ? __ldg(table + key0 / p.bs) : -1;
-            };
-            auto loaded = [&](int blk) { return __ballot_sync(FULL, blk >= 0 && blk < p.NB) & 0xffu; };
             // This group's half (64 keys) of V tile j: codes -> f16 in the other buffer,
-            // times their block's scale over `unit`, rows past k_len or of unloaded boxes
+            // times their box's factor, rows past k_len or of boxes that are not read
             // zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups take part
-            // in every V tile of the item, in order, so both have the same `unit`: it
-            // moves to a tile's largest scale where that is 2^7 above it (448 * 2^7 is
-            // within f16) or 2^8 below (where f16 would begin to lose bits).
-            auto convert_v = [&](int j, uint32_t boxes) -> bool {
-                const int gv = g0 + j, s = gv % kSRStages, kb = (j0 + j) * kSKeys + 64 * tq;
+            // in every V tile of the item, in order.
+            auto convert_v = [&](int j) -> bool {
+                const int gv = g0 + j, s = gv % kSRStages, b = gv % kSVStages, kb = (j0 + j) * kSKeys;
                 if (!__all_sync(FULL, mbar_wait(&r_full[s], (gv / kSRStages) & 1)))
                     return false;
-                constexpr int CPR = D / 16;              // 16-byte pieces of a row of codes
-                constexpr int NCH = 64 * CPR / 128;      // ... per thread
-                const uint4 *vr = reinterpret_cast<const uint4 *>(sR + (size_t)s * kTile + tq * (kTile / 2));
-                uint4 w[NCH];
+                const uint8_t *vr = sR + (size_t)s * kTile + conv_from;
+                uint4 w[kConvPieces];
 #pragma unroll
-                for (int u = 0; u < NCH; u++)
-                    w[u] = vr[r + 128 * u];
-                const float *sc = v_scales[gv % kSScales].scale;
-                const float4 s0 = *reinterpret_cast<const float4 *>(sc), s1 = *reinterpret_cast<const float4 *>(sc + 4);
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&r_empty[s]);
-                const float most = fmaxf(fmaxf(fmaxf(s0.x, s0.y), fmaxf(s0.z, s0.w)),
-                                         fmaxf(fmaxf(s1.x, s1.y), fmaxf(s1.z, s1.w)));
-                if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f))
-                    unit = most;
-                const float inv = 1.f / unit;
-                const uint32_t mine = (boxes >> (4 * tq)) & 0xfu;
-                const bool clear = mine != 0xfu || kb + 64 > k_len;
+                for (int u = 0; u < kConvPieces; u++)
+                    w[u] = *reinterpret_cast<const uint4 *>(vr + u * kConvStep * D);
+                const BoxScales &vs = v_scales[gv % kSScales];
+                uint32_t f[kConvPieces];
+#pragma unroll
+                for (int u = 0; u < kConvPieces; u++)
+                    f[u] = vs.factor[(conv_row + u * kConvStep) / kBox];
+                const uint32_t boxes = (uint32_t)vs.read;
+                unit = vs.unit;
                 // the f16 buffer's last tile has been read
-                const int b = gv % kSVStages;
                 if (!__all_sync(FULL, mbar_wait(&v_empty[b], ((gv / kSVStages) & 1) ^ 1)))
                     return false;
+                __syncwarp();  // every lane's reads
+                if (lane == 0)
+                    mbar_arrive(&r_empty[s]);
                 uint8_t *vt = sV + (size_t)b * kVTile;
+                const bool clear = boxes != 0xffu || kb + kSKeys > k_len;
 #pragma unroll
-                for (int u = 0; u < NCH; u++) {
-                    const int at = r + 128 * u, row = at / CPR;
-                    // as the copy swizzled it: piece `col` of the row lies at at % CPR
-                    const int col = D == 128 ? (at % CPR) ^ (row & 7) : (at % CPR) ^ ((row >> 1) & 3);
-                    const float f = sc[4 * tq + row / kBox];
-                    const uint32_t f2 = pack_f16x2(f * inv, f * inv);
-                    uint4 a = e4m3x8_to_f16(w[u].x, w[u].y, f2), c = e4m3x8_to_f16(w[u].z, w[u].w, f2);
-                    if (clear && (kb + row >= k_len || !((mine >> (row / kBox)) & 1u)))
-                        a = c = make_uint4(0u, 0u, 0u, 0u);
-                    // sixteen values: pieces 2 (col % 4) and the next of their half's row.
-                    // Lanes of the second half write the next one first, so that eight lanes
-                    // (a row of D = 128, two of D = 64) touch all banks
-                    uint8_t *line = vt + (col >> 2) * kVHalf + (64 * tq + row) * 128;
-                    const bool swap = D == 128 && (col >> 2) != 0;
-                    const int p0 = (2 * (col & 3)) ^ (row & 7), p1 = (2 * (col & 3) + 1) ^ (row & 7);
-                    *reinterpret_cast<uint4 *>(line + 16 * (swap ? p1 : p0)) = swap ? c : a;
-                    *reinterpret_cast<uint4 *>(line + 16 * (swap ? p0 : p1)) = swap ? a : c;
+                for (int u = 0; u < kConvPieces; u++) {
+                    uint4 x = e4m3x8_to_f16(w[u].x, w[u].y, f[u]), y = e4m3x8_to_f16(w[u].z, w[u].w, f[u]);
+                    if (clear) {
+                        const int row = conv_row + u * kConvStep;
+                        if (kb + row >= k_len || !((boxes >> (row / kBox)) & 1u))
+                            x = y = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    *reinterpret_cast<uint4 *>(vt + conv_to0 + u * kConvStep * 128) = x;
+                    *reinterpret_cast<uint4 *>(vt + conv_to1 + u * kConvStep * 128) = y;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&v_conv[b]);
+                return true;
+            };
+            // The scales of K tile j's boxes, brought with its copies; ahead of its scores,
+            // so that they are not waited for on the chain
+            bool equal = true;
+            float ks0 = 1.f;
+            uint32_t boxes = 0;
+            auto scales_k = [&](int j) -> bool {
+                if (!__all_sync(FULL, mbar_wait(&k_full[(g0 + j) % kSKStages], ((g0 + j) / kSKStages) & 1)))
+                    return false;
+                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
+                equal = ks.equal != 0;
+                ks0 = ks.scale[0];
+                boxes = (uint32_t)ks.read;
                 return true;
             };
             // This row of Q as two E4M3 parts, q = sq (high + low), in its own place.  With
@@ -678,33 +707,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0)
                     mbar_arrive(&q_conv[tq]);
             }
-            uint32_t boxes = loaded(table_entry(0));
-            int blk_next = table_entry(1);
-            if (!(ok = convert_v(0, boxes)))
+            if (!(ok = convert_v(0)) || (nkt > 0 && !(ok = scales_k(0))))
                 break;
+            float v_unit = unit;  // of the V tile that the step's P meets
             for (int j = 0; j < nkt; j++) {
                 const int gt = gq + j;
-                const uint32_t boxes_next = loaded(blk_next);
-                blk_next = table_entry(j + 2);
                 ok = __all_sync(FULL, mbar_wait(&s_full[tq], gt & 1));
                 if (!ok)
                     break;
                 tc::fence_after();
-                // the scales of the K tile's boxes (its stage's barrier orders them behind
-                // the producer's writes), then, S_t(j) being complete, the K tile, and
-                // after the item's last one Q, may go
-                const int sk = (g0 + j) % kSKStages;
-                if (!(ok = __all_sync(FULL, mbar_wait(&k_full[sk], ((g0 + j) / kSKStages) & 1))))
-                    break;
-                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
-                const bool equal = ks.equal != 0;
-                const float ks0 = ks.scale[0];
-                __syncwarp();
+                // S_t(j) has completed: its K tile, and after the item's last one its
+                // Q, is read
                 if (lane == 0) {
-                    mbar_arrive(&k_empty[sk]);
-                    if ((warp & 3) == 0 && j == nkt - 1)
+                    mbar_arrive(&k_empty[(g0 + j) % kSKStages]);
+                    if (j == nkt - 1)
                         mbar_arrive(&q_empty[tq]);
                 }
+                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
                 // one scale in the tile: it joins the row's; else every box's scores are
                 // multiplied by theirs
                 const float cs = equal ? sl * ks0 : sl;
@@ -754,11 +773,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mraw = fmaxf(mraw, top());
                 const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
                 const bool moves = __any_sync(FULL, mx > m + kLazy);
-                if (moves || unit != o_unit) {
+                if (moves || v_unit != o_unit) {
                     const float mn = moves ? fmaxf(m, mx) : m;
                     const float alpha = !moves || mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-                    const float o_alpha = unit == o_unit ? alpha : alpha * (o_unit / unit);
-                    o_unit = unit;
+                    const float o_alpha = v_unit == o_unit ? alpha : alpha * (o_unit / v_unit);
+                    o_unit = v_unit;
                     if (j > 0) {
                         // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1)
                         // completed, and the next P.V waits for this group's P
@@ -824,16 +843,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
                 hand_over(0);
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
-                if (j + 1 < all && !(ok = convert_v(j + 1, boxes_next)))
+                if (j + 1 < all && !(ok = convert_v(j + 1)))
                     break;
-                boxes = boxes_next;
+                if (j + 1 < nkt && !(ok = scales_k(j + 1)))
+                    break;
+                v_unit = unit;
             }
             if (!ok)
                 break;
             // V tiles that only the other query tile reads
             for (int jv = max(nkt, 1) + (nkt > 0 ? 1 : 0); ok && jv < all; jv++) {
-                const uint32_t bx = loaded(table_entry(jv));
-                ok = convert_v(jv, bx);
+                ok = convert_v(jv);
             }
             if (!ok)
                 break;

@@ -1210,6 +1210,8 @@ pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache,
                     (long long)N, Hkv, (long long)NB, bs);
     if (N > 0x7fffffffLL || Hkv > 65535)
         return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N must be < 2^31 and Hkv <= 65535");
+    if ((N + 15) / 16 * Hkv * 2 > 0x7fffffffLL)
+        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N*Hkv must be < 2^34");
     if (D != 64 && D != 128)
         return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: head_dim %d not in {64,128}", D);
     if (bs % pkv::kBox != 0)
@@ -1226,8 +1228,8 @@ pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache,
         !aligned16(k_scales) || !aligned16(v_scales) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: pointers must be 16-byte aligned");
     pkv::StoreScaledParams p;
-    p.x[0] = static_cast<const uint4 *>(k);
-    p.x[1] = static_cast<const uint4 *>(v);
+    p.x[0] = static_cast<const uint8_t *>(k);
+    p.x[1] = static_cast<const uint8_t *>(v);
     p.cache[0] = static_cast<uint8_t *>(k_cache);
     p.cache[1] = static_cast<uint8_t *>(v_cache);
     p.scales[0] = k_scales;
@@ -1238,6 +1240,7 @@ pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache,
     p.n_slots = (long long)NB * bs;
     p.Hkv = Hkv;
     p.bs = bs;
+    p.block = pkv::fast_div((uint32_t)bs);
     cudaError_t e = pkv::launch_store_scaled(D, p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(PKV_ERR_CUDA, "store_kvcache_scaled launch: %s", cudaGetErrorString(e));

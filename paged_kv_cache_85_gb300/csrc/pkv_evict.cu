@@ -48,11 +48,6 @@ constexpr int kSelBins = 2048;
 constexpr int kMoveThreads = 256;  // at most
 constexpr int kMoveDepth = 4;  // 16-byte loads per thread and tile; two tiles in flight
 
-__device__ __forceinline__ int divide(int n, FastDiv f)
-{
-    return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift);
-}
-
 // Weight -> 32-bit key, larger weight = larger key: NaN (any) above +inf, and
 // -0 equal to +0.
 __device__ __forceinline__ uint32_t weight_key(float w)

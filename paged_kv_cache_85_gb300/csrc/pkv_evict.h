@@ -22,6 +22,13 @@ inline FastDiv fast_div(uint32_t d)
     return {(uint32_t)((((1ull << l) - d) << 32) / d + 1), l, d};
 }
 
+#ifdef __CUDACC__
+__device__ __forceinline__ int divide(int n, FastDiv f)
+{
+    return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift);
+}
+#endif
+
 struct EvictParams {
     uint4 *k_cache, *v_cache;     // [NB, bs, Hkv, D], D elements = 16 * units bytes
     float *weights;               // [NB, Hkv, bs]

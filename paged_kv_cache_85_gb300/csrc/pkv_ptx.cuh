@@ -345,6 +345,14 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
     return r;
 }
 
+// Per half: a value whose magnitude is max(|a|, |b|) (a NaN loses; the sign carries nothing).
+__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -361,6 +369,15 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
         : "=l"(d)
         : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)),
           "l"(*reinterpret_cast<const uint64_t *>(&c)));
+    return *reinterpret_cast<const float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
     return *reinterpret_cast<const float2 *>(&d);
 }
 

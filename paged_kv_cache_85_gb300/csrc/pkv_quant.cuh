@@ -20,6 +20,14 @@ __device__ __forceinline__ uint2 quantize8(uint4 a, float inv)
     return make_uint2(c0 | (c1 << 16), c2 | (c3 << 16));
 }
 
+// Four bf16 values alike (4 codes).
+__device__ __forceinline__ uint32_t quantize4(uint32_t a, uint32_t b, float inv)
+{
+    const float2 f2 = make_float2(inv, inv);
+    const float2 x = fmul2(bf16x2_to_float2(a), f2), y = fmul2(bf16x2_to_float2(b), f2);
+    return f32x2_to_e4m3x2(x.x, x.y) | (f32x2_to_e4m3x2(y.x, y.y) << 16);
+}
+
 // Four codes as the codes of their values times f.
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float f)
 {

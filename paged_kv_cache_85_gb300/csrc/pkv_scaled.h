@@ -7,16 +7,19 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "pkv_evict.h"
+
 namespace pkv {
 
 struct StoreScaledParams {
-    const uint4 *x[2];        // K and V rows, bf16 [N, Hkv, D]
+    const uint8_t *x[2];      // K and V rows, bf16 [N, Hkv, D]
     uint8_t *cache[2];        // E4M3 [NB, bs, Hkv, D]
     float *scales[2];         // [NB, Hkv]
     const int64_t *slots;     // [N]
     int32_t *err_flag;        // nullable
     long long N, n_slots;     // n_slots = NB * bs < 2^31
     int Hkv, bs;
+    FastDiv block;            // division by bs
 };
 
 cudaError_t launch_store_scaled(int D, const StoreScaledParams &p, cudaStream_t stream);

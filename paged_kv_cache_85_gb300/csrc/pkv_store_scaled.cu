@@ -13,11 +13,10 @@
 // Codes: e4m3(x * (1 / s')), exact products where s' is a power of two.
 //
 // How.  A block's tokens follow each other in slot_mapping (a run).  One CTA takes the
-// runs that start in a window of T tokens, for one KV head and K or V: it keeps the
-// rows that it reads (256 of them at most; later ones of a run are read again, from
-// L2) in registers, takes each run's maximum in shared memory, and writes.  So every
-// row is read once and written once, and the scale needs no second kernel and no
-// workspace.  Bound by HBM (6 D bytes per token and head).
+// runs that start in a window of T tokens, for one KV head and K or V: it keeps a
+// batch of the rows that it reads in registers (those before the last batch are read
+// again, from L2), takes each run's maximum in shared memory, and writes.  So the
+// scale needs no second kernel and no workspace.  Bound by HBM (6 D bytes per token and head).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 #include "pkv_quant.cuh"
@@ -28,18 +27,39 @@ namespace pkv {
 constexpr int kSsThreads = 256;
 constexpr int kScaleLow = -40, kScaleHigh = 40;
 
-// Bits of the largest finite magnitude of eight bf16 values (0 where there is none).
-__device__ __forceinline__ uint32_t finite_max8(uint4 w)
+// Sixteen bf16 values.
+struct Row16 {
+    uint32_t w[8];
+};
+
+__device__ __forceinline__ Row16 load16(const uint8_t *p, bool aligned32)
 {
-    constexpr uint32_t ABS = 0x7fff7fffu;
-    uint32_t m = bf16x2_max(bf16x2_max(w.x & ABS, w.y & ABS), bf16x2_max(w.z & ABS, w.w & ABS));
+    Row16 r;
+    if (!aligned32) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+        return r;
+    }
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]),
+                   "=r"(r.w[6]), "=r"(r.w[7])
+                 : "l"(p));
+    return r;
+}
+
+// Bits of the largest finite magnitude (0 where there is none).
+__device__ __forceinline__ uint32_t finite_max16(const Row16 &r)
+{
+    uint32_t m = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(r.w[0], r.w[1]), bf16x2_absmax(r.w[2], r.w[3])),
+                               bf16x2_absmax(bf16x2_absmax(r.w[4], r.w[5]), bf16x2_absmax(r.w[6], r.w[7]))) &
+                 0x7fff7fffu;
     m = max(m & 0xffffu, m >> 16);
-    if (m >= 0x7f80u) {  // infinities, or nothing but NaN in a place of all four
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    if (m >= 0x7f80u) {  // infinities, or nothing but NaN in a place of all eight
         m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
+        for (int i = 0; i < 8; i++) {
+            const uint32_t lo = r.w[i] & 0x7fffu, hi = (r.w[i] >> 16) & 0x7fffu;
             m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
         }
     }
@@ -55,58 +75,81 @@ __device__ __forceinline__ float scale_for(uint32_t m)
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// T: tokens per window.  HOLD: row loads a thread keeps.
-template <int D, int T, int HOLD>
+// T: tokens per window.  SEEN: tokens from the window's first on whose slots are looked
+// at at once.  HOLD: row loads a thread has in flight and keeps.
+template <int D, int T, int SEEN, int HOLD>
 __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreScaledParams p)
 {
-    constexpr int LPR = D / 8;              // lanes per row (16-byte loads)
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int LPR = D / 16;             // lanes per row (32-byte loads)
     constexpr int RPP = kSsThreads / LPR;   // rows per pass
-    static_assert(T <= kSsThreads - 1, "one thread per token of the window and one beyond");
-    __shared__ int s_run[T];                // run of each token of the window, -1: none that starts here
+    constexpr int BATCH = HOLD * RPP;       // rows kept
+    constexpr int PER = SEEN / kSsThreads;  // slots per thread
+    constexpr int WARPS = kSsThreads / 32;
+    static_assert(SEEN % kSsThreads == 0 && T <= kSsThreads && T < SEEN && T % 16 == 0, "window");
+    __shared__ int s_slot[SEEN + 1], s_of[SEEN + 1];  // slot and block of tokens w0 - 1, w0, ...; -1: none
+    __shared__ short s_run[SEEN];           // run of each token, -1: none that starts here
+    __shared__ uint32_t s_start[WARPS], s_goes[SEEN / 32];  // a bit per token
     __shared__ int s_blk[T];
     __shared__ uint32_t s_max[T], s_begun[T];
     __shared__ float s_inv[T], s_ratio[T];
     __shared__ int s_grown[T];
-    __shared__ uint32_t s_starts[kSsThreads / 32];
-    __shared__ int s_more, s_n_grown;
+    __shared__ int s_n_grown;
     __shared__ long long s_end;
 
     grid_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.y, z = blockIdx.z;
-    const long long w0 = (long long)blockIdx.x * T;
+    // K and V, then heads, then windows: CTAs that run together read the same rows
+    const int z = blockIdx.x & 1, h = (int)((blockIdx.x >> 1) % (uint32_t)p.Hkv);
+    const long long w0 = (long long)((blockIdx.x >> 1) / (uint32_t)p.Hkv) * T;
     const uint32_t bs = (uint32_t)p.bs;
 
-    // ---- the window's runs
-    const auto slot_at = [&](long long i) -> long long { return i >= 0 && i < p.N ? __ldg(p.slots + i) : -1; };
-    const auto block_of = [&](long long s) -> int {
-        return s >= 0 && s < p.n_slots ? (int)((uint32_t)s / bs) : -1;
-    };
-    long long slot = -1;
-    int blk = -1;
-    bool start = false;
-    if (tid <= T) {
-        slot = slot_at(w0 + tid);
-        blk = block_of(slot);
-        const bool follows = blk >= 0 && block_of(slot_at(w0 + tid - 1)) == blk;
-        start = tid < T && blk >= 0 && !follows;
-        if (tid == T)
-            s_more = follows;  // the last run goes on behind the window
-        else if (slot != -1 && blk < 0 && h == 0 && z == 0)
+    // ---- the window's runs: a token starts one unless the token before it lies in its block
+    const auto slot_at = [&](long long i) -> int {
+        const long long s = i >= 0 && i < p.N ? __ldg(p.slots + i) : -1;
+        if (s >= 0 && s < p.n_slots)
+            return (int)s;
+        if (s != -1 && h == 0 && z == 0)
             flag_error(p.err_flag, 0x1 /* PKV_FLAG_BAD_SLOT */);
+        return -1;
+    };
+    const auto block_of = [&](int s) { return s >= 0 ? divide(s, p.block) : -1; };
+    int slots[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        slots[i] = slot_at(w0 + i * kSsThreads + tid);
+    if (tid == 0) {
+        s_of[0] = block_of(slot_at(w0 - 1));
+        s_n_grown = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        s_slot[1 + i * kSsThreads + tid] = slots[i];
+        s_of[1 + i * kSsThreads + tid] = block_of(slots[i]);
     }
     if (tid < T)
         s_max[tid] = s_begun[tid] = 0;
-    if (tid == 0)
-        s_n_grown = 0;
-    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    __syncthreads();
+    const int slot = slots[0], blk = s_of[1 + tid];
+    bool start = false;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int t = i * kSsThreads + tid;
+        const bool follows = s_of[t + 1] >= 0 && s_of[t] == s_of[t + 1];
+        if (i == 0)
+            start = tid < T && slot >= 0 && !follows;
+        const uint32_t goes = __ballot_sync(FULL, follows);
+        if (lane == 0)
+            s_goes[t >> 5] = goes;
+    }
+    const uint32_t starts = __ballot_sync(FULL, start);
     if (lane == 0)
-        s_starts[warp] = starts;
+        s_start[warp] = starts;
     __syncthreads();
     int before = 0, n_runs = 0, first = T;
 #pragma unroll
     for (int i = 0; i < (T + 31) / 32; i++) {
-        const uint32_t s = s_starts[i];
+        const uint32_t s = s_start[i];
         before += i < warp ? __popc(s) : 0;
         n_runs += __popc(s);
         if (s && first == T)
@@ -117,23 +160,41 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
         grid_dependency_wait();
         return;
     }
+    // how far the last run goes on behind the window, of what is seen
+    int end = T;
+#pragma unroll
+    for (int i = T / 32; i < SEEN / 32; i++) {
+        const int from = max(0, T - 32 * i);
+        const uint32_t stops = ~s_goes[i] & (FULL << from);
+        if (end == 32 * i + from)
+            end = stops ? 32 * i + __ffs(stops) - 1 : 32 * i + 32;
+    }
     if (tid < T) {
-        const int run = blk >= 0 ? before + __popc(starts & (0xffffffffu >> (31 - lane))) - 1 : -1;
-        s_run[tid] = run;
+        const int run = slot >= 0 ? before + __popc(starts & (FULL >> (31 - lane))) - 1 : -1;
+        s_run[tid] = (short)run;
         if (start)
             s_blk[run] = blk;
-        if (run >= 0 && (uint32_t)slot % bs == 0)
+        if (run >= 0 && (uint32_t)slot == (uint32_t)blk * bs)
             s_begun[run] = 1;
     }
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int t = i * kSsThreads + tid;
+        if (t >= T) {
+            s_run[t] = (short)(n_runs - 1);
+            if (t < end && (uint32_t)slots[i] == (uint32_t)s_of[t + 1] * bs)
+                s_begun[n_runs - 1] = 1;
+        }
+    }
     if (tid == 0)
-        s_end = w0 + T < p.N ? w0 + T : p.N;
-    __syncthreads();
-    if (s_more) {  // (the token behind the window lies in the last run's block)
-        const int last = s_blk[n_runs - 1];
-        for (long long i = w0 + T + tid;; i += kSsThreads) {
-            const long long s = slot_at(i);
+        s_end = min(w0 + end, p.N);
+    if (end == SEEN) {  // and beyond
+        __syncthreads();
+        const int last = s_of[SEEN];
+        for (long long i = w0 + SEEN + tid;; i += kSsThreads) {
+            const int s = slot_at(i);
             const bool mine = block_of(s) == last;
-            if (mine && (uint32_t)s % bs == 0)
+            if (mine && (uint32_t)s == (uint32_t)last * bs)
                 s_begun[n_runs - 1] = 1;
             const int other = __syncthreads_or(!mine);
             if (other) {
@@ -145,53 +206,79 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
                 break;
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
 
     // ---- each run's largest magnitude; row i is token w0 + first + i
     const long long row0 = w0 + first;
-    const long long rows = s_end - row0;
+    const int rows = (int)(s_end - row0);
     const int sub = tid / LPR, part = tid % LPR;
-    const auto run_of = [&](long long i) { return first + i < T ? s_run[first + i] : n_runs - 1; };
-    const uint4 *src = (z ? p.x[1] : p.x[0]) + (row0 * p.Hkv + h) * LPR + part;
-    const size_t stride = (size_t)p.Hkv * LPR;
-    uint4 held[HOLD];
+    const auto run_of = [&](int i) { return first + i < SEEN ? (int)s_run[first + i] : n_runs - 1; };
+    const size_t stride = (size_t)p.Hkv * D * 2;
+    const uint8_t *src = (z ? p.x[1] : p.x[0]) + (row0 + sub) * stride + (size_t)h * D * 2 + part * 32;
+    const bool aligned32 = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;  // of all or none
+    Row16 held[HOLD];
+    const auto load = [&](int b0) {
 #pragma unroll
-    for (int u = 0; u < HOLD; u++) {
-        const long long i = u * RPP + sub;
-        held[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < rows)
-            held[u] = __ldg(src + i * stride);
-    }
-    const auto note = [&](uint4 w, long long i) {  // by all lanes of a warp
-        uint32_t m = finite_max8(w);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1)
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (part == 0 && i < rows) {
-            const int run = run_of(i);
-            if (run >= 0)
-                atomicMax(&s_max[run], m);
+        for (int u = 0; u < HOLD; u++) {
+            held[u] = Row16{};
+            if (b0 + u * RPP + sub < rows)
+                held[u] = load16(src + (size_t)(b0 + u * RPP) * stride, aligned32);
         }
     };
+    load(0);
+    // (earlier kernels may still read the cache, or have written the scales)
+    grid_dependency_wait();
+    float *scale_at = nullptr;
+    float had = 0.f;
+    if (tid < n_runs) {
+        scale_at = (z ? p.scales[1] : p.scales[0]) + (size_t)s_blk[tid] * p.Hkv + h;
+        had = ld_gpu(scale_at);
+    }
+    // a thread's rows ascend, and so do their runs: it gathers while the run stays
+    uint32_t top = 0;
+    int of = -1;
+    const auto flush = [&]() {  // by all lanes of a warp
+        const int lead = __shfl_sync(FULL, of, 0);
+        if (__all_sync(FULL, of == lead)) {
+            const uint32_t m = __reduce_max_sync(FULL, top);
+            if (lane == 0 && of >= 0)
+                atomicMax(&s_max[of], m);
+        } else if (of >= 0) {
+            atomicMax(&s_max[of], top);
+        }
+    };
+    int b0 = 0;
+    for (;;) {
 #pragma unroll
-    for (int u = 0; u < HOLD; u++)
-        if (u * RPP < rows)
-            note(held[u], u * RPP + sub);
-    for (long long i0 = HOLD * RPP; i0 < rows; i0 += RPP)
-        note(i0 + sub < rows ? __ldg(src + (i0 + sub) * stride) : make_uint4(0u, 0u, 0u, 0u), i0 + sub);
-    grid_dependency_wait();  // earlier kernels may still read the cache, or have written the scales
+        for (int u = 0; u < HOLD; u++) {
+            const int i = b0 + u * RPP;
+            if (i >= rows)
+                break;
+            const int run = i + sub < rows ? run_of(i + sub) : of;  // (behind the last row: zeros)
+            if (__any_sync(FULL, run != of)) {
+                flush();
+                top = 0;
+                of = run;
+            }
+            top = max(top, finite_max16(held[u]));
+        }
+        if (b0 + BATCH >= rows)
+            break;
+        b0 += BATCH;
+        load(b0);
+    }
+    flush();
     __syncthreads();
 
     // ---- the scales
     if (tid < n_runs) {
-        float *at = (z ? p.scales[1] : p.scales[0]) + (size_t)s_blk[tid] * p.Hkv + h;
-        const float had = ld_gpu(at), want = scale_for(s_max[tid]);
+        const float want = scale_for(s_max[tid]);
         const bool keep = !s_begun[tid] && had > 0.f && had < INFINITY;
         const float now = keep ? fmaxf(had, want) : want;
         s_inv[tid] = __frcp_rn(now);
         if (!keep || now != had)
-            *at = now;
+            *scale_at = now;
         if (keep && now != had) {
             s_ratio[tid] = __fdiv_rn(had, now);
             s_grown[atomicAdd(&s_n_grown, 1)] = tid;
@@ -218,20 +305,28 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
         __syncthreads();  // before rows of the same blocks are written over it
     }
 
-    // ---- the rows
-    const auto put = [&](uint4 w, long long i) {
-        const int run = run_of(i);
-        if (run < 0)
-            return;
-        const long long s = __ldg(p.slots + row0 + i);
-        *reinterpret_cast<uint2 *>(cache + ((size_t)s * p.Hkv + h) * D + part * 8) = quantize8(w, s_inv[run]);
-    };
+    // ---- the rows, the batch that is held first
+    cache += (size_t)h * D + part * 16;
+    const size_t token = (size_t)p.Hkv * D;
+    for (;;) {
 #pragma unroll
-    for (int u = 0; u < HOLD; u++)
-        if (u * RPP + sub < rows)
-            put(held[u], u * RPP + sub);
-    for (long long i = HOLD * RPP + sub; i < rows; i += RPP)
-        put(__ldg(src + i * stride), i);
+        for (int u = 0; u < HOLD; u++) {
+            const int i = b0 + u * RPP + sub;
+            const int run = i < rows ? run_of(i) : -1;
+            if (run >= 0) {
+                const int s = first + i < SEEN ? s_slot[1 + first + i] : (int)__ldg(p.slots + row0 + i);
+                const uint32_t *w = held[u].w;
+                const float inv = s_inv[run];
+                *reinterpret_cast<uint4 *>(cache + (size_t)(uint32_t)s * token) =
+                    make_uint4(quantize4(w[0], w[1], inv), quantize4(w[2], w[3], inv), quantize4(w[4], w[5], inv),
+                               quantize4(w[6], w[7], inv));
+            }
+        }
+        if (b0 == 0)
+            break;
+        b0 -= BATCH;
+        load(b0);
+    }
 }
 
 template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStream_t stream)
@@ -244,13 +339,13 @@ template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStrea
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((p.N + T - 1) / T), (unsigned)p.Hkv, 2);
+    cfg.gridDim = dim3((unsigned)((p.N + T - 1) / T * p.Hkv * 2));
     cfg.blockDim = dim3(kSsThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 16, 2>, p)
-               : cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 128, D / 8>, p);
+    return few ? cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 16, 256, 1>, p)
+               : cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 128, 512, D / 32>, p);
 }
 
 cudaError_t launch_store_scaled(int D, const StoreScaledParams &p, cudaStream_t stream)

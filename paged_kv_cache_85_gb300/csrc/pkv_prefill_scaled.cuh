@@ -34,29 +34,26 @@ constexpr int kSKStages = 2;    // K ring: codes
 constexpr int kSRStages = 2;    // V ring: codes
 constexpr int kSVStages = 3;    // V as f16: one more than a tile's P.V of both query tiles needs
                                 // (with two, a query tile that is ahead waits for the other)
-// Tiles whose boxes' scales are kept: twice the stages, so that they may be read until
-// the warp arrives for the tile after the next, which is when the producer goes on.
+// Tiles whose scales are kept: a tile's are read (K's) until the warp has its P, by which
+// time it has not yet taken the V codes of the tile after the next; the producer goes on
+// to a fourth after that.
 constexpr int kSScales = 4;
-static_assert(kSScales >= 2 * kSKStages && kSScales >= 2 * kSRStages, "a tile's scales outlive its stage");
+static_assert(kSScales >= kSRStages + 2, "a tile's scales outlive its stage");
 // q_full[2], q_conv[2], q_empty[2], k_full, k_empty [kSKStages] each, r_full, r_empty
 // [kSRStages] each, v_conv, v_empty [kSVStages] each, per query tile s_full,
 // pv_ready[2 halves], pv_done, o_free, then item_ready[2], item_free[2], mma_done
 constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
 
-// The scales of a tile's eight boxes, and which of them are read (a bit each).
-// K: equal says that all scales are scale[0] (boxes that are not read count as any).
-// V: scale over unit as a pair of f16 in `factor`; O is held in `unit`.
-struct __align__(16) BoxScales {
-    union {
-        float scale[kSKeys / kBox];
-        uint32_t factor[kSKeys / kBox];
-    };
-    int read;
-    union {
-        int equal;
-        float unit;
-    };
-    int pad[2];
+// What the softmax warps need of a key tile beside its codes; the producer brings it with
+// V's.  read: which of the eight boxes are read (a bit each).  k: their K scales, where
+// they are not read one that is; equal: all are k[0].  v: V's scales over `unit`, in which
+// O is held, as pairs of f16.
+struct __align__(16) TileScales {
+    float k[kSKeys / kBox];
+    uint32_t v[kSKeys / kBox];
+    int read, equal;
+    float unit;
+    int pad;
 };
 
 struct ScaledSmem {
@@ -75,8 +72,8 @@ __host__ __device__ inline ScaledSmem scaled_smem_layout(int D)
     o += (size_t)kSRStages * kSKeys * D;
     L.v = o;  // stages of [D/64 halves][128 keys][128 B]
     o += (size_t)kSVStages * (D / 64) * kSKeys * 128;
-    L.scales = o;  // of the last kSScales K tiles, then of V tiles
-    o += 2 * kSScales * sizeof(BoxScales);
+    L.scales = o;  // of the last kSScales tiles
+    o += kSScales * sizeof(TileScales);
     L.bars = o;
     o += 8 * kSBars;
     L.items = align_up(o, 16);  // two published work items
@@ -146,7 +143,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const Turn turn{slot + 1};
     WideItem *items = reinterpret_cast<WideItem *>(smem + L.items);
     uint8_t *sQ = smem + L.q, *sK = smem + L.k, *sR = smem + L.r, *sV = smem + L.v;
-    BoxScales *k_scales = reinterpret_cast<BoxScales *>(smem + L.scales), *v_scales = k_scales + kSScales;
+    TileScales *scales = reinterpret_cast<TileScales *>(smem + L.scales);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
@@ -268,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // ---- publish it in slot n & 1, once the item two back is done with it
             const int sl = n & 1;
-            if (n >= 2 && !(ok = ok && __all_sync(FULL, mbar_wait(&item_free[sl], ((n >> 1) & 1) ^ 1))))
+            if (n >= 2 && !(ok = ok && __all_sync(FULL, mbar_wait_asleep(&item_free[sl], ((n >> 1) & 1) ^ 1))))
                 break;  // the other warps time out on item_ready and stop
             if (!ok)
                 it.b = -1;
@@ -283,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int t = 0; t < 2 && ok; t++) {
                 if (it.nkt[t] == 0)
                     continue;
-                if (n >= 1 && !(ok = __all_sync(FULL, mbar_wait(&q_empty[t], (n - 1) & 1))))
+                if (n >= 1 && !(ok = __all_sync(FULL, mbar_wait_asleep(&q_empty[t], (n - 1) & 1))))
                     break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full[t], HALVES * kQHalf);
@@ -297,9 +294,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok)
                 break;
             n++;
-            // ---- K and V tiles through the two rings: whichever can go.  Lanes 0-7
-            // resolve one 16-token box each: its block two tiles ahead of the copy, the
-            // block's scale one tile ahead.
+            // ---- K and V tiles through their rings, in the order in which stages come free.
+            // Lanes 0-7 resolve one 16-token box each: its block two tiles ahead of the
+            // copies, the block's scales one tile ahead.
             const int nkt = max(it.nkt[0], it.nkt[1]);
             const int j0 = SPLIT ? item.j0 : 0;
             const int32_t *table = p.block_tables + (size_t)it.b * p.MBS;
@@ -308,29 +305,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 return (lane < kBoxes && j < nkt && key0 < it.k_len) ? __ldg(table + key0 / p.bs) : -1;
             };
             // (written by the store, maybe while this kernel was starting)
-            auto scale_of = [&](const float *scales, int blk) {
-                return blk >= 0 && blk < p.NB ? ld_gpu(scales + (size_t)blk * p.Hkv + it.kvh) : 0.f;
+            auto scale_of = [&](const float *scales_of, int blk) {
+                return blk >= 0 && blk < p.NB ? ld_gpu(scales_of + (size_t)blk * p.Hkv + it.kvh) : 0.f;
             };
-            int blk_k = entry(0), next_k = entry(1), blk_v = blk_k, next_v = next_k;
-            float sc_k = scale_of(p.k_scales, blk_k), sc_v = scale_of(p.v_scales, blk_v);
+            int blk = entry(0), blk_next = entry(1);
+            float sk = scale_of(p.k_scales, blk), sv = scale_of(p.v_scales, blk);
+            const int per = p.copy_rows;  // tokens per copy: so many lie in one block
             // V tiles' unit: moves to a tile's largest scale where that is 2^7 above it
             // (448 * 2^7 is within f16) or 2^8 below (where f16 begins to lose bits)
             float unit = 1.f, per_unit = 1.f;
-            const int per = p.copy_rows;  // tokens per copy: so many lie in one block
-            auto issue = [&](int j, int g, bool is_k) {
-                uint64_t *fb = is_k ? k_full : r_full;
-                const int s = g % (is_k ? kSKStages : kSRStages);
-                const int blk = is_k ? blk_k : blk_v;
-                float sc = is_k ? sc_k : sc_v;
-                if (is_k) {
-                    blk_k = next_k;
-                    sc_k = scale_of(p.k_scales, blk_k);
-                    next_k = entry(j + 2);
-                } else {
-                    blk_v = next_v;
-                    sc_v = scale_of(p.v_scales, blk_v);
-                    next_v = entry(j + 2);
-                }
+            for (int j = 0; j < nkt; j++) {
                 const int key0 = (j0 + j) * kSKeys + lane * kBox;
                 int row = -1;
                 if (lane < kBoxes && key0 < it.k_len) {
@@ -339,73 +323,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     else
                         flag_error(p.err_flag, 0x2 /* PKV_FLAG_BAD_BLOCK */);
                 }
-                // the boxes' scales: of K one stands in for those that are not read
                 const uint32_t read = __ballot_sync(FULL, row >= 0);
-                BoxScales &bx = (is_k ? k_scales : v_scales)[g % kSScales];
-                if (is_k) {
-                    const float first = __shfl_sync(FULL, sc, read ? __ffs(read) - 1 : 0);
-                    if (row < 0)
-                        sc = read ? first : 1.f;
-                    const bool equal = __all_sync(FULL, lane >= kBoxes || sc == (read ? first : 1.f));
-                    if (lane < kBoxes)
-                        bx.scale[lane] = sc;
-                    if (lane == 0)
-                        bx.equal = equal;
-                } else {
-                    const float most = __uint_as_float(__reduce_max_sync(
-                        FULL, row >= 0 && sc > 0.f && sc < INFINITY ? __float_as_uint(sc) : 0u));
-                    if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f)) {
-                        unit = most;
-                        per_unit = 1.f / most;
-                    }
-                    if (lane < kBoxes)
-                        bx.factor[lane] = pack_f16x2(sc * per_unit, sc * per_unit);
-                    if (lane == 0)
-                        bx.unit = unit;
+                const float first = read ? __shfl_sync(FULL, sk, __ffs(read) - 1) : 1.f;
+                const float k = row >= 0 ? sk : first;
+                const bool equal = __all_sync(FULL, lane >= kBoxes || k == first);
+                const float most = __uint_as_float(__reduce_max_sync(
+                    FULL, row >= 0 && sv > 0.f && sv < INFINITY ? __float_as_uint(sv) : 0u));
+                if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f)) {
+                    unit = most;
+                    per_unit = 1.f / most;
                 }
-                if (lane == 0)
-                    bx.read = (int)read;
+                const uint32_t factor = pack_f16x2(sv * per_unit, sv * per_unit);
+                // the next tile's, whose loads run while this one's stages are waited for
+                blk = blk_next;
+                sk = scale_of(p.k_scales, blk);
+                sv = scale_of(p.v_scales, blk);
+                blk_next = entry(j + 2);
                 // rows past k_len of a run come along: their scores are masked and
                 // their V rows zeroed
                 const bool copies = row >= 0 && (lane * kBox) % per == 0;
-                const uint32_t mask = __ballot_sync(FULL, copies);
-                __syncwarp();
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL, copies)) * per * D;
+                const int at = lane * (kBox * D);
+                const int rs = gv % kSRStages, vs = gv % kSVStages, ks = gk % kSKStages;
+                ok = __all_sync(FULL, mbar_wait_asleep(&k_empty[ks], ((gk / kSKStages) & 1) ^ 1));
+                if (!ok)
+                    break;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&fb[s], (uint32_t)__popc(mask) * per * D);
+                    mbar_arrive_expect_tx(&k_full[ks], bytes);
                 __syncwarp();
                 if (copies)
-                    tma_load_3d((is_k ? sK : sR) + (size_t)s * kTile + lane * (kBox * D), is_k ? &tmk : &tmv,
-                                0, it.kvh, row, &fb[s]);
-            };
-            int jk = 0, jv = 0;
-            uint64_t t_last = sm_clock();
-            while (jk < nkt || jv < nkt) {
-                bool prog = false;
-                if (jk < nkt) {
-                    const bool free_k = tc::test_wait(smem_u32(&k_empty[gk % kSKStages]),
-                                                      ((gk / kSKStages) & 1) ^ 1);
-                    if (__shfl_sync(FULL, free_k, 0)) {
-                        issue(jk++, gk++, true);
-                        prog = true;
-                    }
+                    tma_load_3d(sK + (size_t)ks * kTile + at, &tmk, 0, it.kvh, row, &k_full[ks]);
+                gk++;
+                // V: its codes' stage, and the f16 buffer that they go to, so that the
+                // softmax warps wait for the codes alone
+                ok = __all_sync(FULL, mbar_wait_asleep(&r_empty[rs], ((gv / kSRStages) & 1) ^ 1) &&
+                                          mbar_wait_asleep(&v_empty[vs], ((gv / kSVStages) & 1) ^ 1));
+                if (!ok)
+                    break;
+                TileScales &ts = scales[gv % kSScales];
+                if (lane < kBoxes) {
+                    ts.k[lane] = k;
+                    ts.v[lane] = factor;
                 }
-                if (jv < jk) {
-                    const bool free_v = tc::test_wait(smem_u32(&r_empty[gv % kSRStages]),
-                                                      ((gv / kSRStages) & 1) ^ 1);
-                    if (__shfl_sync(FULL, free_v, 0)) {
-                        issue(jv++, gv++, false);
-                        prog = true;
-                    }
+                if (lane == 0) {
+                    ts.read = (int)read;
+                    ts.equal = equal;
+                    ts.unit = unit;
                 }
-                if (prog) {
-                    t_last = sm_clock();
-                } else {
-                    __nanosleep(32);
-                    if (__shfl_sync(FULL, sm_clock() - t_last > kPollLimitCycles, 0)) {
-                        ok = false;
-                        break;
-                    }
-                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&r_full[rs], bytes);
+                __syncwarp();
+                if (copies)
+                    tma_load_3d(sR + (size_t)rs * kTile + at, &tmv, 0, it.kvh, row, &r_full[rs]);
+                gv++;
             }
             if (!ok)
                 break;  // the other warps time out on their barriers and stop
@@ -416,11 +387,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // copies still in flight land before the CTA may exit
             for (int t = 0; t < 2; t++)
                 if (q_loads[t] >= 1)
-                    mbar_wait(&q_full[t], (q_loads[t] - 1) & 1);
+                    mbar_wait_asleep(&q_full[t], (q_loads[t] - 1) & 1);
             for (int g = max(0, gk - kSKStages); g < gk; g++)
-                mbar_wait(&k_full[g % kSKStages], (g / kSKStages) & 1);
+                mbar_wait_asleep(&k_full[g % kSKStages], (g / kSKStages) & 1);
             for (int g = max(0, gv - kSRStages); g < gv; g++)
-                mbar_wait(&r_full[g % kSRStages], (g / kSRStages) & 1);
+                mbar_wait_asleep(&r_full[g % kSRStages], (g / kSRStages) & 1);
         }
         __syncwarp();
     } else if (warp == kTcMmaWarp || warp == kTcMmaWarp + 1) {
@@ -451,14 +422,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int gq = 0;    // S/P tiles of this query tile so far
             int used = 0;  // items in which this query tile had work
             for (int n = 0; ok; n++) {
-                if (!(ok = mbar_wait(&item_ready[n & 1], (n >> 1) & 1)))
+                if (!(ok = mbar_wait_asleep(&item_ready[n & 1], (n >> 1) & 1)))
                     break;
                 const PrefillItem it = items[n & 1].f;
                 if (it.b < 0)
                     break;
                 const int nk = it.nkt[t];
                 const int nkt = max(it.nkt[0], it.nkt[1]);
-                if (nk > 0 && !(ok = mbar_wait(&q_conv[t], used & 1)))
+                if (nk > 0 && !(ok = mbar_wait_asleep(&q_conv[t], used & 1)))
                     break;
                 tc::fence_after();
                 for (int w = 0; nk == 0 && w < 4; w++)  // this tile reads no Q this item
@@ -479,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc::commit(smem_u32(&s_full[t]));
                 };
                 auto landed = [&](int j) {
-                    return mbar_wait(&k_full[(g0 + j) % kSKStages], ((g0 + j) / kSKStages) & 1);
+                    return mbar_wait_asleep(&k_full[(g0 + j) % kSKStages], ((g0 + j) / kSKStages) & 1);
                 };
                 if (nk > 0) {
                     // the buffer is free: this warp saw the previous item's last P.V complete
@@ -493,11 +464,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // nothing is waited for that the other warp may owe while the turn is
                     // held, K tile j + 1 landed
                     const int s = (g0 + j) % kSVStages;
-                    if (!(ok = mbar_wait(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
+                    if (!(ok = mbar_wait_asleep(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
                         break;
                     // the item's first P.V overwrites O: the tile's previous epilogue
                     // must have read it out
-                    if (j == 0 && used >= 1 && !(ok = mbar_wait(&o_free[t], (used - 1) & 1)))
+                    if (j == 0 && used >= 1 && !(ok = mbar_wait_asleep(&o_free[t], (used - 1) & 1)))
                         break;
                     if (j + 1 < nk && !(ok = landed(j + 1)))
                         break;
@@ -514,16 +485,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                        (add || i > 0) ? 1u : 0u);
                         }
                     };
-                    if (!(ok = mbar_wait(&pv_ready[2 + t], gq & 1)) || !(ok = turn.take()))
+                    if (!(ok = mbar_wait_asleep(&pv_ready[2 + t], gq & 1)) || !(ok = turn.take()))
                         break;
                     pv(1, j > 0);
                     turn.pass();
-                    if (!(ok = mbar_wait(&pv_ready[t], gq & 1)) || !(ok = turn.take()))
+                    if (!(ok = mbar_wait_asleep(&pv_ready[t], gq & 1)) || !(ok = turn.take()))
                         break;
                     pv(0, true);
                     tc::commit(smem_u32(&pv_done[t]));
                     // S_t(j + 1) overwrites P_t(j)
-                    ok = mbar_wait(&pv_done[t], gq & 1);
+                    ok = mbar_wait_asleep(&pv_done[t], gq & 1);
                     gq++;
                     if (ok) {
                         mbar_arrive(&v_empty[s]);
@@ -541,7 +512,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         break;
                     for (int w = 0; w < 4; w++)  // for its softmax warps
                         mbar_arrive(&k_empty[(g0 + j) % kSKStages]);
-                    if (!(ok = mbar_wait(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
+                    if (!(ok = mbar_wait_asleep(&v_conv[s], ((g0 + j) / kSVStages) & 1)))
                         break;
                     mbar_arrive(&v_empty[s]);
                 }
@@ -556,7 +527,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::commit(smem_u32(mma_done));  // every MMA completes before TMEM is released
         }
         __syncwarp();
-        mbar_wait(mma_done, 0);
+        mbar_wait_asleep(mma_done, 0);
         __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax
@@ -580,7 +551,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int conv_to0 = conv_line + 16 * ((2 * (conv_col & 3)) ^ (conv_row & 7));
         const int conv_to1 = conv_line + 16 * ((2 * (conv_col & 3) + 1) ^ (conv_row & 7));
         for (int n = 0; ok; n++) {
-            ok = __all_sync(FULL, mbar_wait(&item_ready[n & 1], (n >> 1) & 1));
+            ok = __all_sync(FULL, mbar_wait_asleep(&item_ready[n & 1], (n >> 1) & 1));
             if (!ok)
                 break;
             const WideItem item = items[n & 1];
@@ -594,34 +565,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int pos = (it.k_len - it.q_len) + tok;
             const int k_len = it.k_len;
             float m = -INFINITY, l = 0.f;
-            float unit = 1.f;   // of the V tiles so far: V = unit * f16
-            float o_unit = 1.f; // of O
-            // This group's half (64 keys) of V tile j: codes -> f16 in the other buffer,
-            // times their box's factor, rows past k_len or of boxes that are not read
-            // zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups take part
-            // in every V tile of the item, in order.
+            // of the next key tile's codes, and of O
+            float unit = 1.f, o_unit = 1.f;
+            // K's scales of the next key tile: equal ones are ks0
+            bool equal = true;
+            float ks0 = 1.f;
+            uint32_t boxes = 0;
+            // Key tile j's scales, and this group's half (64 keys) of its V: codes -> f16 in
+            // the other buffer, times their box's factor, rows past k_len or of boxes that
+            // are not read zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups
+            // take part in every tile of the item, in order.
             auto convert_v = [&](int j) -> bool {
                 const int gv = g0 + j, s = gv % kSRStages, b = gv % kSVStages, kb = (j0 + j) * kSKeys;
-                if (!__all_sync(FULL, mbar_wait(&r_full[s], (gv / kSRStages) & 1)))
+                if (!__all_sync(FULL, mbar_wait_asleep(&r_full[s], (gv / kSRStages) & 1)))
                     return false;
                 const uint8_t *vr = sR + (size_t)s * kTile + conv_from;
                 uint4 w[kConvPieces];
 #pragma unroll
                 for (int u = 0; u < kConvPieces; u++)
                     w[u] = *reinterpret_cast<const uint4 *>(vr + u * kConvStep * D);
-                const BoxScales &vs = v_scales[gv % kSScales];
+                const TileScales &ts = scales[gv % kSScales];
                 uint32_t f[kConvPieces];
 #pragma unroll
                 for (int u = 0; u < kConvPieces; u++)
-                    f[u] = vs.factor[(conv_row + u * kConvStep) / kBox];
-                const uint32_t boxes = (uint32_t)vs.read;
-                unit = vs.unit;
-                // the f16 buffer's last tile has been read
-                if (!__all_sync(FULL, mbar_wait(&v_empty[b], ((gv / kSVStages) & 1) ^ 1)))
-                    return false;
-                __syncwarp();  // every lane's reads
-                if (lane == 0)
-                    mbar_arrive(&r_empty[s]);
+                    f[u] = ts.v[(conv_row + u * kConvStep) / kBox];
+                const int4 rest = *reinterpret_cast<const int4 *>(&ts.read);
+                boxes = (uint32_t)rest.x;
+                equal = rest.y != 0;
+                unit = __int_as_float(rest.z);
+                ks0 = ts.k[0];
                 uint8_t *vt = sV + (size_t)b * kVTile;
                 const bool clear = boxes != 0xffu || kb + kSKeys > k_len;
 #pragma unroll
@@ -637,22 +609,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    mbar_arrive(&r_empty[s]);
                     mbar_arrive(&v_conv[b]);
-                return true;
-            };
-            // The scales of K tile j's boxes, brought with its copies; ahead of its scores,
-            // so that they are not waited for on the chain
-            bool equal = true;
-            float ks0 = 1.f;
-            uint32_t boxes = 0;
-            auto scales_k = [&](int j) -> bool {
-                if (!__all_sync(FULL, mbar_wait(&k_full[(g0 + j) % kSKStages], ((g0 + j) / kSKStages) & 1)))
-                    return false;
-                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
-                equal = ks.equal != 0;
-                ks0 = ks.scale[0];
-                boxes = (uint32_t)ks.read;
+                }
                 return true;
             };
             // This row of Q as two E4M3 parts, q = sq (high + low), in its own place.  With
@@ -662,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // infinite element makes the row NaN.
             float sl = 0.f;  // score -> log2 units, but for K's scale
             if (nkt > 0) {
-                if (!(ok = __all_sync(FULL, mbar_wait(&q_full[tq], used & 1))))
+                if (!(ok = __all_sync(FULL, mbar_wait_asleep(&q_full[tq], used & 1))))
                     break;
                 used++;
                 uint8_t *qr = sQ + (size_t)tq * kQTile + r * 128;
@@ -707,12 +667,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0)
                     mbar_arrive(&q_conv[tq]);
             }
-            if (!(ok = convert_v(0)) || (nkt > 0 && !(ok = scales_k(0))))
+            if (!(ok = convert_v(0)))
                 break;
-            float v_unit = unit;  // of the V tile that the step's P meets
             for (int j = 0; j < nkt; j++) {
                 const int gt = gq + j;
-                ok = __all_sync(FULL, mbar_wait(&s_full[tq], gt & 1));
+                ok = __all_sync(FULL, mbar_wait_asleep(&s_full[tq], gt & 1));
                 if (!ok)
                     break;
                 tc::fence_after();
@@ -723,7 +682,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (j == nkt - 1)
                         mbar_arrive(&q_empty[tq]);
                 }
-                const BoxScales &ks = k_scales[(g0 + j) % kSScales];
                 // one scale in the tile: it joins the row's; else every box's scores are
                 // multiplied by theirs
                 const float cs = equal ? sl * ks0 : sl;
@@ -747,7 +705,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!equal) {
 #pragma unroll
                         for (int i = 0; i < 64; i++)
-                            x[i] *= ks.scale[4 * half + i / kBox];
+                            x[i] *= scales[(g0 + j) % kSScales].k[4 * half + i / kBox];
                     }
                     if (any_masked) {
                         const uint32_t hb = boxes >> (4 * half);
@@ -757,15 +715,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 };
                 auto top = [&]() {
-                    float t8[8];
+                    float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        t8[i] = x[i];
+                    for (int i = 4; i < 64; i += 8)
 #pragma unroll
-                    for (int i = 8; i < 64; i++)
-                        t8[i & 7] = fmaxf(t8[i & 7], x[i]);
-                    return fmaxf(fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])),
-                                 fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7])));
+                        for (int c = 0; c < 4; c++)
+                            t4[c] = i + 4 < 64 ? max3(t4[c], x[i + c], x[i + 4 + c]) : fmaxf(t4[c], x[i + c]);
+                    return max3(t4[0], t4[1], fmaxf(t4[2], t4[3]));
                 };
                 load(0);
                 float mraw = top();
@@ -773,11 +729,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mraw = fmaxf(mraw, top());
                 const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
                 const bool moves = __any_sync(FULL, mx > m + kLazy);
-                if (moves || v_unit != o_unit) {
+                if (moves || unit != o_unit) {
                     const float mn = moves ? fmaxf(m, mx) : m;
                     const float alpha = !moves || mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-                    const float o_alpha = v_unit == o_unit ? alpha : alpha * (o_unit / v_unit);
-                    o_unit = v_unit;
+                    const float o_alpha = unit == o_unit ? alpha : alpha * (o_unit / unit);
+                    o_unit = unit;
                     if (j > 0) {
                         // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1)
                         // completed, and the next P.V waits for this group's P
@@ -845,9 +801,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
                 if (j + 1 < all && !(ok = convert_v(j + 1)))
                     break;
-                if (j + 1 < nkt && !(ok = scales_k(j + 1)))
-                    break;
-                v_unit = unit;
             }
             if (!ok)
                 break;
@@ -864,7 +817,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                            ((size_t)it.kvh * p.Tq + it.cq0 + tok) * G + g] = -INFINITY;
             if (nkt > 0) {
                 const int gl = gq + nkt - 1;
-                ok = __all_sync(FULL, mbar_wait(&pv_done[tq], gl & 1));
+                ok = __all_sync(FULL, mbar_wait_asleep(&pv_done[tq], gl & 1));
                 if (!ok)
                     break;
                 tc::fence_after();

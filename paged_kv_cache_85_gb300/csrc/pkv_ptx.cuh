@@ -109,6 +109,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
     return true;
 }
 
+// The same for kernels whose warps wait often: the thread is suspended until the phase
+// completes (or a time of the hardware's passes), so that waiting takes few issue slots
+// from the warps that work, and the limit is looked at by the cycle counter.
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t *bar, uint32_t parity)
+{
+    const auto tried = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        return ok != 0;
+    };
+    if (tried())
+        return true;
+    const uint64_t t0 = sm_clock();
+    while (!tried())
+        if (sm_clock() - t0 > kPollLimitCycles)
+            return false;
+    return true;
+}
+
 // ---- TMA / bulk copies (global -> shared, completion on an mbarrier) -----
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y,
                                             int z, uint64_t *bar)
@@ -394,6 +419,14 @@ __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The largest of three (a NaN loses).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 

@@ -45,15 +45,14 @@ static_assert(kSScales >= kSRStages + 2, "a tile's scales outlive its stage");
 constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
 
 // What the softmax warps need of a key tile beside its codes; the producer brings it with
-// V's.  read: which of the eight boxes are read (a bit each).  k: their K scales, where
-// they are not read one that is; equal: all are k[0].  v: V's scales over `unit`, in which
-// O is held, as pairs of f16.
+// V's.  read: which of the eight boxes are read (a bit each).  k: their K scales (1 where
+// they are not read).  v: V's scales over `unit`, in which O is held, as pairs of f16.
 struct __align__(16) TileScales {
     float k[kSKeys / kBox];
     uint32_t v[kSKeys / kBox];
-    int read, equal;
+    int read;
     float unit;
-    int pad;
+    int pad[2];
 };
 
 struct ScaledSmem {
@@ -84,6 +83,20 @@ __host__ __device__ inline ScaledSmem scaled_smem_layout(int D)
     if (L.total < kTcMinSmem)
         L.total = kTcMinSmem;
     return L;
+}
+
+// Eight words, 32 bytes.
+__device__ __forceinline__ void store32(void *to, const uint32_t *v, bool aligned32)
+{
+    if (aligned32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        uint4 *d = reinterpret_cast<uint4 *>(to);
+        d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // Eight E4M3 codes times f (a pair of f16) as eight f16.
@@ -324,9 +337,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         flag_error(p.err_flag, 0x2 /* PKV_FLAG_BAD_BLOCK */);
                 }
                 const uint32_t read = __ballot_sync(FULL, row >= 0);
-                const float first = read ? __shfl_sync(FULL, sk, __ffs(read) - 1) : 1.f;
-                const float k = row >= 0 ? sk : first;
-                const bool equal = __all_sync(FULL, lane >= kBoxes || k == first);
+                // (a masked score is -inf, which no scale may turn into NaN)
+                const float k = row < 0 ? 1.f : sk == 0.f ? 0x1p-40f : sk;
                 const float most = __uint_as_float(__reduce_max_sync(
                     FULL, row >= 0 && sv > 0.f && sv < INFINITY ? __float_as_uint(sv) : 0u));
                 if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f)) {
@@ -367,7 +379,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (lane == 0) {
                     ts.read = (int)read;
-                    ts.equal = equal;
                     ts.unit = unit;
                 }
                 __syncwarp();
@@ -567,10 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.f;
             // of the next key tile's codes, and of O
             float unit = 1.f, o_unit = 1.f;
-            // K's scales of the next key tile: equal ones are ks0
-            bool equal = true;
-            float ks0 = 1.f;
-            uint32_t boxes = 0;
+            uint32_t boxes = 0;  // of the next key tile, those that are read
             // Key tile j's scales, and this group's half (64 keys) of its V: codes -> f16 in
             // the other buffer, times their box's factor, rows past k_len or of boxes that
             // are not read zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups
@@ -589,11 +597,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int u = 0; u < kConvPieces; u++)
                     f[u] = ts.v[(conv_row + u * kConvStep) / kBox];
-                const int4 rest = *reinterpret_cast<const int4 *>(&ts.read);
+                const int2 rest = *reinterpret_cast<const int2 *>(&ts.read);
                 boxes = (uint32_t)rest.x;
-                equal = rest.y != 0;
-                unit = __int_as_float(rest.z);
-                ks0 = ts.k[0];
+                unit = __int_as_float(rest.y);
                 uint8_t *vt = sV + (size_t)b * kVTile;
                 const bool clear = boxes != 0xffu || kb + kSKeys > k_len;
 #pragma unroll
@@ -637,12 +643,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     top = bf16x2_max(bf16x2_max(top, w[i].x & ABS), bf16x2_max(w[i].y & ABS, bf16x2_max(w[i].z & ABS, w[i].w & ABS)));
                 }
                 const int ebits = min(max((int)(max(top & 0xffffu, top >> 16) >> 7), 8), 254);
-                sl = p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23);
+                // (not so small that it or its product with a K scale is 0, which times a masked
+                // score, -inf, would be NaN: no score that small moves a weight)
+                sl = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23), 1e-25f);
                 if (max(top & 0xffffu, top >> 16) == 0x7f80u)
                     sl = NAN;
                 float inv = __uint_as_float((uint32_t)(261 - ebits) << 23);
                 if (p.neg_scale)
                     inv = -inv;
+                const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {  // sixteen elements
                     const uint4 e[2] = {w[2 * i], w[2 * i + 1]};
@@ -650,13 +659,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         const uint32_t w0 = c & 1 ? e[c >> 1].z : e[c >> 1].x, w1 = c & 1 ? e[c >> 1].w : e[c >> 1].y;
-                        const float2 x0 = bf16x2_to_float2(w0), x1 = bf16x2_to_float2(w1);
-                        const float a0 = x0.x * inv, a1 = x0.y * inv, a2 = x1.x * inv, a3 = x1.y * inv;
-                        const uint32_t h01 = f32x2_to_e4m3x2(a0, a1), h23 = f32x2_to_e4m3x2(a2, a3);
-                        const float2 b01 = f16x2_to_float2(e4m3x2_to_f16x2(h01));
-                        const float2 b23 = f16x2_to_float2(e4m3x2_to_f16x2(h23));
-                        hi[c] = h01 | (h23 << 16);
-                        lo[c] = f32x2_to_e4m3x2(a0 - b01.x, a1 - b01.y) | (f32x2_to_e4m3x2(a2 - b23.x, a3 - b23.y) << 16);
+                        const float2 a0 = fmul2(bf16x2_to_float2(w0), inv2), a1 = fmul2(bf16x2_to_float2(w1), inv2);
+                        // (in f16 both are exact, but for what lies below 2^-14)
+                        const uint32_t x0 = pack_f16x2(a0.x, a0.y), x1 = pack_f16x2(a1.x, a1.y);
+                        const uint32_t h0 = f16x2_to_e4m3x2(x0), h1 = f16x2_to_e4m3x2(x1);
+                        hi[c] = h0 | (h1 << 16);
+                        lo[c] = f16x2_to_e4m3x2(f16x2_sub(x0, e4m3x2_to_f16x2(h0))) |
+                                (f16x2_to_e4m3x2(f16x2_sub(x1, e4m3x2_to_f16x2(h1))) << 16);
                     }
                     const int lo_at = D == 128 ? (int)kQHalf + ((i ^ (r & 7)) << 4) : ((4 + i) ^ (r & 7)) << 4;
                     *reinterpret_cast<uint4 *>(qr + ((i ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -682,15 +691,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (j == nkt - 1)
                         mbar_arrive(&q_empty[tq]);
                 }
-                // one scale in the tile: it joins the row's; else every box's scores are
-                // multiplied by theirs
-                const float cs = equal ? sl * ks0 : sl;
-                const float2 cs2 = make_float2(cs, cs);
                 const int key_base = (j0 + j) * kSKeys;
-                // masked keys: past this row's position (the diagonal tiles) or in an
-                // unloaded box; most tiles have none in the whole warp
-                const bool any_masked = __any_sync(FULL, boxes != 0xffu || key_base + kSKeys - 1 > pos);
-                const int lim = pos - key_base;  // keys i > lim are in the future
+                // Masked keys, past their row's position (the diagonal tiles) or in a box that
+                // is not read: -inf into the scores, so that what follows knows of none.  Most
+                // tiles have none in the whole warp; of its own and short, because the
+                // instructions of the rest barely fit the caches.
+                if (__any_sync(FULL, boxes != 0xffu || key_base + kSKeys - 1 > pos)) {
+                    const int lim = pos - key_base;  // keys i > lim are in the future
+#pragma unroll 1
+                    for (int b = 0; b < kBoxes; b++) {
+                        const int last = (boxes >> b) & 1u ? lim - kBox * b : -1;
+                        if (__all_sync(FULL, last >= kBox - 1))
+                            continue;
+                        uint32_t r[16];
+                        tc::ld16(tS + kBox * b, r);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kBox; i++)
+                            r[i] = i > last ? __float_as_uint(-INFINITY) : r[i];
+                        tc::st16(tS + kBox * b, r);
+                    }
+                    tc::wait_st();
+                }
+                // K's scales of the tile's boxes join the row's
+                const float *ks = scales[(g0 + j) % kSScales].k;
                 float x[64];
                 auto load = [&](int half) {
                     uint32_t a[32], b[32];
@@ -702,32 +726,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         x[i] = __uint_as_float(a[i]);
                         x[32 + i] = __uint_as_float(b[i]);
                     }
-                    if (!equal) {
-#pragma unroll
-                        for (int i = 0; i < 64; i++)
-                            x[i] *= scales[(g0 + j) % kSScales].k[4 * half + i / kBox];
-                    }
-                    if (any_masked) {
-                        const uint32_t hb = boxes >> (4 * half);
-#pragma unroll
-                        for (int i = 0; i < 64; i++)
-                            x[i] = (64 * half + i > lim || !((hb >> (i / kBox)) & 1u)) ? -INFINITY : x[i];
-                    }
                 };
-                auto top = [&]() {
-                    float t4[4] = {x[0], x[1], x[2], x[3]};
+                auto top = [&](int half, float t) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(ks + 4 * half);
 #pragma unroll
-                    for (int i = 4; i < 64; i += 8)
-#pragma unroll
-                        for (int c = 0; c < 4; c++)
-                            t4[c] = i + 4 < 64 ? max3(t4[c], x[i + c], x[i + 4 + c]) : fmaxf(t4[c], x[i + c]);
-                    return max3(t4[0], t4[1], fmaxf(t4[2], t4[3]));
+                    for (int b = 0; b < 4; b++) {
+                        const float *y = x + kBox * b;
+                        const float u = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[8]));
+                        const float v = max3(max3(y[9], y[10], y[11]), max3(y[12], y[13], y[14]), y[15]);
+                        t = fmaxf(t, fmaxf(u, v) * (b == 0 ? k4.x : b == 1 ? k4.y : b == 2 ? k4.z : k4.w));
+                    }
+                    return t;
                 };
                 load(0);
-                float mraw = top();
+                float mraw = top(0, -INFINITY);
                 load(1);
-                mraw = fmaxf(mraw, top());
-                const float mx = mraw == -INFINITY ? -INFINITY : mraw * cs;
+                mraw = top(1, mraw);
+                const float mx = mraw * sl;
                 const bool moves = __any_sync(FULL, mx > m + kLazy);
                 if (moves || unit != o_unit) {
                     const float mn = moves ? fmaxf(m, mx) : m;
@@ -755,33 +770,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float nmu = m == -INFINITY ? 0.f : -m;
                 const float2 nm2 = make_float2(nmu, nmu);
                 float2 ls0 = make_float2(0.f, 0.f), ls1 = ls0;
-                auto exponentiate = [&](uint32_t to) {
+                auto exponentiate = [&](int half, uint32_t to) {
                     uint32_t pk[32];
-                    if (!any_masked) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(ks + 4 * half);
 #pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            const float2 a = ffma2(make_float2(x[2 * i], x[2 * i + 1]), cs2, nm2);
-                            const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                            if (i & 1)
-                                ls1 = fadd2(ls1, e);
-                            else
-                                ls0 = fadd2(ls0, e);
-                            pk[i] = pack_f16x2(e.x, e.y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            float2 a = ffma2(make_float2(x[2 * i], x[2 * i + 1]), cs2, nm2);
-                            // exact zeros for masked keys (also when the scale is 0)
-                            a.x = x[2 * i] == -INFINITY ? -INFINITY : a.x;
-                            a.y = x[2 * i + 1] == -INFINITY ? -INFINITY : a.y;
-                            const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                            if (i & 1)
-                                ls1 = fadd2(ls1, e);
-                            else
-                                ls0 = fadd2(ls0, e);
-                            pk[i] = pack_f16x2(e.x, e.y);
-                        }
+                    for (int i = 0; i < 32; i++) {
+                        const float c = sl * (i < 8 ? k4.x : i < 16 ? k4.y : i < 24 ? k4.z : k4.w);
+                        const float2 a = ffma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(c, c), nm2);
+                        const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                        if (i & 1)
+                            ls1 = fadd2(ls1, e);
+                        else
+                            ls0 = fadd2(ls0, e);
+                        pk[i] = pack_f16x2(e.x, e.y);
                     }
                     tc::st32(to, pk);
                 };
@@ -792,10 +793,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (lane == 0)
                         mbar_arrive(&pv_ready[2 * half + tq]);
                 };
-                exponentiate(tS + 96);  // keys 64..127, over score columns read above
+                exponentiate(1, tS + 96);  // keys 64..127, over score columns read above
                 hand_over(1);
                 load(0);                // keys 0..63 again
-                exponentiate(tS);
+                exponentiate(0, tS);
                 l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
                 hand_over(0);
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
@@ -829,67 +830,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (valid)
                         p.part_lse[(size_t)item.split * p.Tq * p.Hq + lse_at] =
                             l == 0.f ? -INFINITY : m + log2f(l);
-                    float4 *dst = reinterpret_cast<float4 *>(
-                        p.part_out + (((size_t)item.split * p.Tq + row) * p.Hq + it.kvh * G + g) * D);
+                    float *dst = p.part_out + (((size_t)item.split * p.Tq + row) * p.Hq + it.kvh * G + g) * D;
+                    const bool aligned32 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; cc++) {
                         uint32_t ro[32];
                         tc::ld32(tO + 32 * cc, ro);
                         tc::wait_ld();
-                        if (valid) {
 #pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                dst[8 * cc + i] = make_float4(__uint_as_float(ro[4 * i]) * inv,
-                                                              __uint_as_float(ro[4 * i + 1]) * inv,
-                                                              __uint_as_float(ro[4 * i + 2]) * inv,
-                                                              __uint_as_float(ro[4 * i + 3]) * inv);
-                        }
+                        for (int i = 0; i < 32; i++)
+                            ro[i] = __float_as_uint(__uint_as_float(ro[i]) * inv);
+#pragma unroll
+                        for (int i = 0; i < 32 && valid; i += 8)
+                            store32(dst + 32 * cc + i, ro + i, aligned32);
                     }
                 } else {
                     if (SPLIT && valid)
                         p.part_lse[lse_at] = INFINITY;  // nothing to join
-                    // 64 columns (eight 16-byte pieces) of a row at a time; eight lanes
-                    // trade their rows' pieces (three butterfly steps), so that a store
-                    // instruction writes whole 128-byte lines of four rows, not 16 bytes
-                    // in each of 32 lines
+                    // a row per thread in 32-byte pieces: whole sectors
+                    uint16_t *dst = p.out + (row * p.Hq + it.kvh * G + g) * D;
+                    const bool aligned32 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
-                    for (int hf = 0; hf < HALVES; hf++) {
-                        uint32_t ra[32], rb[32], v[32];
-                        tc::ld32(tO + 64 * hf, ra);
-                        tc::ld32(tO + 64 * hf + 32, rb);
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t ro[32], v[16];
+                        tc::ld32(tO + 32 * cc, ro);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            v[i] = pack_bf16x2(__uint_as_float(ra[2 * i]) * inv, __uint_as_float(ra[2 * i + 1]) * inv);
-                            v[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]) * inv,
-                                                    __uint_as_float(rb[2 * i + 1]) * inv);
-                        }
-#pragma unroll
-                        for (int s = 1; s < 8; s *= 2) {
-                            const bool up = (lane & s) != 0;
-#pragma unroll
-                            for (int k = 0; k < 8; k++) {
-                                if (k & s)
-                                    continue;
-#pragma unroll
-                                for (int w = 0; w < 4; w++) {  // piece k of the upper lane for k + s of the lower
-                                    const uint32_t give = up ? v[4 * k + w] : v[4 * (k + s) + w];
-                                    const uint32_t got = __shfl_xor_sync(FULL, give, s);
-                                    v[4 * k + w] = up ? got : v[4 * k + w];
-                                    v[4 * (k + s) + w] = up ? v[4 * (k + s) + w] : got;
-                                }
-                            }
-                        }
-                        // this lane now has piece lane % 8 of the rows 8 (lane / 8) + k
-#pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const int rr = 32 * (warp & 3) + (lane & 24) + k;
-                            const int tk = it.tok0 + tq * TPC + rr / G;
-                            if (tk < it.q_len)
-                                *reinterpret_cast<uint4 *>(
-                                    p.out + (((size_t)it.cq0 + tk) * p.Hq + it.kvh * G + rr % G) * D + 64 * hf +
-                                    8 * (lane & 7)) =
-                                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        for (int i = 0; i < 16; i++)
+                            v[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv, __uint_as_float(ro[2 * i + 1]) * inv);
+                        if (valid) {
+                            store32(dst + 32 * cc, v, aligned32);
+                            store32(dst + 32 * cc + 16, v + 8, aligned32);
                         }
                     }
                 }

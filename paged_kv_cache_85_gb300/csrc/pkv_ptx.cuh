@@ -316,6 +316,21 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
     return r;
 }
 
+// Two f16 -> two E4M3 codes alike.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Byte permute: result byte i = byte sel_i of the 8-byte value {b, a}.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
 {

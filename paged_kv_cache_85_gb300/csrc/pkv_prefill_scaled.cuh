@@ -632,34 +632,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 used++;
                 uint8_t *qr = sQ + (size_t)tq * kQTile + r * 128;
-                uint4 w[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 8; i++)
-                    w[i] = *reinterpret_cast<const uint4 *>(qr + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4));
+                const auto at = [&](int i) {  // sixteen bytes of the row
+                    return reinterpret_cast<uint4 *>(qr + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4));
+                };
                 uint32_t top = 0;  // two bf16 magnitudes
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < D / 8; i++) {
-                    constexpr uint32_t ABS = 0x7fff7fffu;
-                    top = bf16x2_max(bf16x2_max(top, w[i].x & ABS), bf16x2_max(w[i].y & ABS, bf16x2_max(w[i].z & ABS, w[i].w & ABS)));
+                    const uint4 w = *at(i);
+                    top = bf16x2_absmax(top, bf16x2_absmax(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w)));
                 }
-                const int ebits = min(max((int)(max(top & 0xffffu, top >> 16) >> 7), 8), 254);
+                top &= 0x7fff7fffu;
+                top = max(top & 0xffffu, top >> 16);
+                const int ebits = min(max((int)(top >> 7), 8), 254);
                 // (not so small that it or its product with a K scale is 0, which times a masked
                 // score, -inf, would be NaN: no score that small moves a weight)
                 sl = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23), 1e-25f);
-                if (max(top & 0xffffu, top >> 16) == 0x7f80u)
+                if (top == 0x7f80u)
                     sl = NAN;
                 float inv = __uint_as_float((uint32_t)(261 - ebits) << 23);
                 if (p.neg_scale)
                     inv = -inv;
                 const float2 inv2 = make_float2(inv, inv);
-#pragma unroll
+                // The high parts fill the row's first half, behind what is read; the low parts
+                // its second, once all is read: until then they lie in the score columns.  A
+                // loop, for its instructions' sake.
+#pragma unroll 1
                 for (int i = 0; i < D / 16; i++) {  // sixteen elements
-                    const uint4 e[2] = {w[2 * i], w[2 * i + 1]};
+                    const uint4 w0 = *at(2 * i), w1 = *at(2 * i + 1);
+                    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
-                        const uint32_t w0 = c & 1 ? e[c >> 1].z : e[c >> 1].x, w1 = c & 1 ? e[c >> 1].w : e[c >> 1].y;
-                        const float2 a0 = fmul2(bf16x2_to_float2(w0), inv2), a1 = fmul2(bf16x2_to_float2(w1), inv2);
+                        const float2 a0 = fmul2(bf16x2_to_float2(w[2 * c]), inv2),
+                                     a1 = fmul2(bf16x2_to_float2(w[2 * c + 1]), inv2);
                         // (in f16 both are exact, but for what lies below 2^-14)
                         const uint32_t x0 = pack_f16x2(a0.x, a0.y), x1 = pack_f16x2(a1.x, a1.y);
                         const uint32_t h0 = f16x2_to_e4m3x2(x0), h1 = f16x2_to_e4m3x2(x1);
@@ -667,10 +672,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         lo[c] = f16x2_to_e4m3x2(f16x2_sub(x0, e4m3x2_to_f16x2(h0))) |
                                 (f16x2_to_e4m3x2(f16x2_sub(x1, e4m3x2_to_f16x2(h1))) << 16);
                     }
-                    const int lo_at = D == 128 ? (int)kQHalf + ((i ^ (r & 7)) << 4) : ((4 + i) ^ (r & 7)) << 4;
-                    *reinterpret_cast<uint4 *>(qr + ((i ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(qr + lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *at(i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    tc::st4(tS + 4 * i, lo);
                 }
+                tc::wait_st();
+                uint32_t lo[D / 4];
+                if constexpr (D == 128)
+                    tc::ld32(tS, lo);
+                else
+                    tc::ld16(tS, lo);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+                    *at(D / 16 + i) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                tc::fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)

@@ -666,6 +666,22 @@ def evict_kvcache(k_cache, v_cache, weights, block_tables, context_lens, budget,
 
 
 # ---------------------------------------------------------------- FP8 caches with a scale per block and KV head
+#
+# The smallest calls are bound by what happens on the host, so each looks its tensors
+# over in one expression; what it finds amiss is told by the checks of the calls above.
+
+_torch = None
+_get_stream = _raw_stream
+
+
+def _import_torch():
+    global _torch, _get_stream
+    import torch
+
+    load_library()
+    _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+    _torch = torch
+    return torch
 
 
 def prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs) -> int:
@@ -673,8 +689,8 @@ def prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs) -> 
     return int(load_library().pkv_prefill_scaled_workspace_bytes(B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs))
 
 
-def _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales):
-    """Check the caches and their scales; returns (device index, NB, bs, Hkv, D)."""
+def _amiss_caches(torch, k_cache, v_cache, k_scales, v_scales):
+    """Raise what is wrong with the caches or their scales."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -690,7 +706,49 @@ def _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales):
     for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
         if t.shape != (NB, Hkv):
             raise ValueError(f"{name} must be [NB, Hkv] = {(NB, Hkv)} for these caches; got {tuple(t.shape)}")
-    return dev, NB, bs, Hkv, D
+
+
+def _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales):
+    """Check the caches and their scales; returns (device index, shape)."""
+    f32, types = torch.float32, (torch.uint8, torch.float8_e4m3fn)
+    try:
+        dev, shape = k_cache.get_device(), k_cache.shape
+        scales = (shape[0], shape[2])
+        if (dev >= 0 and len(shape) == 4 and k_cache.dtype in types and v_cache.dtype in types
+                and v_cache.shape == shape and k_scales.shape == scales and v_scales.shape == scales
+                and k_scales.dtype is f32 and v_scales.dtype is f32 and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and v_cache.get_device() == dev and k_scales.get_device() == dev
+                and v_scales.get_device() == dev):
+            return dev, shape
+    except (AttributeError, IndexError):
+        pass
+    _amiss_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    return k_cache.get_device(), k_cache.shape
+
+
+def _well(t, dtype, dim, dev):
+    """Whether ``t`` is a contiguous tensor of ``dim`` dims and this type on CUDA device ``dev``."""
+    try:
+        return t.dtype is dtype and t.dim() == dim and t.get_device() == dev and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+def _result_scaled(torch, dev, out, q):
+    if not (_well(out, torch.bfloat16, 3, dev) and out.shape == q.shape):
+        _result(torch, dev, out, q)
+
+
+def _call(torch, dev, function, *args):
+    """A library call on the current stream of device ``dev``, which it makes the current one."""
+    if torch.cuda.current_device() == dev:
+        status = function(*args, _get_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = function(*args, _get_stream(dev))
+    if status:
+        _check(status)
 
 
 def store_kvcache_scaled(k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None):
@@ -702,86 +760,112 @@ def store_kvcache_scaled(k, v, k_cache, v_cache, k_scales, v_scales, slot_mappin
     not, and the rows that the block holds are recoded.  The tokens of one block
     follow each other in ``slot_mapping``.  Nothing needs initialising.
     """
-    import torch
-
-    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
-    bf16 = torch.bfloat16
-    _tensors(torch, dev, (k, "k", bf16, 3), (v, "v", bf16, 3), (slot_mapping, "slot_mapping", torch.int64, 1))
-    N = k.shape[0]
-    if v.shape != k.shape or tuple(k.shape[1:]) != (Hkv, D):
-        raise ValueError(f"k and v must be [N, {Hkv}, {D}] for these caches; got {tuple(k.shape)} and {tuple(v.shape)}")
+    torch = _torch or _import_torch()
+    dev, (NB, bs, Hkv, D) = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    bf16, i64 = torch.bfloat16, torch.int64
+    if not (_well(k, bf16, 3, dev) and _well(v, bf16, 3, dev) and _well(slot_mapping, i64, 1, dev)):
+        _tensors(torch, dev, (k, "k", bf16, 3), (v, "v", bf16, 3), (slot_mapping, "slot_mapping", i64, 1))
+    shape = k.shape
+    N = shape[0]
+    if v.shape != shape or shape[1] != Hkv or shape[2] != D:
+        raise ValueError(f"k and v must be [N, {Hkv}, {D}] for these caches; got {tuple(shape)} and {tuple(v.shape)}")
     if slot_mapping.shape[0] != N:
         raise ValueError(f"slot_mapping has {slot_mapping.shape[0]} slots for {N} rows")
-    flag = _flag(torch, dev, err_flag)
-    lib = _lib or load_library()
-    with _on_device(dev):
-        _check(lib.pkv_store_kvcache_scaled(
-            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), slot_mapping.data_ptr(), N, Hkv, D, NB, bs, flag, _raw_stream(dev)))
+    _call(torch, dev, _lib.pkv_store_kvcache_scaled, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), N, Hkv, D, NB,
+          bs, None if err_flag is None else _flag(torch, dev, err_flag))
 
 
 def paged_attn_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
                              max_ctas=0, workspace=None, err_flag=None):
     """Decode attention over FP8 caches with a scale per block and KV head; writes ``out`` and returns it."""
-    import torch
-
+    torch = _torch or _import_torch()
     max_ctas = _c_int(max_ctas, "max_ctas")
-    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
-    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", torch.int32, 2),
-             (context_lens, "context_lens", torch.int32, 1))
+    dev, (NB, bs, Hkv, D) = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (_well(q, bf16, 3, dev) and _well(block_tables, i32, 2, dev) and _well(context_lens, i32, 1, dev)):
+        _tensors(torch, dev, (q, "q", bf16, 3), (block_tables, "block_tables", i32, 2),
+                 (context_lens, "context_lens", i32, 1))
     B, Hq, D2 = q.shape
     if D2 != D:
         raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
-    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+    rows, MBS = block_tables.shape
+    if rows != B or context_lens.shape[0] != B:
         raise ValueError("block_tables/context_lens batch != q batch")
-    _result(torch, dev, out, q)
-    flag = _flag(torch, dev, err_flag)
-    MBS = max(block_tables.shape[1], 1)
-    lib = _lib or load_library()
-    with _on_device(dev):
-        stream = _raw_stream(dev)
-        ws, ws_ptr, ws_bytes = _scratch(torch, workspace, _bytes(
-            "pkv_decode_workspace_bytes", B, Hq, Hkv, D, MBS, bs, max_ctas), dev, stream)
-        _check(lib.pkv_paged_attn_decode_scaled(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+    _result_scaled(torch, dev, out, q)
+    flag = None if err_flag is None else _flag(torch, dev, err_flag)
+    MBS = MBS or 1
+    need = _bytes("pkv_decode_workspace_bytes", B, Hq, Hkv, D, MBS, bs, max_ctas)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             block_tables.data_ptr(), MBS, context_lens.data_ptr(), B, Hq, Hkv, D, NB, bs, float(scale),
-            out.data_ptr(), ws_ptr, ws_bytes, max_ctas, flag, stream))
+            out.data_ptr())
+    _call_scratch(torch, dev, _lib.pkv_paged_attn_decode_scaled, args, workspace, need, (max_ctas, flag))
     return out
+
+
+def _call_scratch(torch, dev, function, before, workspace, need, after):
+    """``_call`` with a workspace (address and bytes) between two groups of arguments."""
+    if torch.cuda.current_device() == dev:
+        stream = _get_stream(dev)
+        ws, ptr, nbytes = _scratch(torch, workspace, need, dev, stream)
+        status = function(*before, ptr, nbytes, *after, stream)
+    else:
+        with torch.cuda.device(dev):
+            stream = _get_stream(dev)
+            ws, ptr, nbytes = _scratch(torch, workspace, need, dev, stream)
+            status = function(*before, ptr, nbytes, *after, stream)
+    if status:
+        _check(status)
 
 
 def paged_prefill_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens_q, cu_seqlens_k,
                          max_seqlen_q, scale, out, workspace=None, err_flag=None):
     """``paged_prefill`` over FP8 caches with a scale per block and KV head; writes ``out`` and returns it."""
-    import torch
-
+    torch = _torch or _import_torch()
     max_seqlen_q = _c_int(max_seqlen_q, "max_seqlen_q")
-    dev, NB, bs, Hkv, D = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
-    i32 = torch.int32
-    _tensors(torch, dev, (q, "q", torch.bfloat16, 3), (block_tables, "block_tables", i32, 2),
-             (cu_seqlens_q, "cu_seqlens_q", i32, 1), (cu_seqlens_k, "cu_seqlens_k", i32, 1))
+    dev, (NB, bs, Hkv, D) = _scaled_caches(torch, k_cache, v_cache, k_scales, v_scales)
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (_well(q, bf16, 3, dev) and _well(block_tables, i32, 2, dev) and _well(cu_seqlens_q, i32, 1, dev)
+            and _well(cu_seqlens_k, i32, 1, dev)):
+        _tensors(torch, dev, (q, "q", bf16, 3), (block_tables, "block_tables", i32, 2),
+                 (cu_seqlens_q, "cu_seqlens_q", i32, 1), (cu_seqlens_k, "cu_seqlens_k", i32, 1))
     Tq, Hq, D2 = q.shape
     if D2 != D:
         raise ValueError(f"q's head_dim {D2} is not the caches' {D}")
     B = cu_seqlens_q.shape[0] - 1
-    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
+    rows, MBS = block_tables.shape
+    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or rows != B:
         raise ValueError("cu_seqlens / block_tables batch sizes differ")
-    _result(torch, dev, out, q)
-    flag = _flag(torch, dev, err_flag)
-    MBS = max(block_tables.shape[1], 1)
-    lib = _lib or load_library()
-    with _on_device(dev):
-        stream = _raw_stream(dev)
-        need = _bytes("pkv_prefill_scaled_workspace_bytes", B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs)
-        ws, ws_ptr, ws_bytes = (None, None, 0) if need == 0 and workspace is None else _scratch(
-            torch, workspace, need, dev, stream)
-        _check(lib.pkv_paged_prefill_scaled(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+    _result_scaled(torch, dev, out, q)
+    flag = None if err_flag is None else _flag(torch, dev, err_flag)
+    MBS = MBS or 1
+    need = _bytes("pkv_prefill_scaled_workspace_bytes", B, Tq, max_seqlen_q, Hq, Hkv, D, MBS, bs)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             block_tables.data_ptr(), MBS, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq, max_seqlen_q,
-            Hq, Hkv, D, NB, bs, float(scale), out.data_ptr(), ws_ptr, ws_bytes, flag, stream))
+            Hq, Hkv, D, NB, bs, float(scale), out.data_ptr())
+    if need == 0 and workspace is None:
+        _call(torch, dev, _lib.pkv_paged_prefill_scaled, *args, None, 0, flag)
+    else:
+        _call_scratch(torch, dev, _lib.pkv_paged_prefill_scaled, args, workspace, need, (flag,))
     return out
 
 
 # ---------------------------------------------------------------- copies of blocks
+
+
+def _amiss_pages(torch, tensors):
+    """Raise what is wrong with a list of tensors under one set of block ids."""
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"tensors[{i}] must be a torch.Tensor")
+        if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"tensors[{i}] must be a contiguous CUDA tensor [NB, ...]")
+        if t.get_device() != tensors[0].get_device() or t.shape[0] != tensors[0].shape[0]:
+            raise ValueError(f"tensors[{i}] is {tuple(t.shape)} on {t.device}; the first has "
+                             f"{tensors[0].shape[0]} blocks on {tensors[0].device}")
+
+
+_arrays: dict = {}  # ctypes array types by length
 
 
 def copy_blocks(tensors, pairs, err_flag=None):
@@ -793,35 +877,35 @@ def copy_blocks(tensors, pairs, err_flag=None):
     Destinations are distinct and no other pair's source (``BlockManager.fork``
     and ``BlockManager.compact`` give such pairs).
     """
-    import torch
-
+    torch = _torch or _import_torch()
     tensors = list(tensors)
     if not tensors:
         raise ValueError("copy_blocks: no tensors")
-    if not isinstance(tensors[0], torch.Tensor):
-        raise TypeError("tensors[0] must be a torch.Tensor")
-    dev = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"tensors[{i}] must be a torch.Tensor")
-        if not t.is_cuda or t.dim() < 1 or not t.is_contiguous():
-            raise ValueError(f"tensors[{i}] must be a contiguous CUDA tensor [NB, ...]")
-        if t.get_device() != dev or t.shape[0] != tensors[0].shape[0]:
-            raise ValueError(f"tensors[{i}] is {tuple(t.shape)} on {t.device}; the first has "
-                             f"{tensors[0].shape[0]} blocks on {tensors[0].device}")
-    _tensors(torch, dev, (pairs, "pairs", torch.int32, 2))
+    try:
+        dev, NB = tensors[0].get_device(), tensors[0].shape[0]
+        well = dev >= 0
+        for t in tensors:
+            if not (t.get_device() == dev and t.shape[0] == NB and t.is_contiguous()):
+                well = False
+    except (AttributeError, IndexError):
+        well = False
+    if not well:
+        _amiss_pages(torch, tensors)
+    if not _well(pairs, torch.int32, 2, dev):
+        _tensors(torch, dev, (pairs, "pairs", torch.int32, 2))
     n, two = pairs.shape
     if two != 2:
         raise ValueError(f"pairs must be [n, 2]; got {tuple(pairs.shape)}")
-    flag = _flag(torch, dev, err_flag)
-    NB = tensors[0].shape[0]
-    tensors = [t for t in tensors if t.numel()]
+    flag = None if err_flag is None else _flag(torch, dev, err_flag)
+    nbytes = [t.nbytes for t in tensors]
+    if 0 in nbytes:  # blocks of nothing
+        tensors = [t for t in tensors if t.nbytes]
+        nbytes = [t.nbytes for t in tensors]
     if n == 0 or not tensors:
         return
-    lib = _lib or load_library()
     m = len(tensors)
-    with _on_device(dev):
-        _check(lib.pkv_copy_blocks(
-            (ctypes.c_void_p * m)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * m)(*[t.numel() // NB * t.element_size() for t in tensors]), m,
-            pairs.data_ptr(), n, NB, flag, _raw_stream(dev)))
+    types = _arrays.get(m)
+    if types is None:
+        types = _arrays[m] = (ctypes.c_void_p * m, ctypes.c_int64 * m)
+    _call(torch, dev, _lib.pkv_copy_blocks, types[0](*[t.data_ptr() for t in tensors]),
+          types[1](*[b // NB for b in nbytes]), m, pairs.data_ptr(), n, NB, flag)

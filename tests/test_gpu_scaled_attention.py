@@ -273,15 +273,15 @@ def test_captured_with_two_graphs(pkv):
         ref.check(host(want[0]), w, m)
         w, m = ref.prefill(qp, c, [50, 5, 5], 0.1)
         ref.check(host(want[1]), w, m)
-        jobs.append((g, (out, outp), want))
+        jobs.append((g, (out, outp), want, call))  # (call keeps the inputs)
     streams = [torch.cuda.Stream() for _ in jobs]
     torch.cuda.synchronize()
     for _ in range(10):
-        for (g, _, _), t in zip(jobs, streams):
+        for (g, *_), t in zip(jobs, streams):
             with torch.cuda.stream(t):
                 g.replay()
     torch.cuda.synchronize()
-    for _, outs, wants in jobs:
+    for _, outs, wants, _ in jobs:
         for a, b in zip(outs, wants):
             assert torch.equal(a, b)
 

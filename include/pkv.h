@@ -486,7 +486,8 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
  * and infinities saturate, NaN stays NaN.  All products in fp32.
  *
  *   k, v, slot_mapping, err_flag   as in pkv_store_kvcache
- *   D in {64, 128}, bs a multiple of 16, Hkv <= 65535, NB*bs < 2^31
+ *   N < 2^30, D in {64, 128}, bs a multiple of 16, Hkv <= 65535, N*Hkv < 2^34,
+ *   NB*bs < 2^31
  * The tokens of one block follow each other in slot_mapping with nothing between
  * them (as the block manager's slots of a sequence do; in any order among
  * themselves): where they do not, that block's rows and scales are unspecified.

@@ -1208,10 +1208,9 @@ pkv_status pkv_store_kvcache_scaled(const void *k, const void *v, void *k_cache,
     if (N < 0 || Hkv < 1 || NB < 1 || bs < 1)
         return fail(PKV_ERR_INVALID_ARG, "store_kvcache_scaled: bad sizes N=%lld Hkv=%d NB=%lld bs=%d",
                     (long long)N, Hkv, (long long)NB, bs);
-    if (N > 0x7fffffffLL || Hkv > 65535)
-        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N must be < 2^31 and Hkv <= 65535");
-    if ((N + 15) / 16 * Hkv * 2 > 0x7fffffffLL)
-        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N*Hkv must be < 2^34");
+    if (N >= (1LL << 30) || Hkv > 65535 || N * Hkv >= (1LL << 34))
+        return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: N must be < 2^30, Hkv <= 65535 and "
+                    "N*Hkv < 2^34");
     if (D != 64 && D != 128)
         return fail(PKV_ERR_UNSUPPORTED, "store_kvcache_scaled: head_dim %d not in {64,128}", D);
     if (bs % pkv::kBox != 0)

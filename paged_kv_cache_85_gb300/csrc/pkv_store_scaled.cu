@@ -98,6 +98,9 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
     __shared__ long long s_end;
 
     grid_launch_dependents();
+    // Earlier kernels may have written any of the inputs, and may still read the cache.
+    // (With the inputs read ahead of this, a step behind another one 1.8 us, so 2.5.)
+    grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // K and V, then heads, then windows: CTAs that run together read the same rows
     const int z = blockIdx.x & 1, h = (int)((blockIdx.x >> 1) % (uint32_t)p.Hkv);
@@ -155,11 +158,8 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
         if (s && first == T)
             first = 32 * i + __ffs(s) - 1;
     }
-    if (n_runs == 0) {
-        // (a step of nothing but padding must not end before the kernel ahead of it)
-        grid_dependency_wait();
+    if (n_runs == 0)
         return;
-    }
     // how far the last run goes on behind the window, of what is seen
     int end = T;
 #pragma unroll
@@ -227,8 +227,6 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
         }
     };
     load(0);
-    // (earlier kernels may still read the cache, or have written the scales)
-    grid_dependency_wait();
     float *scale_at = nullptr;
     float had = 0.f;
     if (tid < n_runs) {
@@ -295,8 +293,8 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
             const int run = s_grown[g];
             const float ratio = s_ratio[run];
             uint8_t *base = cache + ((size_t)s_blk[run] * bs * p.Hkv + h) * D;
-            for (uint32_t c = tid; c < bs * CPR; c += kSsThreads) {
-                uint4 *w = reinterpret_cast<uint4 *>(base + (size_t)(c / CPR) * p.Hkv * D + (c % CPR) * 16);
+            for (size_t c = tid; c < (size_t)bs * CPR; c += kSsThreads) {
+                uint4 *w = reinterpret_cast<uint4 *>(base + c / CPR * p.Hkv * D + c % CPR * 16);
                 const uint4 a = *w;
                 *w = make_uint4(recode4(a.x, ratio), recode4(a.y, ratio), recode4(a.z, ratio),
                                 recode4(a.w, ratio));
@@ -331,9 +329,12 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
 
 template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStream_t stream)
 {
-    // Few tokens (decode steps: a run each): small windows, so that more CTAs share
-    // them.  Many: windows of 128, of which a thread keeps 256 rows' loads in flight.
-    const bool few = p.N < 2048;
+    // Few tokens (decode steps, short chunks): small windows, so that more CTAs share
+    // them.  Many: windows of 128, whose look at the slots costs less per token.  8 KV
+    // heads, us in small and large windows: 256 sequences' step 2.6 / 3.7, 512 sequences'
+    // 3.4 / 4.0, a chunk of 512 in blocks of 16 3.6 / 4.7; two chunks of 256 in blocks of
+    // 256 6.5 / 5.2, four 7.2 / 6.4, 2000 sequences' step 7.8 / 5.9, a chunk of 4096 14.8 / 9.6.
+    const bool few = p.N <= 512;
     const int T = few ? 16 : 128;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -44,8 +44,8 @@
  *   - Tensors are dense row-major; bf16 data is passed as `const void *`.
  *     Every pointer must be 16-byte aligned.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
- *     pkv_store_kvcache, pkv_paged_attn_decode, pkv_paged_prefill and the FP8
- *     calls only enqueue work: they never synchronise the host and never
+ *     pkv_store_kvcache, pkv_paged_attn_decode, pkv_paged_prefill, the FP8 calls
+ *     and pkv_copy_blocks only enqueue work: they never synchronise the host and never
  *     allocate, so they can be captured into a CUDA graph.
  *   - Argument errors are reported by the return status before any launch;
  *     pkv_last_error() then gives a message.  Data errors found on the
@@ -466,7 +466,9 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
  *
  * A head or block of large values then costs no other one its small ones, and no
  * calibration is needed: the store sets the scales.  Attention takes any finite
- * scales > 0 within [2^-40, 2^40], a NaN scale makes what it touches NaN.
+ * scales > 0 within [2^-40, 2^40] (zeros are taken for blocks of zeros; a NaN scale
+ * makes what it touches NaN).  pkv_copy_blocks moves such blocks with their scales;
+ * the calls of a cache with a budget know of none and are not for these caches.
  */
 
 /*

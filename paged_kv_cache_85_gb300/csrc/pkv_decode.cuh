@@ -648,7 +648,9 @@ template <int D> __device__ __forceinline__ uint32_t box8_chunk(int t, int c)
 // ratio leaves [2^-7, 2^7] (with the running max's 2^8 that keeps P in f16's range,
 // and its rounding, subnormals included, below 2^-17 of the largest weight): O is
 // then rescaled.  Scales that are powers of two make every one of these products
-// exact but the last.
+// exact but the last.  (512 sequences, 759 MB: 137.8 us, 133.5 with one scale per tensor
+// on the same GPU, 137 without any arithmetic: bound by the memory's rate, 6.2 to 6.8 TB/s
+// once it runs, and some 10 us of ends.)
 template <int D, int G, int NW, int BT, bool WT, bool SC>
 __device__ __forceinline__ void decode_consumer_fp8(const DecodeParams &p, uint8_t *smem,
                                                     const DecodeSmem &L, int warp, int lane)

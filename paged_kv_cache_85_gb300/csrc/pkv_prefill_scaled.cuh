@@ -2,22 +2,40 @@
 //
 // What it computes, its work items, their order and splits, and its schedule are those
 // of pkv_prefill_wide.cuh (128-key tiles, one score buffer per query tile, P over S in
-// two halves, the MMA warps' lock).  What the codes change:
+// two halves, the MMA warps' lock).  What differs:
 //
 //  * Scores run on the E4M3 path with K as the raw codes, so a K tile is half the bytes
 //    and nobody converts it.  Q becomes two E4M3 parts, q = sq (high + low), once per
 //    item and row: two multiplications at twice the rate of bf16's one, in the same
-//    shared memory.  sq and K's scale join the softmax scale of a row; where the boxes of
-//    a tile have different scales, every box's scores are multiplied by theirs first.
+//    shared memory.  A key's multiplier inside the exponential is the softmax scale times
+//    its row's sq times its 16-token box's K scale: no score is scaled on its own.
 //  * V's codes become f16, times their block's scale over a unit in which O is held, in
 //    buffers of their own (they are twice the codes' bytes).  With scales that are powers
 //    of two that product is exact.  The unit moves where a tile's largest scale leaves
 //    [2^-8, 2^7] of it; O is then rescaled with the running maximum.
-//  * The producer brings each box's scales beside its tile's copies: blocks two tiles
-//    ahead, scales one.
+//  * The producer, whose time is free, does what can be done once per tile: it loads
+//    each box's block two tiles ahead and its scales one, works out V's factors and the
+//    unit, and waits for V's f16 buffer, so that a softmax warp waits once per tile for
+//    all of that (each wait, met or not, is 100 to 180 cycles of its chain).
+//  * The instructions of a tile are few: the main path has no masks (a short loop writes
+//    -inf into the scores of the tiles that have some) and no second form for boxes of
+//    different scales, and the halves of a row's exponentials share theirs.  With forms
+//    for each, 32 KB of instructions, the warps waited for those: 815 -> 747 us below,
+//    394 -> 277 us for ragged prompts.
 //
 // Precision: Q's parts below; P and V in f16, fp32 sums.  A V value far below the tile's
 // largest scale is held to 2^-25 of that scale.
+//
+// Measured: 8 sequences of 2048 new tokens on up to 2048 (16 heads, 275 GFLOP) 249 us,
+// 1103 TFLOP/s, tensor pipe 50% busy; on 28672 each 1440 TFLOP/s; one chunk of 2048 on
+// 28672 (32 heads, 996 GFLOP) 747 us, 1333 TFLOP/s, 61%.  Bound by the chain of a query
+// tile (scores, maximum, exponentials, P.V, next scores: some 3000 cycles per 128 keys
+// against 2048 of MMA), and where items are short by their ends: Q's conversion 3600
+// cycles, the output 2200.
+// Not kept: sixteen softmax warps, with half of a row each (bookkeeping per warp: 962 us
+// for the chunk, 850 at the time); four warps for the conversions (1100, 996 at the
+// time); the lock passed on before the wait for P.V (774), or left out (816); 96 of a
+// row's 128 scores kept in registers (1048: instructions).
 //
 // Warps (352 threads): 0..3 softmax of query tile A, 4..7 of tile B (thread = row = TMEM
 // lane); 8 producer; 9, 10 the MMAs of tiles A and B.  TMEM as in pkv_prefill_wide.cuh.
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // lock in shared memory) with such a pair: a tile's MMAs then run back to
         // back while the other tile's softmax works.  Without it both tiles' MMAs
         // share the pipe, both softmax groups get their scores at the same time, and
-        // the pipe idles while both work (4707 cycles per pair of tiles and 128 keys).
+        // the pipe idles while both work (a long chunk 747 -> 816 us).
         // A K, V or Q stage is released by one arrival per query tile: V by this warp,
         // which waits for its P.V, K and Q by the softmax group as it finds S_t(j), or
         // by this warp, for a stage its tile does not read, once that stage's tile has

@@ -16,7 +16,13 @@
 // runs that start in a window of T tokens, for one KV head and K or V: it keeps a
 // batch of the rows that it reads in registers (those before the last batch are read
 // again, from L2), takes each run's maximum in shared memory, and writes.  So the
-// scale needs no second kernel and no workspace.  Bound by HBM (6 D bytes per token and head).
+// scale needs no second kernel and no workspace.
+//
+// Measured (8 KV heads, D = 128): 16384 tokens 22 us, 0.69 of the rate of a plain copy
+// for their 101 MB (in blocks of 16 25 us); a step of 256 sequences 2.6 us behind another
+// one.  Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an
+// SM, whose issue slots are 63% used.  Not kept: 16-byte loads, twice the lanes per row
+// (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 #include "pkv_quant.cuh"

@@ -103,8 +103,11 @@ pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget);
  * prompt).  Their full blocks are shared (one more reference each).  A last block
  * that is partly filled would be written by both, so the child gets a free block in
  * its place: pair[0], pair[1] receive the two ids, source and destination, for
- * pkv_copy_blocks, or -1, -1 where the last block is full.  Enqueue the copy before
- * either sequence's next store on the same stream.  Fails with PKV_ERR_INVALID_ARG
+ * pkv_copy_blocks, or -1, -1 where the last block is full.  Enqueue the copy behind
+ * the stores of the parent's tokens and before either sequence's next store, on the
+ * same stream.  Pairs of several forks may go into one copy, but not those of a child
+ * and of a fork of that child (its block would be written and read at once): copy
+ * the first before the second is enqueued.  Fails with PKV_ERR_INVALID_ARG
  * (unknown parent, existing child) or PKV_ERR_WORKSPACE (no free block, no host
  * memory), changing nothing.
  */
@@ -117,8 +120,9 @@ pkv_status pkv_bm_fork(pkv_block_manager *bm, int64_t parent_id, int64_t child_i
  * id is both, and what moves keeps its references, its place in every table and its
  * content hash; free blocks that moves overwrite lose theirs.  With more moves than
  * `cap` pairs nothing changes, *n says how many there are, and PKV_ERR_WORKSPACE is
- * returned.  Block tables and slots taken before are void; enqueue the copy before
- * any use of new ones on the same stream.
+ * returned.  Block tables and slots taken before are void; enqueue the copy, in a
+ * call of its own behind those of earlier forks, before any use of new ones on the
+ * same stream.
  */
 pkv_status pkv_bm_compact(pkv_block_manager *bm, int32_t *pairs, int64_t cap, int64_t *n);
 

@@ -143,7 +143,9 @@ class BlockManager:
 
         Returns int32 ``[n, 2]``, the (source, destination) of the last block where it is
         partly filled (n is 0 or 1): give it to ``copy_blocks`` with every tensor under the
-        block ids before either sequence's next store.
+        block ids, behind the stores of the parent's tokens and before either sequence's
+        next store.  Pairs of several forks may go into one call, but not those of a child
+        and of a fork of that child.
         """
         pair = np.empty((1, 2), dtype=np.int32)
         _check(self._lib, self._lib.pkv_bm_fork(self._h, int(parent_id), int(child_id), _ptr(pair)))
@@ -152,8 +154,8 @@ class BlockManager:
     def compact(self) -> np.ndarray:
         """Move the sequences' blocks to the lowest ids; returns the moves, int32 ``[n, 2]``.
 
-        Give them to ``copy_blocks`` before any use of the tables and slots as they are
-        now; those taken before are void.
+        Give them to ``copy_blocks``, in a call of their own behind those of earlier forks,
+        before any use of the tables and slots as they are now; those taken before are void.
         """
         pairs = np.empty((self.num_blocks, 2), dtype=np.int32)
         n = ctypes.c_int64()

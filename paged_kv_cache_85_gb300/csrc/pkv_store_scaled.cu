@@ -18,11 +18,11 @@
 // again, from L2), takes each run's maximum in shared memory, and writes.  So the
 // scale needs no second kernel and no workspace.
 //
-// Measured (8 KV heads, D = 128): 16384 tokens 22 us, 0.69 of the rate of a plain copy
-// for their 101 MB (in blocks of 16 25 us); a step of 256 sequences 2.6 us behind another
-// one.  Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an
+// Measured (8 KV heads, D = 128): 16384 tokens 22 us, in blocks of 256 or of 16, 0.67 of the
+// rate of a plain copy for their 101 MB; a step of 256 sequences 2.6 us behind another one.  Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an
 // SM, whose issue slots are 63% used.  Not kept: 16-byte loads, twice the lanes per row
-// (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26).
+// (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26),
+// 512 threads (25), K and V by one CTA (21.4, but 4096 tokens 15.6 for 10.8).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 #include "pkv_quant.cuh"
@@ -166,15 +166,15 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
     }
     if (n_runs == 0)
         return;
-    // how far the last run goes on behind the window, of what is seen
-    int end = T;
-#pragma unroll
-    for (int i = T / 32; i < SEEN / 32; i++) {
-        const int from = max(0, T - 32 * i);
-        const uint32_t stops = ~s_goes[i] & (FULL << from);
-        if (end == 32 * i + from)
-            end = stops ? 32 * i + __ffs(stops) - 1 : 32 * i + 32;
-    }
+    // how far the last run goes on behind the window, of what is seen (a lane per word)
+    static_assert(SEEN / 32 <= 32, "a lane per word");
+    uint32_t stops = lane < SEEN / 32 ? ~s_goes[lane] : 0u;
+    if (32 * lane < T)
+        stops = T - 32 * lane >= 32 ? 0u : stops & (FULL << (T - 32 * lane));
+    const uint32_t words = __ballot_sync(FULL, stops != 0u);
+    const int word = words ? __ffs(words) - 1 : 0;
+    const uint32_t stop = __shfl_sync(FULL, stops, word);
+    const int end = words ? 32 * word + __ffs(stop) - 1 : SEEN;
     if (tid < T) {
         const int run = slot >= 0 ? before + __popc(starts & (FULL >> (31 - lane))) - 1 : -1;
         s_run[tid] = (short)run;
@@ -336,12 +336,15 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
 template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStream_t stream)
 {
     // Few tokens (decode steps, short chunks): small windows, so that more CTAs share
-    // them.  Many: windows of 128, whose look at the slots costs less per token.  8 KV
+    // them.  More: windows of 128, whose look at the slots costs less per token.  8 KV
     // heads, us in small and large windows: 256 sequences' step 2.6 / 3.7, 512 sequences'
     // 3.4 / 4.0, a chunk of 512 in blocks of 16 3.6 / 4.7; two chunks of 256 in blocks of
     // 256 6.5 / 5.2, four 7.2 / 6.4, 2000 sequences' step 7.8 / 5.9, a chunk of 4096 14.8 / 9.6.
-    const bool few = p.N <= 512;
-    const int T = few ? 16 : 128;
+    // Where those of 128 are more than a round of CTAs (608), 256, in windows of 128 and of
+    // 256: a chunk of 8192 in blocks of 16 14.1 / 13.6, 32768 in blocks of 256 42.4 / 40.8, 16k
+    // tokens of ragged prompts in blocks of 16 24.1 / 21.8; of 4096 8.5 / 11.1.
+    const bool few = p.N <= 512, many = !few && p.N * p.Hkv > 40960;
+    const int T = few ? 16 : many ? 256 : 128;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -351,8 +354,9 @@ template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStrea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 16, 256, 1>, p)
-               : cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 128, 512, D / 32>, p);
+    return few    ? cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 16, 256, 1>, p)
+           : many ? cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 256, 512, D / 32>, p)
+                  : cudaLaunchKernelEx(&cfg, store_scaled_kernel<D, 128, 512, D / 32>, p);
 }
 
 cudaError_t launch_store_scaled(int D, const StoreScaledParams &p, cudaStream_t stream)

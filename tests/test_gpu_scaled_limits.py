@@ -172,6 +172,36 @@ def test_store_where_its_windows_change(pkv, N):
         np.testing.assert_array_equal(got.cpu().numpy()[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("N,Hkv,D,bs,runs", [
+    (5120, 8, 128, 16, "long"), (5121, 8, 128, 16, "long"), (5121, 8, 64, 256, "long"), (5300, 8, 128, 1024, "long"),
+    (2561, 16, 64, 48, "long"), (41000, 1, 128, 2048, "long"), (5633, 8, 128, 16, "one"), (5121, 8, 128, 32, "short"),
+])
+def test_store_of_many_tokens(pkv, N, Hkv, D, bs, runs):
+    """Both sides of 40960 rows of a head, where windows become larger: blocks that go on over several windows, that
+    start in each place of one, that are full, begun or continued; a block for every token; padding between."""
+    rng = np.random.default_rng(N + bs)
+    slots, blk = [], 0
+    while len(slots) < N:
+        first = int(rng.integers(0, bs)) if runs != "one" and rng.random() < 0.5 else 0
+        n = {"long": bs - first, "short": int(rng.integers(1, bs - first + 1)), "one": 1}[runs]
+        slots += list(range(blk * bs + first, blk * bs + first + n))
+        blk += 1
+        if rng.random() < 0.1:
+            slots += [-1] * int(rng.integers(1, 40))
+    slots = np.asarray(slots[:N])
+    order = rng.permutation(blk)
+    slots = np.where(slots >= 0, order[slots // bs] * bs + slots % bs, -1)
+    c = [rng.integers(0, 0x7F, (blk, bs, Hkv, D)).astype(np.uint8) for _ in range(2)]
+    s = [np.full((blk, Hkv), 2.0 ** -6, np.float32) for _ in range(2)]
+    t = [dev(x) for x in (*c, *s)]
+    k, v = (ref.bf16(rng.standard_normal((N, Hkv, D)) * 2.0 ** (3 * rng.standard_normal((N, Hkv, 1)))) for _ in range(2))
+    pkv.store_kvcache_scaled(dev(k), dev(v), *t, dev(slots))
+    for x, cc, ss in zip((k, v), c, s):
+        ref.store(x, cc, ss, slots)
+    for got, want in zip(t, c + s):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
 def test_queries_of_all_sizes(pkv):
     """Elements far below their row's largest, rows of zeros, of tiny and of huge numbers."""
     rng = np.random.default_rng(7)

@@ -19,8 +19,9 @@
 // scale needs no second kernel and no workspace.
 //
 // Measured (8 KV heads, D = 128): 16384 tokens 22 us, in blocks of 256 or of 16, 0.67 of the
-// rate of a plain copy for their 101 MB; a step of 256 sequences 2.6 us behind another one.  Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an
-// SM, whose issue slots are 60% used.  Not kept: 16-byte loads, twice the lanes per row
+// rate of a plain copy for their 101 MB; a step of 256 sequences 2.6 us behind another one.
+// Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an SM,
+// whose issue slots are 60% used.  Not kept: 16-byte loads, twice the lanes per row
 // (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26),
 // 512 threads (25), K and V by one CTA (21.4, but 4096 tokens 15.6 for 10.8).
 #include "pkv_kernels.h"

@@ -18,12 +18,12 @@
 // again, from L2), takes each run's maximum in shared memory, and writes.  So the
 // scale needs no second kernel and no workspace.
 //
-// Measured (8 KV heads, D = 128): 16384 tokens 22 us, in blocks of 256 or of 16, 0.67 of the
+// Measured (8 KV heads, D = 128): 16384 tokens 21.3 us, in blocks of 256 or of 16, 0.71 of the
 // rate of a plain copy for their 101 MB; a step of 256 sequences 2.6 us behind another one.
 // Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an SM,
 // whose issue slots are 60% used.  Not kept: 16-byte loads, twice the lanes per row
 // (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26),
-// 512 threads (25), K and V by one CTA (21.4, but 4096 tokens 15.6 for 10.8).
+// 512 threads (25), K and V by one CTA (4096 tokens 15.6 for 10.8).
 #include "pkv_kernels.h"
 #include "pkv_ptx.cuh"
 #include "pkv_quant.cuh"
@@ -156,17 +156,14 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
     if (lane == 0)
         s_start[warp] = starts;
     __syncthreads();
-    int before = 0, n_runs = 0, first = T;
-#pragma unroll
-    for (int i = 0; i < (T + 31) / 32; i++) {
-        const uint32_t s = s_start[i];
-        before += i < warp ? __popc(s) : 0;
-        n_runs += __popc(s);
-        if (s && first == T)
-            first = 32 * i + __ffs(s) - 1;
-    }
-    if (n_runs == 0)
+    const uint32_t begin = lane < WARPS ? s_start[lane] : 0u;
+    const uint32_t some = __ballot_sync(FULL, begin != 0u);
+    if (some == 0u)
         return;
+    const int n_runs = __reduce_add_sync(FULL, __popc(begin));
+    const int before = __reduce_add_sync(FULL, lane < warp ? __popc(begin) : 0);
+    const int at = __ffs(some) - 1;
+    const int first = 32 * at + __ffs(__shfl_sync(FULL, begin, at)) - 1;
     // how far the last run goes on behind the window, of what is seen (a lane per word)
     static_assert(SEEN / 32 <= 32, "a lane per word");
     uint32_t stops = lane < SEEN / 32 ? ~s_goes[lane] : 0u;
@@ -222,15 +219,13 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
     const int sub = tid / LPR, part = tid % LPR;
     const auto run_of = [&](int i) { return first + i < SEEN ? (int)s_run[first + i] : n_runs - 1; };
     const size_t stride = (size_t)p.Hkv * D * 2;
-    const uint8_t *src = (z ? p.x[1] : p.x[0]) + (row0 + sub) * stride + (size_t)h * D * 2 + part * 32;
+    const uint8_t *src = (z ? p.x[1] : p.x[0]) + row0 * stride + (size_t)h * D * 2 + part * 32;
     const bool aligned32 = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;  // of all or none
     Row16 held[HOLD];
-    const auto load = [&](int b0) {
+    const auto load = [&](int b0) {  // (behind the last row: that one again)
 #pragma unroll
         for (int u = 0; u < HOLD; u++) {
-            held[u] = Row16{};
-            if (b0 + u * RPP + sub < rows)
-                held[u] = load16(src + (size_t)(b0 + u * RPP) * stride, aligned32);
+            held[u] = load16(src + (size_t)min(b0 + u * RPP + sub, rows - 1) * stride, aligned32);
         }
     };
     load(0);
@@ -260,7 +255,7 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
             const int i = b0 + u * RPP;
             if (i >= rows)
                 break;
-            const int run = i + sub < rows ? run_of(i + sub) : of;  // (behind the last row: zeros)
+            const int run = run_of(min(i + sub, rows - 1));
             if (__any_sync(FULL, run != of)) {
                 flush();
                 top = 0;
@@ -342,8 +337,9 @@ template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStrea
     // 3.4 / 4.0, a chunk of 512 in blocks of 16 3.6 / 4.7; two chunks of 256 in blocks of
     // 256 6.5 / 5.2, four 7.2 / 6.4, 2000 sequences' step 7.8 / 5.9, a chunk of 4096 14.8 / 9.6.
     // Where those of 128 are more than a round of CTAs (608), 256, in windows of 128 and of
-    // 256: a chunk of 8192 in blocks of 16 14.1 / 13.6, 32768 in blocks of 256 42.4 / 40.8, 16k
-    // tokens of ragged prompts in blocks of 16 24.1 / 21.8; of 4096 8.5 / 11.1.
+    // 256: a chunk of 4096 in blocks of 16 8.4 / 10.8, of 6144 11.8 / 11.8, of 8192 14.0 / 13.4,
+    // 16k tokens of ragged prompts 23.6 / 21.2, 32768 in blocks of 256 41.0 / 40.2 (16384 that
+    // begin inside theirs 20.9 / 21.2).
     const bool few = p.N <= 512, many = !few && p.N * p.Hkv > 40960;
     const int T = few ? 16 : many ? 256 : 128;
     cudaLaunchConfig_t cfg = {};

@@ -525,10 +525,14 @@ pkv_status pkv_paged_attn_decode_scaled(const void *q, const void *k_cache, cons
  *
  * Precision: scores on the tensor cores in E4M3 with fp32 accumulation, K as its
  * codes and q in two parts, exact for elements of magnitude >= max|q| 2^-9 of their
- * row and within max|q| 2^-17 for the rest; P . V in f16 with fp32 accumulation, V =
- * code_value * scale rounded to f16 relative to the larger scales of its 128-token
- * tile (absolute error <= 2^-25 of them; none where scales are powers of two within
- * 2^13 of each other).  An infinite element of q makes its row NaN.
+ * row and within max|q| 2^-17 for the rest.  P . V in f16 with fp32 accumulation.
+ * Where the V scales of a 128-token tile lie within 2^13 of each other, V =
+ * code_value * scale is exact for powers of two (else rounded twice, by 2^-11 of
+ * itself) and a weight is rounded by 2^-11 of itself or 2^-25 of the row's largest.
+ * Where they lie further apart, the part of a scale that V does not take multiplies
+ * the weight before that rounding: a row keeps the values of the blocks that its
+ * weight lies on, whatever the scales of others.  An infinite element of q makes its
+ * row NaN.
  */
 size_t pkv_prefill_scaled_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
                                           int D, int MBS, int bs);

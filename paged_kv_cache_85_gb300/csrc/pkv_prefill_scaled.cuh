@@ -9,10 +9,17 @@
 //    item and row: two multiplications at twice the rate of bf16's one, in the same
 //    shared memory.  A key's multiplier inside the exponential is the softmax scale times
 //    its row's sq times its 16-token box's K scale: no score is scaled on its own.
-//  * V's codes become f16, times their block's scale over a unit in which O is held, in
+//  * V's codes become f16, times f = their block's scale over a unit in which O is held, in
 //    buffers of their own (they are twice the codes' bytes).  With scales that are powers
-//    of two that product is exact.  The unit moves where a tile's largest scale leaves
-//    [2^-8, 2^7] of it; O is then rescaled with the running maximum.
+//    of two that product is exact, f being kept within [2^-15, 2^7] (codes end at 2^-9, f16
+//    at 2^-24).  The unit, a power of two, moves where a tile's largest scale leaves
+//    [2^-2, 2^7) of it; O is then rescaled with the running maximum.  Of a scale below
+//    2^-15 units the rest, g = 2^-1, 2^-2, ..., joins the weights: its scores are moved by
+//    log2 g before the running maximum sees them, P holds w g, and the sum gets its
+//    w = (w g) / g.  So a row whose weight lies on a block of small scale keeps it, whatever
+//    the other blocks hold.  Rows that see no larger block of such a tile (it is in their
+//    future) hold O in a unit of their own.  A tile with such a block costs two more loops
+//    over its scores; no other tile knows of it.
 //  * The producer, whose time is free, does what can be done once per tile: it loads
 //    each box's block two tiles ahead and its scales one, works out V's factors and the
 //    unit, and waits for V's f16 buffer, so that a softmax warp waits once per tile for
@@ -23,8 +30,10 @@
 //    for each, 32 KB of instructions, the warps waited for those: 815 -> 747 us below,
 //    394 -> 277 us for ragged prompts.
 //
-// Precision: Q's parts below; P and V in f16, fp32 sums.  A V value far below the tile's
-// largest scale is held to 2^-25 of that scale.
+// Precision: Q's parts below; P and V in f16, fp32 sums.  Where V's scales of a tile lie
+// within 2^13 of each other, V is exact for powers of two (else rounded twice, 2^-11 each)
+// and w rounded by 2^-11 of itself or 2^-25 of the row's largest.  Elsewhere w g is, by
+// 2^-11 of itself or 2^-25 of the row's largest w g.
 //
 // Measured: 8 sequences of 2048 new tokens on up to 2048 (16 heads, 275 GFLOP) 249 us,
 // 1103 TFLOP/s, tensor pipe 50% busy; on 28672 each 1440 TFLOP/s; one chunk of 2048 on
@@ -64,10 +73,13 @@ constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 
 
 // What the softmax warps need of a key tile beside its codes; the producer brings it with
 // V's.  read: which of the eight boxes are read (a bit each).  k: their K scales (1 where
-// they are not read).  v: V's scales over `unit`, in which O is held, as pairs of f16.
+// they are not read).  V's scales are `unit` f g: v = f, as pairs of f16, and lg = log2 g,
+// 0 but in tiles with kFarApart in `read`.
+constexpr int kFarApart = 0x10000;
 struct __align__(16) TileScales {
     float k[kSKeys / kBox];
     uint32_t v[kSKeys / kBox];
+    float lg[kSKeys / kBox];
     int read;
     float unit;
     int pad[2];
@@ -115,6 +127,15 @@ __device__ __forceinline__ void store32(void *to, const uint32_t *v, bool aligne
         d[0] = make_uint4(v[0], v[1], v[2], v[3]);
         d[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
+}
+
+// 2^e of a whole e within [-126, 127].
+__device__ __forceinline__ float exp2_int(float e) { return __uint_as_float((uint32_t)(127 + (int)e) << 23); }
+
+// a / b for powers of two whose quotient is within that range.
+__device__ __forceinline__ float exp2_ratio(float a, float b)
+{
+    return __uint_as_float(0x3f800000u + __float_as_uint(a) - __float_as_uint(b));
 }
 
 // Eight E4M3 codes times f (a pair of f16) as eight f16.
@@ -342,9 +363,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int blk = entry(0), blk_next = entry(1);
             float sk = scale_of(p.k_scales, blk), sv = scale_of(p.v_scales, blk);
             const int per = p.copy_rows;  // tokens per copy: so many lie in one block
-            // V tiles' unit: moves to a tile's largest scale where that is 2^7 above it
-            // (448 * 2^7 is within f16) or 2^8 below (where f16 begins to lose bits)
-            float unit = 1.f, per_unit = 1.f;
+            // V tiles' unit, 2^(unit - 127): moves to 2^-2 of a tile's largest scale where
+            // that is not below 2^7 units (448 * 2^7 is within f16) or below 2^-2 (2^13 above
+            // the least f)
+            int unit = 127;
             for (int j = 0; j < nkt; j++) {
                 const int key0 = (j0 + j) * kSKeys + lane * kBox;
                 int row = -1;
@@ -357,13 +379,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t read = __ballot_sync(FULL, row >= 0);
                 // (a masked score is -inf, which no scale may turn into NaN)
                 const float k = row < 0 ? 1.f : sk == 0.f ? 0x1p-40f : sk;
-                const float most = __uint_as_float(__reduce_max_sync(
-                    FULL, row >= 0 && sv > 0.f && sv < INFINITY ? __float_as_uint(sv) : 0u));
-                if (most > 0.f && (j == 0 || most > unit * 0x1p7f || most < unit * 0x1p-8f)) {
-                    unit = most;
-                    per_unit = 1.f / most;
-                }
-                const uint32_t factor = pack_f16x2(sv * per_unit, sv * per_unit);
+                const uint32_t bits = row >= 0 && sv > 0.f && sv < INFINITY ? __float_as_uint(sv) : 0u;
+                const int most = (int)(__reduce_max_sync(FULL, bits) >> 23);
+                if (most > 0 && (j == 0 || most - unit >= 7 || most - unit < -2))
+                    unit = max(most - 2, 1);
+                const int e = bits ? (int)(bits >> 23) - unit : 0;
+                const float f = bits ? __uint_as_float((bits & 0x7fffffu) | (uint32_t)(127 + max(e, -15)) << 23)
+                                     : sv * 0.f;  // 0, or NaN
+                const uint32_t factor = pack_f16x2(f, f);
+                const int lg = min(e + 15, 0), least = __reduce_min_sync(FULL, lg);
                 // the next tile's, whose loads run while this one's stages are waited for
                 blk = blk_next;
                 sk = scale_of(p.k_scales, blk);
@@ -394,10 +418,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane < kBoxes) {
                     ts.k[lane] = k;
                     ts.v[lane] = factor;
+                    // (a block of zeros has the least one, so that its weights are not the
+                    // larger ones of a row in a unit of its own)
+                    ts.lg[lane] = (float)(bits ? lg : least);
                 }
                 if (lane == 0) {
-                    ts.read = (int)read;
-                    ts.unit = unit;
+                    ts.read = (int)read | (least < 0 ? kFarApart : 0);
+                    ts.unit = __uint_as_float((uint32_t)unit << 23);
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -594,9 +621,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int pos = (it.k_len - it.q_len) + tok;
             const int k_len = it.k_len;
             float m = -INFINITY, l = 0.f;
-            // of the next key tile's codes, and of O
+            // of the next key tile's codes, and of this row's O
             float unit = 1.f, o_unit = 1.f;
-            uint32_t boxes = 0;  // of the next key tile, those that are read
+            uint32_t boxes = 0;  // of the next key tile, those that are read; kFarApart
             // Key tile j's scales, and this group's half (64 keys) of its V: codes -> f16 in
             // the other buffer, times their box's factor, rows past k_len or of boxes that
             // are not read zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups
@@ -662,9 +689,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 top &= 0x7fff7fffu;
                 top = max(top & 0xffffu, top >> 16);
                 const int ebits = min(max((int)(top >> 7), 8), 254);
-                // (not so small that it or its product with a K scale is 0, which times a masked
-                // score, -inf, would be NaN: no score that small moves a weight)
-                sl = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23), 1e-25f);
+                // (not so small that its product with a K scale is 0, which times a masked score,
+                // -inf, would be NaN, or that log2 g over it is infinite: no score that small moves
+                // a weight)
+                sl = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(ebits - 7) << 23), 1e-24f);
                 if (top == 0x7f80u)
                     sl = NAN;
                 float inv = __uint_as_float((uint32_t)(261 - ebits) << 23);
@@ -725,6 +753,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         mbar_arrive(&q_empty[tq]);
                 }
                 const int key_base = (j0 + j) * kSKeys;
+                const TileScales &ts = scales[(g0 + j) % kSScales];
+                // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1) completed, and
+                // the next P.V waits for this group's P
+                auto rescale = [&](float by) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; cc++) {
+                        uint32_t ro[32];
+                        tc::ld32(tO + 32 * cc, ro);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            ro[i] = __float_as_uint(__uint_as_float(ro[i]) * by);
+                        tc::st32(tO + 32 * cc, ro);
+                    }
+                    tc::wait_st();
+                };
                 // Masked keys, past their row's position (the diagonal tiles) or in a box that
                 // is not read: -inf into the scores, so that what follows knows of none.  Most
                 // tiles have none in the whole warp; of its own and short, because the
@@ -745,9 +789,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::st16(tS + kBox * b, r);
                     }
                     tc::wait_st();
+                    // V's scales far apart: log2 g joins the scores, 2^shift g in a unit of the
+                    // row's own.  The running maximum follows at once, so that the sum, which is
+                    // of w, can be given (w g) / g - w g beyond what it gets below.
+                    if (__builtin_expect(boxes & kFarApart, 0)) {
+                        float seen = -INFINITY;
+#pragma unroll 1
+                        for (int b = 0; b < kBoxes; b++)
+                            if (((boxes >> b) & 1u) && lim >= kBox * b && ts.v[b])
+                                seen = fmaxf(seen, ts.lg[b]);
+                        const float shift = seen > -INFINITY ? -seen : 0.f;
+                        unit *= exp2_int(-shift);
+                        float mn = m;
+#pragma unroll 1
+                        for (int b = 0; b < kBoxes; b++) {
+                            const float c = sl * ts.k[b], move = (ts.lg[b] + shift) / c;
+                            uint32_t r[16];
+                            tc::ld16(tS + kBox * b, r);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < kBox; i++) {
+                                const float moved = __uint_as_float(r[i]) + move;
+                                mn = fmaxf(mn, moved * c);
+                                r[i] = __float_as_uint(moved);
+                            }
+                            tc::st16(tS + kBox * b, r);
+                        }
+                        tc::wait_st();
+                        const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+                        if (j > 0)
+                            rescale(alpha * exp2_ratio(o_unit, unit));
+                        o_unit = unit;
+                        m = mn;
+                        l *= alpha;
+                        const float nmu = m == -INFINITY ? 0.f : -m;
+#pragma unroll 1
+                        for (int b = 0; b < kBoxes; b++) {
+                            uint32_t r[16];
+                            tc::ld16(tS + kBox * b, r);
+                            tc::wait_ld();
+                            const float c = sl * ts.k[b];
+                            float e = 0.f;
+#pragma unroll
+                            for (int i = 0; i < kBox; i++)
+                                e += fast_exp2(fmaf(__uint_as_float(r[i]), c, nmu));
+                            l = fmaf(exp2_int(-ts.lg[b] - shift) - 1.f, e, l);
+                        }
+                    }
                 }
                 // K's scales of the tile's boxes join the row's
-                const float *ks = scales[(g0 + j) % kSScales].k;
+                const float *ks = ts.k;
                 float x[64];
                 auto load = [&](int half) {
                     uint32_t a[32], b[32];
@@ -776,27 +867,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 load(1);
                 mraw = top(1, mraw);
                 const float mx = mraw * sl;
-                const bool moves = __any_sync(FULL, mx > m + kLazy);
-                if (moves || unit != o_unit) {
-                    const float mn = moves ? fmaxf(m, mx) : m;
-                    const float alpha = !moves || mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-                    const float o_alpha = unit == o_unit ? alpha : alpha * (o_unit / unit);
+                if (__any_sync(FULL, mx > m + kLazy || unit != o_unit)) {
+                    const float mn = fmaxf(m, mx);
+                    const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+                    const float o_alpha = alpha * exp2_ratio(o_unit, unit);
                     o_unit = unit;
-                    if (j > 0) {
-                        // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1)
-                        // completed, and the next P.V waits for this group's P
-#pragma unroll 1
-                        for (int cc = 0; cc < D / 32; cc++) {
-                            uint32_t ro[32];
-                            tc::ld32(tO + 32 * cc, ro);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i++)
-                                ro[i] = __float_as_uint(__uint_as_float(ro[i]) * o_alpha);
-                            tc::st32(tO + 32 * cc, ro);
-                        }
-                        tc::wait_st();
-                    }
+                    if (j > 0)
+                        rescale(o_alpha);
                     l *= alpha;
                     m = mn;
                 }
@@ -839,7 +916,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     exponentiate(h, tS + 96 * h);
                     hand_over(h);
                 }
-                l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+                l += (ls0.x + ls0.y) + (ls1.x + ls1.y) ;
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
                 if (j + 1 < all && !(ok = convert_v(j + 1)))
                     break;

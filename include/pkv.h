@@ -467,8 +467,9 @@ pkv_status pkv_evict_kvcache(void *k_cache, void *v_cache, float *weights,
  * A head or block of large values then costs no other one its small ones, and no
  * calibration is needed: the store sets the scales.  Attention takes any finite
  * scales > 0 within [2^-40, 2^40] (zeros are taken for blocks of zeros; a NaN scale
- * makes what it touches NaN).  pkv_copy_blocks moves such blocks with their scales;
- * the calls of a cache with a budget know of none and are not for these caches.
+ * makes NaN the outputs of the queries that see a token of its block, and no others).
+ * pkv_copy_blocks moves such blocks with their scales; the calls of a cache with a
+ * budget know of none and are not for these caches.
  */
 
 /*

@@ -72,9 +72,9 @@ static_assert(kSScales >= kSRStages + 2, "a tile's scales outlive its stage");
 constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
 
 // What the softmax warps need of a key tile beside its codes; the producer brings it with
-// V's.  read: which of the eight boxes are read (a bit each).  k: their K scales (1 where
-// they are not read).  V's scales are `unit` f g: v = f, as pairs of f16, and lg = log2 g,
-// 0 but in tiles with kFarApart in `read`.
+// V's.  read: which of the eight boxes are read (a bit each), above them which have a scale
+// that is NaN, and kFarApart.  k: their K scales (1 where there is none).  V's scales are `unit` f g: v = f, as pairs of f16, and lg = log2 g,
+// 0 but in tiles with kFarApart.
 constexpr int kFarApart = 0x10000;
 struct __align__(16) TileScales {
     float k[kSKeys / kBox];
@@ -149,6 +149,98 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(uint32_t a, uint32_t b, uint32_t 
     r.z = f16x2_mul(r.z, f);
     r.w = f16x2_mul(r.w, f);
     return r;
+}
+
+// O (a row per thread) times a number per row.  In place while P . V rests: S_t(j) was
+// issued after P.V_t(j - 1) completed, and the next P.V waits for this group's P.
+template <int D> __device__ __forceinline__ void rescale_o(uint32_t tO, float by)
+{
+#pragma unroll 1
+    for (int cc = 0; cc < D / 32; cc++) {
+        uint32_t ro[32];
+        tc::ld32(tO + 32 * cc, ro);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+            ro[i] = __float_as_uint(__uint_as_float(ro[i]) * by);
+        tc::st32(tO + 32 * cc, ro);
+    }
+    tc::wait_st();
+}
+
+// A row's running maximum and sum, the unit of the tile at hand and the one its O is in.
+struct RowState {
+    float m, l, unit, o_unit;
+};
+
+// What a tile asks of its scores (masked ones are -inf already) where it has scales that
+// are NaN or V's far apart.  NaN: into the scores that are seen in their boxes.  Far apart:
+// log2 g joins the scores, 2^shift g in a unit of the row's own; the running maximum follows
+// at once, so that the sum, which is of w, can be given the (w g) / g - w g that it lacks
+// when w g is added to it.  lim: the last key of the tile that the row sees.  Out of line,
+// for the instructions of what always runs barely fit the caches (inline ragged 278 us, long
+// chunk 769; so 274, 761).
+template <int D>
+__device__ __noinline__ RowState odd_scales(uint32_t tS, uint32_t tO, const TileScales &ts, uint32_t boxes, int lim,
+                                            float sl, RowState s, bool has_o)
+{
+    constexpr int kBoxes = kSKeys / kBox;
+    uint32_t r[16];
+#pragma unroll 1
+    for (int b = 0; b < kBoxes; b++) {
+        if (!((boxes >> (kBoxes + b)) & 1u))
+            continue;
+        tc::ld16(tS + kBox * b, r);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < kBox; i++)
+            r[i] = kBox * b + i > lim ? r[i] : 0x7fffffffu;
+        tc::st16(tS + kBox * b, r);
+    }
+    tc::wait_st();
+    if (!(boxes & kFarApart))
+        return s;
+    float seen = -INFINITY;
+#pragma unroll 1
+    for (int b = 0; b < kBoxes; b++)
+        if (((boxes >> b) & 1u) && lim >= kBox * b && ts.v[b])
+            seen = fmaxf(seen, ts.lg[b]);
+    const float shift = seen > -INFINITY ? -seen : 0.f;
+    s.unit *= exp2_int(-shift);
+    float mn = s.m;
+#pragma unroll 1
+    for (int b = 0; b < kBoxes; b++) {
+        const float c = sl * ts.k[b], move = (ts.lg[b] + shift) / c;
+        tc::ld16(tS + kBox * b, r);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < kBox; i++) {
+            const float moved = __uint_as_float(r[i]) + move;
+            mn = fmaxf(mn, moved * c);
+            r[i] = __float_as_uint(moved);
+        }
+        tc::st16(tS + kBox * b, r);
+    }
+    tc::wait_st();
+    const float alpha = mn == -INFINITY ? 1.f : fast_exp2(s.m - mn);
+    if (has_o)
+        rescale_o<D>(tO, alpha * exp2_ratio(s.o_unit, s.unit));
+    s.o_unit = s.unit;
+    s.m = mn;
+    s.l *= alpha;
+    const float nm = mn == -INFINITY ? 0.f : -mn;
+#pragma unroll 1
+    for (int b = 0; b < kBoxes; b++) {
+        tc::ld16(tS + kBox * b, r);
+        tc::wait_ld();
+        const float c = sl * ts.k[b];
+        float e = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBox; i++)
+            e += fast_exp2(fmaf(__uint_as_float(r[i]), c, nm));
+        s.l = fmaf(exp2_int(-ts.lg[b] - shift) - 1.f, e, s.l);
+    }
+    return s;
 }
 
 // SPLIT: p.splits > 1.  Of its own, for the others' items are 4% slower with it
@@ -377,15 +469,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         flag_error(p.err_flag, 0x2 /* PKV_FLAG_BAD_BLOCK */);
                 }
                 const uint32_t read = __ballot_sync(FULL, row >= 0);
-                // (a masked score is -inf, which no scale may turn into NaN)
-                const float k = row < 0 ? 1.f : sk == 0.f ? 0x1p-40f : sk;
-                const uint32_t bits = row >= 0 && sv > 0.f && sv < INFINITY ? __float_as_uint(sv) : 0u;
+                // A scale that is none (NaN) makes NaN the rows that see its box and no others,
+                // so it goes into their scores, and what stands here is harmless.  (A masked
+                // score is -inf, which no K scale may turn into NaN: zero neither.)
+                const bool scaled = row >= 0 && sk >= 0.f && sk < INFINITY && sv >= 0.f && sv < INFINITY;
+                const uint32_t broken = read & ~__ballot_sync(FULL, scaled);
+                const float k = !scaled ? 1.f : sk == 0.f ? 0x1p-40f : sk;
+                const uint32_t bits = scaled && sv > 0.f ? __float_as_uint(sv) : 0u;
                 const int most = (int)(__reduce_max_sync(FULL, bits) >> 23);
                 if (most > 0 && (j == 0 || most - unit >= 7 || most - unit < -2))
                     unit = max(most - 2, 1);
                 const int e = bits ? (int)(bits >> 23) - unit : 0;
-                const float f = bits ? __uint_as_float((bits & 0x7fffffu) | (uint32_t)(127 + max(e, -15)) << 23)
-                                     : sv * 0.f;  // 0, or NaN
+                const float f =
+                    bits ? __uint_as_float((bits & 0x7fffffu) | (uint32_t)(127 + max(e, -15)) << 23) : 0.f;
                 const uint32_t factor = pack_f16x2(f, f);
                 const int lg = min(e + 15, 0), least = __reduce_min_sync(FULL, lg);
                 // the next tile's, whose loads run while this one's stages are waited for
@@ -423,7 +519,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ts.lg[lane] = (float)(bits ? lg : least);
                 }
                 if (lane == 0) {
-                    ts.read = (int)read | (least < 0 ? kFarApart : 0);
+                    ts.read = (int)(read | broken << 8) | (least < 0 ? kFarApart : 0);
                     ts.unit = __uint_as_float((uint32_t)unit << 23);
                 }
                 __syncwarp();
@@ -623,7 +719,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.f;
             // of the next key tile's codes, and of this row's O
             float unit = 1.f, o_unit = 1.f;
-            uint32_t boxes = 0;  // of the next key tile, those that are read; kFarApart
+            uint32_t boxes = 0;  // `read` of the next key tile
             // Key tile j's scales, and this group's half (64 keys) of its V: codes -> f16 in
             // the other buffer, times their box's factor, rows past k_len or of boxes that
             // are not read zeroed (their weight is 0, and 0 * NaN would be NaN).  Both groups
@@ -754,21 +850,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 const int key_base = (j0 + j) * kSKeys;
                 const TileScales &ts = scales[(g0 + j) % kSScales];
-                // O holds P_0..P_{j-1} V: S_t(j) was issued after P.V_t(j - 1) completed, and
-                // the next P.V waits for this group's P
-                auto rescale = [&](float by) {
-#pragma unroll 1
-                    for (int cc = 0; cc < D / 32; cc++) {
-                        uint32_t ro[32];
-                        tc::ld32(tO + 32 * cc, ro);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            ro[i] = __float_as_uint(__uint_as_float(ro[i]) * by);
-                        tc::st32(tO + 32 * cc, ro);
-                    }
-                    tc::wait_st();
-                };
                 // Masked keys, past their row's position (the diagonal tiles) or in a box that
                 // is not read: -inf into the scores, so that what follows knows of none.  Most
                 // tiles have none in the whole warp; of its own and short, because the
@@ -789,52 +870,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::st16(tS + kBox * b, r);
                     }
                     tc::wait_st();
-                    // V's scales far apart: log2 g joins the scores, 2^shift g in a unit of the
-                    // row's own.  The running maximum follows at once, so that the sum, which is
-                    // of w, can be given (w g) / g - w g beyond what it gets below.
-                    if (__builtin_expect(boxes & kFarApart, 0)) {
-                        float seen = -INFINITY;
-#pragma unroll 1
-                        for (int b = 0; b < kBoxes; b++)
-                            if (((boxes >> b) & 1u) && lim >= kBox * b && ts.v[b])
-                                seen = fmaxf(seen, ts.lg[b]);
-                        const float shift = seen > -INFINITY ? -seen : 0.f;
-                        unit *= exp2_int(-shift);
-                        float mn = m;
-#pragma unroll 1
-                        for (int b = 0; b < kBoxes; b++) {
-                            const float c = sl * ts.k[b], move = (ts.lg[b] + shift) / c;
-                            uint32_t r[16];
-                            tc::ld16(tS + kBox * b, r);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < kBox; i++) {
-                                const float moved = __uint_as_float(r[i]) + move;
-                                mn = fmaxf(mn, moved * c);
-                                r[i] = __float_as_uint(moved);
-                            }
-                            tc::st16(tS + kBox * b, r);
-                        }
-                        tc::wait_st();
-                        const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-                        if (j > 0)
-                            rescale(alpha * exp2_ratio(o_unit, unit));
-                        o_unit = unit;
-                        m = mn;
-                        l *= alpha;
-                        const float nmu = m == -INFINITY ? 0.f : -m;
-#pragma unroll 1
-                        for (int b = 0; b < kBoxes; b++) {
-                            uint32_t r[16];
-                            tc::ld16(tS + kBox * b, r);
-                            tc::wait_ld();
-                            const float c = sl * ts.k[b];
-                            float e = 0.f;
-#pragma unroll
-                            for (int i = 0; i < kBox; i++)
-                                e += fast_exp2(fmaf(__uint_as_float(r[i]), c, nmu));
-                            l = fmaf(exp2_int(-ts.lg[b] - shift) - 1.f, e, l);
-                        }
+                    if (__builtin_expect(boxes >> kBoxes, 0)) {
+                        const RowState now = odd_scales<D>(tS, tO, ts, boxes, lim, sl, {m, l, unit, o_unit}, j > 0);
+                        m = now.m;
+                        l = now.l;
+                        unit = now.unit;
+                        o_unit = now.o_unit;
                     }
                 }
                 // K's scales of the tile's boxes join the row's
@@ -873,7 +914,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float o_alpha = alpha * exp2_ratio(o_unit, unit);
                     o_unit = unit;
                     if (j > 0)
-                        rescale(o_alpha);
+                        rescale_o<D>(tO, o_alpha);
                     l *= alpha;
                     m = mn;
                 }
@@ -916,7 +957,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     exponentiate(h, tS + 96 * h);
                     hand_over(h);
                 }
-                l += (ls0.x + ls0.y) + (ls1.x + ls1.y) ;
+                l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
                 // off the chain: V tile j + 1 while P.V_t(j) and S_t(j + 1) run
                 if (j + 1 < all && !(ok = convert_v(j + 1)))
                     break;

@@ -20,6 +20,11 @@
 //    the other blocks hold.  Rows that see no larger block of such a tile (it is in their
 //    future) hold O in a unit of their own.  A tile with such a block costs two more loops
 //    over its scores; no other tile knows of it.
+//  * A NaN in V's codes would reach every row of its item through a weight of 0 (the rows
+//    that do not see its token).  Nothing looks for one but an item's end, where an element
+//    of O is NaN and the row's sum is not: the item is then done again, its codes brought
+//    without NaN, and NaN written where a row sees one.  (Codes looked at as they are
+//    converted: 16k 253, ragged 283, long chunk 773 us; so 251, 280, 762.)
 //  * The producer, whose time is free, does what can be done once per tile: it loads
 //    each box's block two tiles ahead and its scales one, works out V's factors and the
 //    unit, and waits for V's f16 buffer, so that a softmax warp waits once per tile for
@@ -86,7 +91,7 @@ struct __align__(16) TileScales {
 };
 
 struct ScaledSmem {
-    size_t q, k, r, v, scales, bars, items, slot, total;
+    size_t q, k, r, v, scales, bars, items, nans, slot, total;
 };
 
 __host__ __device__ inline ScaledSmem scaled_smem_layout(int D)
@@ -107,6 +112,9 @@ __host__ __device__ inline ScaledSmem scaled_smem_layout(int D)
     o += 8 * kSBars;
     L.items = align_up(o, 16);  // two published work items
     o = L.items + 2 * sizeof(WideItem);
+    L.nans = o;  // of the two items: whether it has to be done again, then per column the
+    o += 2 * (1 + D) * sizeof(int);  // first token (of the sequence) whose V is NaN
+    o = align_up(o, 16);
     L.slot = o;  // TMEM base, and the MMA warps' lock
     o += 16;
     L.total = align_up(o, 16) + 1024;
@@ -243,6 +251,44 @@ __device__ __noinline__ RowState odd_scales(uint32_t tS, uint32_t tO, const Tile
     return s;
 }
 
+// A tile of V's codes, brought by the producer's warp itself: 0 for NaN, whose token is noted
+// for its column.  codes: of the KV head; row: of lane i, where box i's tokens lie (-1: not read).
+template <int D>
+__device__ __noinline__ void clean_codes(uint8_t *to, const uint8_t *codes, int Hkv, int row, int key0, int k_len,
+                                         int *nan_from, int lane)
+{
+    constexpr int kPieces = D / 16;
+#pragma unroll 1
+    for (int i = lane; i < kSKeys * kPieces; i += 32) {
+        const int r = i / kPieces, piece = i % kPieces;
+        const int first = __shfl_sync(0xffffffffu, row, r / kBox);
+        if (first < 0 || key0 + r >= k_len)
+            continue;  // (cleared as it is converted)
+        uint4 w = *reinterpret_cast<const uint4 *>(codes + (size_t)(first + r % kBox) * Hkv * D + 16 * piece);
+        uint8_t *c = reinterpret_cast<uint8_t *>(&w);
+#pragma unroll 1
+        for (int d = 0; d < 16; d++)
+            if ((c[d] & 0x7f) == 0x7f) {
+                c[d] = 0;
+                atomicMin(nan_from + 16 * piece + d, key0 + r);
+            }
+        // swizzled as a copy would be
+        const int at = D == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3);
+        *reinterpret_cast<uint4 *>(to + r * D + 16 * at) = w;
+    }
+    fence_proxy_async_smem();  // the next copy into the stage is behind these
+    __syncwarp();
+}
+
+// NaN into the columns of an output row that see one.
+template <int D, typename T> __device__ __noinline__ void write_nans(T *out, T nan, const int *nan_from, int pos)
+{
+#pragma unroll 1
+    for (int d = 0; d < D; d++)
+        if (nan_from[d] <= pos)
+            out[d] = nan;
+}
+
 // SPLIT: p.splits > 1.  Of its own, for the others' items are 4% slower with it
 // where they are short.
 template <int D, int G, bool SPLIT>
@@ -288,6 +334,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     WideItem *items = reinterpret_cast<WideItem *>(smem + L.items);
     uint8_t *sQ = smem + L.q, *sK = smem + L.k, *sR = smem + L.r, *sV = smem + L.v;
     TileScales *scales = reinterpret_cast<TileScales *>(smem + L.scales);
+    int *again = reinterpret_cast<int *>(smem + L.nans);  // [2]
+    int *nan_from = again + 2;                            // [2][D]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_launch_dependents();
@@ -318,6 +366,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(mma_done, 2);
         *turn.word = 0;
+        again[0] = again[1] = 0;
         fence_mbarrier_init();
     } else if (warp == kTcMmaWarp) {
         tc::alloc(smem_u32(slot), kTcCols);
@@ -344,10 +393,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int n = 0;                // items published
         int k = 0;                // walk rounds
         for (;;) {
-            // ---- the next item with work (round k: forward, then backward), or the end
+            // ---- slot n & 1, once the item two back is done with it
+            const int sl = n & 1;
+            if (n >= 2 && !__all_sync(FULL, mbar_wait_asleep(&item_free[sl], ((n >> 1) & 1) ^ 1))) {
+                ok = false;
+                break;  // the other warps time out on item_ready and stop
+            }
+            // ---- that item again, if its V held NaN; else the next item with work (round k:
+            // forward, then backward), or the end
             WideItem item{{-1, 0, 0, 0, 0, 0, {0, 0}}, 0, 0, 0, 0};
             PrefillItem &it = item.f;
-            for (; ok; k++) {
+            bool repeat = again[sl] != 0;
+            for (; !repeat; k++) {
                 const long long at = (long long)k * nC + ((k & 1) ? nC - 1 - c : c);
                 if (at >= units)
                     break;
@@ -407,13 +464,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 }
             }
-            // ---- publish it in slot n & 1, once the item two back is done with it
-            const int sl = n & 1;
-            if (n >= 2 && !(ok = ok && __all_sync(FULL, mbar_wait_asleep(&item_free[sl], ((n >> 1) & 1) ^ 1))))
-                break;  // the other warps time out on item_ready and stop
-            if (!ok)
-                it.b = -1;
+            // ---- before the end, the last item may ask for it too
+            int from = sl;
+            if (!repeat && it.b < 0 && n >= 1) {
+                from = sl ^ 1;
+                if (!(ok = __all_sync(FULL, mbar_wait_asleep(&item_free[from], ((n - 1) >> 1) & 1))))
+                    break;
+                repeat = again[from] != 0;
+            }
+            if (repeat) {
+                item = items[from];
+                item.clean = 1;
+#pragma unroll 1
+                for (int d = lane; d < D; d += 32)
+                    nan_from[sl * D + d] = 0x7fffffff;
+            }
+            __syncwarp();
+            // ---- publish it
             if (lane == 0) {
+                if (repeat)
+                    again[from] = 0;
                 items[sl] = item;
                 mbar_arrive(&item_ready[sl]);
             }
@@ -523,11 +593,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ts.unit = __uint_as_float((uint32_t)unit << 23);
                 }
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&r_full[rs], bytes);
-                __syncwarp();
-                if (copies)
-                    tma_load_3d(sR + (size_t)rs * kTile + at, &tmv, 0, it.kvh, row, &r_full[rs]);
+                if (__builtin_expect(item.clean, 0)) {
+                    clean_codes<D>(sR + (size_t)rs * kTile, p.v_codes + (size_t)it.kvh * D, p.Hkv, row, (j0 + j) * kSKeys,
+                                   it.k_len, nan_from + sl * D, lane);
+                    if (lane == 0)
+                        mbar_arrive(&r_full[rs]);
+                } else {
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&r_full[rs], bytes);
+                    __syncwarp();
+                    if (copies)
+                        tma_load_3d(sR + (size_t)rs * kTile + at, &tmv, 0, it.kvh, row, &r_full[rs]);
+                }
                 gv++;
             }
             if (!ok)
@@ -982,6 +1059,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 tc::fence_after();
                 const float inv = l > 0.f ? o_unit / l : 0.f;
+                float any = 0.f;  // NaN if an element of the row is
+                const auto pair = [](const uint32_t *o) {
+                    return make_float2(__uint_as_float(o[0]), __uint_as_float(o[1]));
+                };
                 const size_t row = (size_t)it.cq0 + tok;
                 const size_t lse_at = ((size_t)it.kvh * p.Tq + row) * G + g;
                 if (piece) {
@@ -997,8 +1078,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::ld32(tO + 32 * cc, ro);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            ro[i] = __float_as_uint(__uint_as_float(ro[i]) * inv);
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y = fmul2(pair(ro + i), make_float2(inv, inv));
+                            any = max3_nan(any, y.x, y.y);
+                            ro[i] = __float_as_uint(y.x);
+                            ro[i + 1] = __float_as_uint(y.y);
+                        }
 #pragma unroll
                         for (int i = 0; i < 32 && valid; i += 8)
                             store32(dst + 32 * cc + i, ro + i, aligned32);
@@ -1015,13 +1100,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::ld32(tO + 32 * cc, ro);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            v[i] = pack_bf16x2(__uint_as_float(ro[2 * i]) * inv, __uint_as_float(ro[2 * i + 1]) * inv);
+                        for (int i = 0; i < 16; i++) {
+                            const float2 y = fmul2(pair(ro + 2 * i), make_float2(inv, inv));
+                            any = max3_nan(any, y.x, y.y);
+                            v[i] = pack_bf16x2(y.x, y.y);
+                        }
                         if (valid) {
                             store32(dst + 32 * cc, v, aligned32);
                             store32(dst + 32 * cc + 16, v + 8, aligned32);
                         }
                     }
+                }
+                // A NaN that is not the scores': one in V, which a weight of 0 (a row that does
+                // not see its token) makes one too.  The item once more, from codes without
+                // them, and then NaN where a row sees one.
+                if (any != any && l == l && valid && !item.clean)
+                    again[n & 1] = 1;
+                if (__builtin_expect(item.clean, 0) && valid) {
+                    const size_t at = (row * p.Hq + it.kvh * G + g) * D;
+                    if (piece)
+                        write_nans<D>(p.part_out + (size_t)item.split * p.Tq * p.Hq * D + at, NAN,
+                                      nan_from + (n & 1) * D, pos);
+                    else
+                        write_nans<D>(p.out + at, (uint16_t)0x7fff, nan_from + (n & 1) * D, pos);
                 }
                 tc::fence_before();
                 __syncwarp();

@@ -76,7 +76,9 @@ constexpr int kWBars = 4 + 2 * kWKStages + 3 * kWVStages + 10 + 4 + 1;
 // An item's share of the key tiles: tiles j0 .. j0 + nkt[t] - 1 of query tile t.
 struct WideItem {
     PrefillItem f;
-    int j0, split, pad0, pad1;
+    int j0, split;
+    int clean;  // V's codes come without NaN (the kernel over scaled E4M3 caches)
+    int pad;
 };
 
 struct WideSmem {

@@ -445,6 +445,14 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return y;
 }
 
+// The same, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Two bf16 packed in a 32-bit word -> two fp32 (exact widening).
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w)
 {

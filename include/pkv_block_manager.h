@@ -104,10 +104,14 @@ pkv_status pkv_bm_evict(pkv_block_manager *bm, int64_t seq_id, int64_t budget);
  * that is partly filled would be written by both, so the child gets a free block in
  * its place: pair[0], pair[1] receive the two ids, source and destination, for
  * pkv_copy_blocks, or -1, -1 where the last block is full.  Enqueue the copy behind
- * the stores of the parent's tokens and before either sequence's next store, on the
- * same stream.  Pairs of several forks may go into one copy, but not those of a child
- * and of a fork of that child (its block would be written and read at once): copy
- * the first before the second is enqueued.  Fails with PKV_ERR_INVALID_ARG
+ * the stores of the parent's tokens, and ahead of either sequence's next store, of an
+ * eviction of the parent and of any write into a block handed out after the fork, on
+ * the same stream: only the parent holds the source, so once it is deallocated another
+ * sequence may be given that block.  (In a step that does all its allocation first:
+ * the copies before its stores.)  Pairs of several forks may go into one copy, but not
+ * those of a child and of a fork of that child, nor of forks between which a sequence
+ * was deallocated (a block would be written and read at once): those into copies of
+ * their own, in order.  Fails with PKV_ERR_INVALID_ARG
  * (unknown parent, existing child) or PKV_ERR_WORKSPACE (no free block, no host
  * memory), changing nothing.
  */

@@ -143,9 +143,12 @@ class BlockManager:
 
         Returns int32 ``[n, 2]``, the (source, destination) of the last block where it is
         partly filled (n is 0 or 1): give it to ``copy_blocks`` with every tensor under the
-        block ids, behind the stores of the parent's tokens and before either sequence's
-        next store.  Pairs of several forks may go into one call, but not those of a child
-        and of a fork of that child.
+        block ids, behind the stores of the parent's tokens, and ahead of either sequence's
+        next store, of an eviction of the parent and of any write into a block handed out
+        after the fork (once the parent is deallocated, the source may be one).  Pairs of
+        several forks may go into one call, but not those of a child and of a fork of that
+        child, nor of forks between which a sequence was deallocated: those into calls of
+        their own, in order.
         """
         pair = np.empty((1, 2), dtype=np.int32)
         _check(self._lib, self._lib.pkv_bm_fork(self._h, int(parent_id), int(child_id), _ptr(pair)))

@@ -197,12 +197,6 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// ---- named barrier for a subset of warps ---------------------------------
-__device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // ---- warp-level matrix multiply-accumulate (bf16 in, fp32 accumulate) -----
 // Four 8x8 b16 matrices; lane l supplies the address of row (l % 8) of
 // matrix (l / 8) and receives one 32-bit fragment of each matrix.
@@ -374,14 +368,6 @@ __device__ __forceinline__ uint32_t f16x2_absmax(uint32_t a, uint32_t b)
 {
     uint32_t r;
     asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// The larger of each half, of bf16 magnitudes (a NaN loses).
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 

@@ -803,11 +803,11 @@ pkv_status pkv_paged_attn_decode_weights_fp8(const void *q, const void *k_cache,
 
 // Splits over the keys of a recording prefill's items (query tile pairs of one
 // sequence and KV head), from the sizes alone.
-static pkv::WideSplit prefill_split(int B, int max_seqlen_q, int Hq, int Hkv, int MBS, int bs)
+static pkv::WideSplit prefill_split(int B, int max_seqlen_q, int Hq, int Hkv, int MBS, int bs, bool scaled)
 {
     const long long pairs = ((long long)max_seqlen_q * (Hq / Hkv) + 2 * pkv::kPrefillRows - 1) /
                             (2 * pkv::kPrefillRows);
-    return pkv::wide_split(pairs * Hkv * B, (long long)MBS * bs, max_seqlen_q, B);
+    return pkv::wide_split(pairs * Hkv * B, (long long)MBS * bs, max_seqlen_q, B, scaled);
 }
 
 // record: also leave every row's log-sum-exp in the workspace and add the
@@ -882,7 +882,7 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
         return ps;
     const bool wide = record;  // the calls that record take the 128-key kernel
     const pkv::WideSplit split =
-        record || scaled ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs) : pkv::WideSplit{0, 1, 0};
+        record || scaled ? prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs, scaled) : pkv::WideSplit{0, 1, 0};
     const int splits = split.splits;
     const void *kfn = scaled ? pkv::prefill_scaled_kernel(D, G, splits > 1)
                              : pkv::prefill_kernel(D, G, wide, splits > 1);
@@ -1038,7 +1038,7 @@ size_t pkv_prefill_weights_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, 
     size_t n = pkv::align_up(rows * sizeof(float) + sizeof(int32_t), 256);
     if (pkv::pw_may_split(B, Tq, max_seqlen_q, Hq / Hkv, Hkv))
         n += pkv::align_up(pkv::kPwCountBytes, 256) + pkv::kPwPartBytes;
-    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs).splits;
+    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs, false).splits;
     if (splits > 1)
         n += pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float);
     return n;
@@ -1268,7 +1268,7 @@ size_t pkv_prefill_scaled_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, i
     if (B < 1 || Tq < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || MBS < 1 || bs < 1)
         return 0;
     const size_t rows = (size_t)Tq * Hq;
-    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs).splits;
+    const int splits = prefill_split(B, max_seqlen_q, Hq, Hkv, MBS, bs, true).splits;
     return splits > 1 ? pkv::align_up(splits * rows * sizeof(float), 256) + splits * rows * D * sizeof(float)
                       : 0;
 }

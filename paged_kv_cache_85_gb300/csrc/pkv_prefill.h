@@ -89,7 +89,8 @@ __host__ __device__ inline int wide_chunk(int nkt, int splits, int least)
 // How a call's items are split, from its sizes: items from `whole` on, where they
 // have `least` key tiles, into up to `splits` pieces.
 //  * Where there are fewer items than SMs, all of them, into enough pieces for two
-//    per SM, none shorter than kMinSplitTiles tiles of the longest context.
+//    per SM, none shorter than kMinSplitTiles tiles of the longest context.  Over scaled
+//    E4M3 caches (few_split) into the number that costs least, or not at all.
 //  * Where there are a few rounds of long items, those of the last, incomplete
 //    round: 256 items (2048 new tokens of 32 heads on a context of 28672) are two
 //    rounds of 152 SMs, in the second of which 48 have nothing to do.  Worth it
@@ -109,11 +110,35 @@ struct WideSplit {
 // results are the same.
 constexpr long long kWideSms = 152;
 constexpr int kJoinMaxSeqs = 152;  // sequences that the join kernel can look through
-inline WideSplit wide_split(long long items, long long max_ctx, int max_q, int B)
+// Fewer items than SMs, scaled caches: pieces follow each other on an SM, each with its
+// ends (9000 cycles) beside its share of the item's key tiles (3000 each), and their outputs'
+// way and the join cost what they do above.  32 / 8 heads, us whole and in s pieces (the
+// choice marked): 1000 tokens (128 items) on 1000 43* / 80 (3), on 16000 238* / 258 (2); 700
+// (88) on 4000 78* / 82 (3), on 20000 285 / 215* (3) / 246 (4); 512 (64) on 1024 35* / 41 (2),
+// on 2048 49* / 47 (2) / 59 (3), on 8192 129 / 86* (2) / 111 (3) / 96 (4); 300 (40) on 8192 127
+// / 63* (3) / 72 (8); 64 (8) on 4096 70 / 33* (8), on 30000 401 / 57* (19) / 74 (38).
+inline WideSplit few_split(long long items, long long tiles)
+{
+    const long long most = (2 * kWideSms + items - 1) / items, item = tiles * 3000;
+    WideSplit best = {0, 1, 0};
+    long long cheapest = item - item / 20;  // a twentieth at least
+    for (long long s = 2; s <= most && s <= tiles / kMinSplitTiles; s++) {
+        const long long pieces = (items * s + kWideSms - 1) / kWideSms;
+        const long long ends = (pieces - 1) * 9000 + items * s * 75 + 20000;
+        if (pieces * item / s + ends < cheapest) {  // (so pieces < s)
+            cheapest = pieces * item / s + ends;
+            best = {0, (int)s, (int)(s * ends / ((s - pieces) * 3000)) + 1};
+        }
+    }
+    return best;
+}
+inline WideSplit wide_split(long long items, long long max_ctx, int max_q, int B, bool scaled)
 {
     const long long tiles = (max_ctx + 127) / 128;
     if (items < 1 || B > kJoinMaxSeqs)
         return {0, 1, 0};
+    if (scaled && items < kWideSms)
+        return few_split(items, tiles);
     if (items < kWideSms) {
         long long s = (2 * kWideSms + items - 1) / items;
         if (s > tiles / kMinSplitTiles)

@@ -331,16 +331,25 @@ __global__ void __launch_bounds__(kSsThreads) store_scaled_kernel(const StoreSca
 
 template <int D> static cudaError_t launch(const StoreScaledParams &p, cudaStream_t stream)
 {
-    // Few tokens (decode steps, short chunks): small windows, so that more CTAs share
-    // them.  More: windows of 128, whose look at the slots costs less per token.  8 KV
-    // heads, us in small and large windows: 256 sequences' step 2.6 / 3.7, 512 sequences'
-    // 3.4 / 4.0, a chunk of 512 in blocks of 16 3.6 / 4.7; two chunks of 256 in blocks of
-    // 256 6.5 / 5.2, four 7.2 / 6.4, 2000 sequences' step 7.8 / 5.9, a chunk of 4096 14.8 / 9.6.
+    // Few rows of a head (decode steps, short chunks): small windows, so that more CTAs
+    // share them.  More: windows of 128, whose look at the slots costs less per token.  What
+    // decides is the number of CTAs, N * Hkv.  us in windows of 16 and of 128, one token in
+    // each of N blocks, prompts of 200 tokens and of whole blocks in blocks of 16:
+    //   N * Hkv = 2048   2.7-3.5 / 3.8   2.8-3.7 / 4.6   2.7-3.9 / 3.9
+    //             4096   3.9 / 4.0       4.1 / 4.8       4.7-5.0 / 4.1
+    //             8192   5.8 / 5.2       5.7 / 6.1       5.9 / 5.1
+    //            16384   8.8 / 6.3       9.0 / 7.5       9.2 / 6.4
+    // with 1, 2, 4 and 8 heads alike.  Prompts in large blocks have a CTA take a whole block
+    // in either, and many that find nothing: 1024 tokens of 1 head in blocks of 256 6.5 / 5.2,
+    // 4096 7.5 / 5.6; 512 of 8 heads 7.1 / 5.3.  So with blocks of more than 32 tokens, small
+    // windows up to 512 tokens only, which are rather a step's (512 sequences of 1 head
+    // 2.6 / 3.7, of 8 heads 3.9 / 4.0).
     // Where those of 128 are more than a round of CTAs (608), 256, in windows of 128 and of
     // 256: a chunk of 4096 in blocks of 16 8.4 / 10.8, of 6144 11.8 / 11.8, of 8192 14.0 / 13.4,
     // 16k tokens of ragged prompts 23.6 / 21.2, 32768 in blocks of 256 41.0 / 40.2 (16384 that
-    // begin inside theirs 20.9 / 21.2).
-    const bool few = p.N <= 512, many = !few && p.N * p.Hkv > 40960;
+    // begin inside theirs 20.9 / 21.2); 32768 of 1 head 7.3 / 10.2, of 2 heads 12.1 / 12.0.
+    const long long rows = p.N * p.Hkv;
+    const bool few = rows <= 4096 && (p.N <= 512 || p.bs <= 32), many = !few && rows > 40960;
     const int T = few ? 16 : many ? 256 : 128;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

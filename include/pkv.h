@@ -534,7 +534,8 @@ pkv_status pkv_paged_attn_decode_scaled(const void *q, const void *k_cache, cons
  * the weight before that rounding: a row keeps the values of the blocks that its
  * weight lies on, whatever the scales of others.  An infinite element of q makes its
  * row NaN.  A NaN code of V makes NaN its column of the rows that see its token (and
- * what shares its 256 rows of q takes twice the time), one of K those rows.
+ * the tiles of 256 rows of q that come across it take up to three times their time),
+ * one of K those rows.
  */
 size_t pkv_prefill_scaled_workspace_bytes(int B, int64_t Tq, int max_seqlen_q, int Hq, int Hkv,
                                           int D, int MBS, int bs);

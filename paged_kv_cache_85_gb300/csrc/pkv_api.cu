@@ -941,7 +941,6 @@ static pkv_status prefill_impl(const void *q, const void *k_cache, const void *v
     if (scaled) {
         p.k_scales = k_scales;
         p.v_scales = v_scales;
-        p.v_codes = static_cast<const uint8_t *>(v_cache);
         p.copy_rows = copy_rows;
         p.splits = splits;
         p.whole = split.whole;

@@ -41,7 +41,6 @@ struct PrefillParams {
     float *pw_part = nullptr;
     // E4M3 caches with a scale per block and KV head; null elsewhere
     const float *k_scales = nullptr, *v_scales = nullptr;  // [NB, Hkv]
-    const uint8_t *v_codes = nullptr;  // the V cache
     int copy_rows = 0;            // tokens per copy: 128, 64, 32 or 16, which divide bs
 };
 

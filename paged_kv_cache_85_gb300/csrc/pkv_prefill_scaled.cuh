@@ -22,9 +22,11 @@
 //    over its scores; no other tile knows of it.
 //  * A NaN in V's codes would reach every row of its item through a weight of 0 (the rows
 //    that do not see its token).  Nothing looks for one but an item's end, where an element
-//    of O is NaN and the row's sum is not: the item is then done again, its codes brought
-//    without NaN, and NaN written where a row sees one.  (Codes looked at as they are
-//    converted: 16k 253, ragged 283, long chunk 773 us; so 251, 280, 762.)
+//    of O is NaN and the row's sum is not: the item is then done again, the producer taking
+//    NaN out of its codes a tile behind the copies, and NaN written where a row sees one.
+//    (Codes looked at as they are converted: 16k 253, ragged 283, long chunk 773 us; so 251,
+//    280, 760.  With a NaN in each sequence's first block 750, 830, 1820; with clean codes
+//    loaded by the producer itself 1120, 1150, 3140.)
 //  * The producer, whose time is free, does what can be done once per tile: it loads
 //    each box's block two tiles ahead and its scales one, works out V's factors and the
 //    unit, and waits for V's f16 buffer, so that a softmax warp waits once per tile for
@@ -40,9 +42,9 @@
 // and w rounded by 2^-11 of itself or 2^-25 of the row's largest.  Elsewhere w g is, by
 // 2^-11 of itself or 2^-25 of the row's largest w g.
 //
-// Measured: 8 sequences of 2048 new tokens on up to 2048 (16 heads, 275 GFLOP) 249 us,
-// 1103 TFLOP/s, tensor pipe 50% busy; on 28672 each 1440 TFLOP/s; one chunk of 2048 on
-// 28672 (32 heads, 996 GFLOP) 747 us, 1333 TFLOP/s, 61%.  Bound by the chain of a query
+// Measured: 8 sequences of 2048 new tokens on up to 2048 (16 heads, 275 GFLOP) 251 us,
+// 1095 TFLOP/s, tensor pipe 49% busy; one chunk of 2048 on 28672 (32 heads, 996 GFLOP)
+// 760 us, 1310 TFLOP/s, 60%.  Bound by the chain of a query
 // tile (scores, maximum, exponentials, P.V, next scores: some 3000 cycles per 128 keys
 // against 2048 of MMA), and where items are short by their ends: Q's conversion 3600
 // cycles, the output 2200.
@@ -73,8 +75,8 @@ constexpr int kSScales = 4;
 static_assert(kSScales >= kSRStages + 2, "a tile's scales outlive its stage");
 // q_full[2], q_conv[2], q_empty[2], k_full, k_empty [kSKStages] each, r_full, r_empty
 // [kSRStages] each, v_conv, v_empty [kSVStages] each, per query tile s_full,
-// pv_ready[2 halves], pv_done, o_free, then item_ready[2], item_free[2], mma_done
-constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1;
+// pv_ready[2 halves], pv_done, o_free, then item_ready[2], item_free[2], mma_done, raw[2]
+constexpr int kSBars = 6 + 2 * kSKStages + 2 * kSRStages + 2 * kSVStages + 10 + 4 + 1 + 2;
 
 // What the softmax warps need of a key tile beside its codes; the producer brings it with
 // V's.  read: which of the eight boxes are read (a bit each), above them which have a scale
@@ -251,32 +253,32 @@ __device__ __noinline__ RowState odd_scales(uint32_t tS, uint32_t tO, const Tile
     return s;
 }
 
-// A tile of V's codes, brought by the producer's warp itself: 0 for NaN, whose token is noted
-// for its column.  codes: of the KV head; row: of lane i, where box i's tokens lie (-1: not read).
+// NaN in a tile of V's codes (of `keys` tokens; those of boxes that are not read are cleared as
+// they are converted): 0 in their place, their token noted for their column.
 template <int D>
-__device__ __noinline__ void clean_codes(uint8_t *to, const uint8_t *codes, int Hkv, int row, int key0, int k_len,
-                                         int *nan_from, int lane)
+__device__ __noinline__ void clean_codes(uint8_t *tile, uint32_t read, int key0, int keys, int *nan_from, int lane)
 {
     constexpr int kPieces = D / 16;
-#pragma unroll 1
+#pragma unroll 8
     for (int i = lane; i < kSKeys * kPieces; i += 32) {
-        const int r = i / kPieces, piece = i % kPieces;
-        const int first = __shfl_sync(0xffffffffu, row, r / kBox);
-        if (first < 0 || key0 + r >= k_len)
-            continue;  // (cleared as it is converted)
-        uint4 w = *reinterpret_cast<const uint4 *>(codes + (size_t)(first + r % kBox) * Hkv * D + 16 * piece);
-        uint8_t *c = reinterpret_cast<uint8_t *>(&w);
+        const int r = i / kPieces;
+        uint4 *at = reinterpret_cast<uint4 *>(tile) + i;
+        const uint4 w = *at;
+        const auto nan = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+        if (!(nan(w.x) | nan(w.y) | nan(w.z) | nan(w.w)) || r >= keys || !((read >> (r / kBox)) & 1u))
+            continue;
+        // swizzled as it was copied
+        const int piece = D == 128 ? i % kPieces ^ (r & 7) : i % kPieces ^ ((r >> 1) & 3);
+        uint32_t *words = reinterpret_cast<uint32_t *>(at);
 #pragma unroll 1
-        for (int d = 0; d < 16; d++)
-            if ((c[d] & 0x7f) == 0x7f) {
-                c[d] = 0;
-                atomicMin(nan_from + 16 * piece + d, key0 + r);
-            }
-        // swizzled as a copy would be
-        const int at = D == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3);
-        *reinterpret_cast<uint4 *>(to + r * D + 16 * at) = w;
+        for (int c = 0; c < 4; c++) {
+            uint32_t t = nan(words[c]);  // the top bit of a byte that is
+            words[c] &= ~((t >> 7) * 0xffu);
+            for (; t; t &= t - 1)
+                atomicMin(nan_from + 16 * piece + 4 * c + (__ffs(t) >> 3) - 1, key0 + r);
+        }
     }
-    fence_proxy_async_smem();  // the next copy into the stage is behind these
+    fence_proxy_async_smem();  // the next copy into the stage is behind this
     __syncwarp();
 }
 
@@ -329,6 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t *item_ready = o_free + 2;            // [2] item parameters published
     uint64_t *item_free = item_ready + 2;         // [2] ... no longer needed
     uint64_t *mma_done = item_free + 2;           // every MMA of the CTA completed
+    uint64_t *raw = mma_done + 1;                 // [2] V codes landed that are to be looked through
     uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.slot);
     const Turn turn{slot + 1};
     WideItem *items = reinterpret_cast<WideItem *>(smem + L.items);
@@ -365,6 +368,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&v_empty[s], 2);  // both MMA warps
         }
         mbar_init(mma_done, 2);
+        mbar_init(&raw[0], 1);
+        mbar_init(&raw[1], 1);
         *turn.word = 0;
         again[0] = again[1] = 0;
         fence_mbarrier_init();
@@ -388,6 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         grid_dependency_wait();  // K/V may have just been written by store_kvcache
         int gk = 0, gv = 0;       // K and V tiles issued so far (all items)
+        int gr = 0, gc = 0;       // V tiles to look through: issued, and done
         int q_loads[2] = {0, 0};  // Q tiles A and B loaded so far
         bool ok = true;
         int n = 0;                // items published
@@ -593,17 +599,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ts.unit = __uint_as_float((uint32_t)unit << 23);
                 }
                 __syncwarp();
+                uint64_t *landed = item.clean ? &raw[gr & 1] : &r_full[rs];
+                if (lane == 0)
+                    mbar_arrive_expect_tx(landed, bytes);
+                __syncwarp();
+                if (copies)
+                    tma_load_3d(sR + (size_t)rs * kTile + at, &tmv, 0, it.kvh, row, landed);
                 if (__builtin_expect(item.clean, 0)) {
-                    clean_codes<D>(sR + (size_t)rs * kTile, p.v_codes + (size_t)it.kvh * D, p.Hkv, row, (j0 + j) * kSKeys,
-                                   it.k_len, nan_from + sl * D, lane);
-                    if (lane == 0)
-                        mbar_arrive(&r_full[rs]);
-                } else {
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&r_full[rs], bytes);
-                    __syncwarp();
-                    if (copies)
-                        tma_load_3d(sR + (size_t)rs * kTile + at, &tmv, 0, it.kvh, row, &r_full[rs]);
+                    // the tile before while this one is on its way; the last one at once
+                    gr++;
+                    for (; gc < gr - (j + 1 < nkt); gc++) {
+                        const int back = gr - 1 - gc, g = gv - back;
+                        if (!(ok = __all_sync(FULL, mbar_wait_asleep(&raw[gc & 1], (gc >> 1) & 1))))
+                            break;
+                        const int first = (j0 + j - back) * kSKeys;
+                        clean_codes<D>(sR + (size_t)(g % kSRStages) * kTile, scales[g % kSScales].read, first,
+                                       it.k_len - first, nan_from + sl * D, lane);
+                        if (lane == 0)
+                            mbar_arrive(&r_full[g % kSRStages]);
+                    }
+                    if (!ok)
+                        break;
                 }
                 gv++;
             }
@@ -619,6 +635,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_wait_asleep(&q_full[t], (q_loads[t] - 1) & 1);
             for (int g = max(0, gk - kSKStages); g < gk; g++)
                 mbar_wait_asleep(&k_full[g % kSKStages], (g / kSKStages) & 1);
+            for (; gc < gr; gc++)
+                mbar_wait_asleep(&raw[gc & 1], (gc >> 1) & 1);
             for (int g = max(0, gv - kSRStages); g < gv; g++)
                 mbar_wait_asleep(&r_full[g % kSRStages], (g / kSRStages) & 1);
         }

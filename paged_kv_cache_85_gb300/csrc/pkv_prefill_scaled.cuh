@@ -19,7 +19,8 @@
 //    w = (w g) / g.  So a row whose weight lies on a block of small scale keeps it, whatever
 //    the other blocks hold.  Rows that see no larger block of such a tile (it is in their
 //    future) hold O in a unit of their own.  A tile with such a block costs two more loops
-//    over its scores; no other tile knows of it.
+//    over its scores (all of them, ragged prompts in blocks of 16: 280 -> 631 us); no other
+//    tile knows of it.
 //  * A NaN in V's codes would reach every row of its item through a weight of 0 (the rows
 //    that do not see its token).  Nothing looks for one but an item's end, where an element
 //    of O is NaN and the row's sum is not: the item is then done again, the producer taking
@@ -44,10 +45,9 @@
 //
 // Measured: 8 sequences of 2048 new tokens on up to 2048 (16 heads, 275 GFLOP) 251 us,
 // 1095 TFLOP/s, tensor pipe 49% busy; one chunk of 2048 on 28672 (32 heads, 996 GFLOP)
-// 760 us, 1310 TFLOP/s, 60%.  Bound by the chain of a query
-// tile (scores, maximum, exponentials, P.V, next scores: some 3000 cycles per 128 keys
-// against 2048 of MMA), and where items are short by their ends: Q's conversion 3600
-// cycles, the output 2200.
+// 760 us, 1310 TFLOP/s, 60%.  Bound by the chain of a query tile (scores, maximum,
+// exponentials, P.V, next scores: some 3000 cycles per 128 keys against 2048 of MMA), and
+// where items are short by their ends: Q's conversion 3600 cycles, the output 2200.
 // Not kept: sixteen softmax warps, with half of a row each (bookkeeping per warp: 962 us
 // for the chunk, 850 at the time); four warps for the conversions (1100, 996 at the
 // time); the lock passed on before the wait for P.V (774), or left out (816); 96 of a

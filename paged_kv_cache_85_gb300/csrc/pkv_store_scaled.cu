@@ -18,8 +18,9 @@
 // again, from L2), takes each run's maximum in shared memory, and writes.  So the
 // scale needs no second kernel and no workspace.
 //
-// Measured (8 KV heads, D = 128): 16384 tokens 21.3 us, in blocks of 256 or of 16, 0.71 of the
-// rate of a plain copy for their 101 MB; a step of 256 sequences 2.6 us behind another one.
+// Measured (8 KV heads, D = 128): 16384 tokens, 101 MB, in blocks of 256 or of 16 21 to 25 us
+// over and over, 0.59 to 0.71 of the rate of a plain copy (L2 holds part of them), 27 us, 0.55,
+// with caches flushed; a step of 256 sequences 2.6 us behind another one.
 // Bound by a CTA's chain (slots, rows, maximum, scale, rows again) at four CTAs an SM,
 // whose issue slots are 60% used.  Not kept: 16-byte loads, twice the lanes per row
 // (28 us), twice the rows in registers and half the CTAs (28), windows of 64 tokens (26),

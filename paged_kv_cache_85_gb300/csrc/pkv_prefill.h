@@ -98,6 +98,9 @@ __host__ __device__ inline int wide_chunk(int nkt, int splits, int least)
 //    piece, at 3500 bytes a cycle) and the join cost; a key tile is 3200 cycles.
 //    Whole call: those 256 items 820 -> 792 us; 168 items (1300 new tokens on 28672)
 //    798 -> 545; 192 (three of 512 on 8192) 269 -> 215; 512 (4096 on 16384) 1002 -> 935.
+//    The kernel over scaled caches (its tile is 3000 cycles, which moves no choice but by a
+//    tile) 797 -> 719, 768 -> 490, 242 -> 182, 983 -> 860; left whole, 256 items on 12288 369
+//    (358 in four pieces), on 8192 262 (268), 168 on 1024 53 (57).
 // The host knows the tables' width and the longest chunk, not the contexts, which may be
 // far shorter: `least` leaves items whole that the sum above does not split (four chunks
 // of 1024 tokens of 16 heads on nothing, tables of 40960: 97 us with every item of the
